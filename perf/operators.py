@@ -376,7 +376,11 @@ def _own(s):
                                    eps=EPS, neighbours=s["neighbours"])
         k, v = api.kv_load(cache, s["slots"], dtype=q.dtype)
         return {"q": q, "k": k, "v": v}
-    out, lse = api.attention_kv4(s["q"], cache, s["table"], s["kv"], cu_q=s["cu_q"], scale=s["scale"], return_lse=True)
+    if "workspace" not in s:            # kept by a program for all its layers and steps
+        s["workspace"] = api.alloc_attention_workspace(s["kv"].numel(), s["q"].shape[0], s["q"].shape[1], s["kv_heads"],
+                                                       s["q"].shape[2])
+    out, lse = api.attention_kv4(s["q"], cache, s["table"], s["kv"], cu_q=s["cu_q"], scale=s["scale"], return_lse=True,
+                                 workspace=s["workspace"])
     return {"out": out, "lse": lse}
 
 # ------------------------------------------------------------------ the definition in 64 bits
