@@ -369,6 +369,145 @@ int sbm_moe_fused_decode_matvec_noalloc(const uint16_t* codes, const uint32_t* r
                                         const uint16_t* x, const int32_t* expert_ids, int32_t n_tokens,
                                         void* y, uint32_t flags, uint32_t* error_word, void* stream);
 
+/* ------------------------------------------------- the attention's side */
+/* What a decoder needs next to its compressed experts: a paged cache of keys
+ * and values held in 4 bits, the plan of a serving step over it, the norms and
+ * the rotation that come before it, and the attention that reads it.
+ *
+ * The cache is uint8 [n_blocks x n_kv_heads x block_size * head_dim * 17 / 16],
+ * 16-byte aligned; block_size is a power of two from 16 to 4096, head_dim 64,
+ * 128 or 256.  Token position p of a request lives in row p % block_size of
+ * block block_table[request][p / block_size]; its slot is block * block_size +
+ * row.  One head of one block holds, for each of its block_size rows,
+ *   K codes [block_size][head_dim / 2],  V codes (the same),
+ *   K scales [block_size][head_dim / 32],  V scales (the same).
+ * A code is an E2M1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign),
+ * the even dimension in a byte's low half; a scale byte s stands for
+ * 2^(s - 127) over 32 dimensions, 255 for NaN (the OCP microscaling types, which
+ * gfx950 converts in one instruction for two codes).  Written values: s is the
+ * smallest at which no magnitude of the 32 passes 7 * 2^(s - 127), between 1
+ * and 252 (140 where the values come as fp16, so that the cache holds nothing
+ * that fp16 does not), codes are the nearest, halves to the even code, and 6
+ * is the most; 32 values with an infinity or a NaN among them become s = 255
+ * with zero codes, which reads as NaN.
+ *
+ * Device-resident lengths, tables, slots and positions are not trusted: every
+ * index made from them is bounded, and `error` (device uint32 that the caller
+ * zeroes, may be NULL) collects what was wrong. */
+#define SBM_F_NEIGHBOURS 256u  /* sbm_qk_norm_rope: the rotation turns dimensions (2i, 2i + 1); without it
+                                  (i, i + rot_dim / 2) */
+
+/* Bits of the error word of sbm_kv_plan. */
+#define SBM_PLAN_EPOOL   1u  /* fewer free blocks than the step needs */
+#define SBM_PLAN_EWIDTH  2u  /* a request needs more than table_width blocks */
+#define SBM_PLAN_ELENGTH 4u  /* a negative length, or a context above 2^30 tokens */
+#define SBM_PLAN_ETOKENS 8u  /* more than max_tokens new tokens */
+#define SBM_PLAN_EBLOCK 16u  /* a block outside [0, n_blocks): its tokens get slot -1 */
+
+/* Bytes of a cache: n_blocks * n_kv_heads * block_size * head_dim * 17 / 16; 0
+ * for a shape that the cache does not have. */
+size_t sbm_kv_cache_bytes(int32_t n_blocks, int32_t n_kv_heads, int32_t block_size, int32_t head_dim);
+
+/* One serving step's block tables and slot maps from the requests' lengths, in
+ * one launch and with nothing on the host.  Request i holds context_lens[i]
+ * tokens, in blocks block_table[i][0 .. ceil(context / block_size)), and gets
+ * new_lens[i] more.  Blocks it lacks are taken from the end of the free list, in
+ * request order: new block f of the step (counted over all requests) is
+ * free_blocks[n_free - 1 - f], written to the table's next column.
+ *   context_lens, new_lens: device int32 [n_requests], n_requests <= 4096
+ *   free_blocks: device int32 [free_capacity];  n_free: device int32 [1]
+ *   block_table: device int32 [n_requests x table_width], in and out; columns
+ *            that the step does not fill keep what they hold
+ *   slots, positions, requests: device int32 [max_tokens], out; the new tokens
+ *            in request order, then (-1, 0, -1).  No output overlaps an input
+ *   cu_q:    device int32 [n_requests + 1], out: each request's first new token
+ *   kv_lens: device int32 [n_requests], out: context + new
+ *   n_free_out: device int32 [1], out (not n_free itself: a call may be repeated)
+ * A step that cannot be had whole (the first four bits of `error`) changes
+ * nothing: cu_q is all zero, every slot -1, kv_lens the contexts (0 for a
+ * negative one), n_free_out = n_free. */
+int sbm_kv_plan(const int32_t* context_lens, const int32_t* new_lens, int32_t n_requests,
+                const int32_t* free_blocks, int32_t free_capacity, const int32_t* n_free,
+                int32_t* block_table, int32_t table_width, int32_t n_blocks, int32_t block_size,
+                int32_t max_tokens, int32_t* slots, int32_t* positions, int32_t* requests, int32_t* cu_q,
+                int32_t* kv_lens, int32_t* n_free_out, uint32_t* error, void* stream);
+
+/* Rows of heads: element (token, head, d) at data[token * token_stride + head *
+ * head_stride + d], strides in elements (any slice of a joint projection). */
+typedef struct {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} sbm_heads;
+
+/* Norms of queries and keys for each head and the position rotation, in one
+ * pass:  y = x / sqrt(mean(x^2) + eps) * weight,  then for each pair (a, b) of
+ * the first rot_dim dimensions, with row positions[t] of `rope` giving (cos, sin)
+ *   (a, b) <- (a cos - b sin, b cos + a sin),
+ * rounded once.  Queries are computed in 32 bits; keys in 64, so that a cached
+ * code does not depend on the order of a sum (a key beside the border of two
+ * codes would otherwise be cached one way by a prompt and another way by a
+ * single token).
+ *   q, k, v:   fp16 (bf16 with SBM_F_IN_BF16): [n_tokens x n_heads], [n_tokens x
+ *              n_kv_heads] twice; v only with a cache, else NULL
+ *   q_weight, k_weight: [head_dim] of the same type, or NULL for ones
+ *   rope:      device fp32 [rope_rows x rot_dim]: rot_dim / 2 cosines, then the
+ *              sines; rot_dim a multiple of 16 up to head_dim, or 0: no rotation
+ *   positions: device int32 [n_tokens] (NULL with rot_dim 0).  A token whose
+ *              position has no row is left out (nothing is written for it) and
+ *              counted in `error`
+ *   q_out, k_out: where the results go; k_out may be NULL with a cache.  They may
+ *              be q and k themselves
+ *   cache, slots: keys (as rounded for k_out) and values are written to the
+ *              cache at slots[t]; a negative slot writes nothing, one past the
+ *              cache is left out and counted in `error`.  NULL: no cache
+ * Slots of one call are distinct.  head_dim 64, 128 or 256. */
+int sbm_qk_norm_rope(const sbm_heads* q, const sbm_heads* k, const sbm_heads* v, const uint16_t* q_weight,
+                     const uint16_t* k_weight, const int32_t* positions, const float* rope, int32_t rope_rows,
+                     int32_t rot_dim, double eps, int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads,
+                     int32_t head_dim, const sbm_heads* q_out, const sbm_heads* k_out, const int32_t* slots,
+                     uint8_t* cache, int32_t n_blocks, int32_t block_size, uint32_t flags, uint32_t* error,
+                     void* stream);
+
+/* Cached tokens as values: k, v device fp16 (bf16 with SBM_F_IN_BF16) [n_tokens
+ * x n_kv_heads x head_dim], 16-byte aligned, either may be NULL.  A negative
+ * slot gives zeros; one past the cache gives zeros and is counted in `error`. */
+int sbm_kv_load(const uint8_t* cache, int32_t n_blocks, int32_t n_kv_heads, int32_t block_size, int32_t head_dim,
+                const int32_t* slots, int32_t n_tokens, uint16_t* k, uint16_t* v, uint32_t flags, uint32_t* error,
+                void* stream);
+
+/* Workspace bytes of sbm_attention_kv4. */
+size_t sbm_attention_kv4_workspace_bytes(int32_t n_requests, int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads,
+                                         int32_t head_dim);
+
+/* Attention of each request's last tokens over its cached ones, the new tokens
+ * among them (they are written before).  Request r has tokens cu_q[r] ..
+ * cu_q[r + 1] of q (cu_q NULL: one token each, n_tokens = n_requests); token i of
+ * its n sees positions 0 .. kv_lens[r] - n + i.  With s = scale * q . k in fp32,
+ *   out = sum softmax(s) v,   lse = ln sum exp s   (lse may be NULL).
+ * A row that sees nothing (kv_lens 0, or more tokens than the cache holds) and a
+ * token that no request has get out = 0 and lse = -inf.  Query head h reads
+ * key head h / (n_heads / n_kv_heads).
+ *   q, out:   fp16 (bf16 with SBM_F_IN_BF16); q's data 16-byte aligned with
+ *             strides that are multiples of 8 elements; out: [n_tokens x n_heads x
+ *             head_dim], 16-byte aligned;  lse: fp32 [n_tokens x n_heads]
+ *   block_table: device int32 [n_requests x table_width]; a block outside
+ *             [0, n_blocks) hides its tokens and sets bit 0 of `error`; a length
+ *             above table_width * block_size is cut to it and sets bit 1; cu_q
+ *             that falls, or passes n_tokens, sets bit 2 (that request's rows
+ *             may be left unwritten)
+ *   workspace: device, 16-byte aligned, of sbm_attention_kv4_workspace_bytes(...)
+ *             or more, ZEROED by the caller before its first use; every call
+ *             leaves it ready for the next (calls that share one must not
+ *             overlap).  n_requests <= 4096
+ * fp16: cached values are read as fp16 (magnitudes above 65504 become
+ * infinite; a cache written from fp16 holds none). */
+int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks, int32_t block_size,
+                      const int32_t* block_table, int32_t table_width, const int32_t* kv_lens, const int32_t* cu_q,
+                      int32_t n_requests, int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                      float scale, uint16_t* out, float* lse, uint32_t flags, void* workspace,
+                      size_t workspace_bytes, uint32_t* error, void* stream);
+
 /* ------------------------------------------- synthetic stack generation */
 /* The QMoE page's c2048 stack (1.6T parameters, under 160 GB at ~0.8 bit per
  * parameter, ~88.6% zeros; Executive Summary and "Natural sparsity") cannot be

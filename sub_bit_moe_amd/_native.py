@@ -19,6 +19,12 @@ SBM_F_MINMAX = 16
 SBM_F_IMAGE4 = 32
 SBM_F_DETERMINISTIC = 64
 SBM_F_IN_BF16 = 128
+SBM_F_NEIGHBOURS = 256
+SBM_PLAN_EPOOL = 1
+SBM_PLAN_EWIDTH = 2
+SBM_PLAN_ELENGTH = 4
+SBM_PLAN_ETOKENS = 8
+SBM_PLAN_EBLOCK = 16
 
 STATUS = {0: "SBM_OK", -1: "SBM_EINVAL", -2: "SBM_EODD_WIDTH", -3: "SBM_ECORRUPT",
           -4: "SBM_EDICT", -5: "SBM_ERANGE", -6: "SBM_ENOSPACE", -7: "SBM_EHIP"}
@@ -41,7 +47,12 @@ class Projection(C.Structure):
                 ("experts", C.c_void_p), ("n_experts", C.c_int32), ("rows", C.c_int32), ("cols", C.c_int32)]
 
 
+class Heads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
 P = C.c_void_p
+I = C.c_int32
 _SIGS = {
     "sbm_last_error": (C.c_char_p, []),
     "sbm_version": (C.c_char_p, []),
@@ -71,6 +82,14 @@ _SIGS = {
     "sbm_stream_read": (C.c_int, [P, C.c_uint64, P, C.c_uint32, P]),
     "sbm_workspace_error": (C.c_int, [P, P, P]),
     "sbm_rms_glue": (C.c_int, [P, C.c_int32, C.c_int32, P, P]),
+    "sbm_kv_cache_bytes": (C.c_size_t, [I, I, I, I]),
+    "sbm_kv_plan": (C.c_int, [P, P, I, P, I, P, P, I, I, I, I, P, P, P, P, P, P, P, P]),
+    "sbm_qk_norm_rope": (C.c_int, [P, P, P, P, P, P, P, I, I, C.c_double, I, I, I, I, P, P, P, P, I, I, C.c_uint32,
+                                   P, P]),
+    "sbm_kv_load": (C.c_int, [P, I, I, I, I, P, I, P, P, C.c_uint32, P, P]),
+    "sbm_attention_kv4_workspace_bytes": (C.c_size_t, [I, I, I, I, I]),
+    "sbm_attention_kv4": (C.c_int, [P, P, I, I, P, I, P, P, I, I, I, I, I, C.c_float, P, P, C.c_uint32, P, C.c_size_t,
+                                    P, P]),
     "sbm_trie_words": (C.c_size_t, []),
     "sbm_build_trie": (C.c_int, [P, P]),
     "sbm_gen_count": (C.c_int, [C.c_uint64, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,

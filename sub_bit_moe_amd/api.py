@@ -384,6 +384,273 @@ def workspace_error(workspace, stream=None) -> int:
     check(lib().sbm_workspace_error(_ptr(workspace), C.addressof(v), _stream(stream)))
     return int(v.value)
 
+# ------------------------------------------------------------------ attention side
+
+@dataclass
+class KVCache:
+    """Paged keys and values of one layer in 4 bits (the layout at "the
+    attention's side" of include/sbm.h): data uint8 [n_blocks, n_kv_heads,
+    block_size * head_dim * 17 / 16]."""
+    data: object
+    block_size: int
+    head_dim: int
+
+    @property
+    def n_blocks(self) -> int:
+        return int(self.data.shape[0])
+
+    @property
+    def n_kv_heads(self) -> int:
+        return int(self.data.shape[1])
+
+
+def alloc_kv_cache(n_blocks: int, n_kv_heads: int, head_dim: int, block_size: int = 16, device="cuda") -> KVCache:
+    import torch
+    if not int(lib().sbm_kv_cache_bytes(n_blocks, n_kv_heads, block_size, head_dim)):
+        raise ValueError(f"no such cache: {n_blocks} blocks, {n_kv_heads} heads of {head_dim}, {block_size} tokens a block")
+    return KVCache(torch.zeros(n_blocks, n_kv_heads, block_size * head_dim * 17 // 16, dtype=torch.uint8, device=device),
+                   block_size, head_dim)
+
+
+def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """fp32 [n_positions, rot_dim]: cosines, then sines, of position *
+    base^(-2i / rot_dim), from angles in 64 bits."""
+    import torch
+    inv = torch.pow(torch.tensor(base, dtype=torch.float64), -torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    angle = torch.arange(n_positions, dtype=torch.float64)[:, None] * inv
+    return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32).to(device)
+
+
+def _dev(t, what: str, dtype=None, like=None, contiguous: bool = True):
+    """A device tensor's address; TypeError / ValueError where it cannot be what the kernels take."""
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on the GPU")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{what} is on {t.device}, not {like.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _heads(t, what: str, dtype, like, shape=None):
+    """[tokens, heads, head_dim] with any strides but the last as sbm_heads."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what} must be [tokens, heads, head_dim] with neighbouring dimensions")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} is {tuple(t.shape)}, not {tuple(shape)}")
+    return N.Heads(_dev(t, what, dtype, like, False), t.stride(0), t.stride(1))
+
+
+def _error(t, like):
+    import torch
+    if t is None:
+        return 0
+    if t.numel() < 1:
+        raise ValueError("error must hold one int32")
+    return _dev(t, "error", torch.int32, like)
+
+
+@dataclass
+class KVPlan:
+    """What one serving step needs of its requests (sbm_kv_plan), all int32:
+    slots, positions, requests [max_tokens]; cu_q [n_requests + 1]; kv_lens
+    [n_requests]; n_free, error [1] (error collects: zero it to use it again);
+    block_table [n_requests, width], the caller's, updated in place."""
+    slots: object
+    positions: object
+    requests: object
+    cu_q: object
+    kv_lens: object
+    n_free: object
+    error: object
+    block_table: object
+
+
+def alloc_kv_plan(n_requests: int, max_tokens: int, block_table=None, device="cuda") -> KVPlan:
+    import torch
+    n, r = max_tokens, n_requests
+    buf = torch.zeros(3 * n + 2 * r + 3, dtype=torch.int32, device=device if block_table is None else block_table.device)
+    return KVPlan(buf[:n], buf[n:2 * n], buf[2 * n:3 * n], buf[3 * n:3 * n + r + 1], buf[3 * n + r + 1:3 * n + 2 * r + 1],
+                  buf[3 * n + 2 * r + 1:3 * n + 2 * r + 2], buf[3 * n + 2 * r + 2:], block_table)
+
+
+def kv_plan(context_lens, new_lens, free_blocks, n_free, block_table, n_blocks: int, block_size: int, max_tokens: int,
+            plan: KVPlan = None, stream=None) -> KVPlan:
+    """Block tables and slot maps of one serving step from the requests' lengths
+    (sbm_kv_plan): request i holds context_lens[i] tokens and gets new_lens[i];
+    blocks it lacks are popped from the end of free_blocks[:n_free].  Nothing is
+    read back: n_free and the error word stay on the device (plan.error:
+    SBM_PLAN_E* bits, and then nothing was given out).  plan: one from
+    alloc_kv_plan, to be filled again."""
+    import torch
+    i32 = torch.int32
+    R = context_lens.numel()
+    if new_lens.numel() != R or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("context_lens, new_lens and block_table must have one row for each request")
+    if n_free.numel() != 1:
+        raise ValueError("n_free must hold one int32")
+    if plan is None:
+        plan = alloc_kv_plan(R, max_tokens, block_table)
+    elif plan.slots.numel() < max_tokens or plan.positions.numel() < max_tokens or plan.requests.numel() < max_tokens \
+            or plan.cu_q.numel() < R + 1 or plan.kv_lens.numel() < R:
+        raise ValueError("the plan was made for fewer requests or tokens")
+    plan.block_table = block_table
+    L = context_lens
+    check(lib().sbm_kv_plan(
+        _dev(L, "context_lens", i32), _dev(new_lens, "new_lens", i32, L), R, _dev(free_blocks, "free_blocks", i32, L),
+        free_blocks.numel(), _dev(n_free, "n_free", i32, L), _dev(block_table, "block_table", i32, L),
+        block_table.shape[1], n_blocks, block_size, max_tokens, _dev(plan.slots, "slots", i32, L),
+        _dev(plan.positions, "positions", i32, L), _dev(plan.requests, "requests", i32, L), _dev(plan.cu_q, "cu_q", i32, L),
+        _dev(plan.kv_lens, "kv_lens", i32, L), _dev(plan.n_free, "plan.n_free", i32, L), _error(plan.error, L),
+        _stream(stream)))
+    return plan
+
+
+def _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours, q_out, k_out, slots, cache, error,
+                  stream):
+    import torch
+    flags = _x_flag(q) | (N.SBM_F_NEIGHBOURS if neighbours else 0)
+    hq = _heads(q, "q", None, None)
+    T, H, D = q.shape
+    hk = _heads(k, "k", q.dtype, q, (T, k.shape[1], D))
+    Hk = k.shape[1]
+    hv = None if v is None else _heads(v, "v", q.dtype, q, (T, Hk, D))
+    w = []
+    for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None and t.numel() != D:
+            raise ValueError(f"{what} must hold {D} elements")
+        w.append(0 if t is None else _dev(t, what, q.dtype, q))
+    pos = rp = rows = rot = 0
+    if rope is not None:
+        rp, rows, rot = _dev(rope, "rope", torch.float32, q), rope.shape[0], rope.shape[1]
+        if positions.numel() != T:
+            raise ValueError(f"positions must hold {T} elements")
+        pos = _dev(positions, "positions", torch.int32, q)
+    ho = _heads(q_out, "q_out", q.dtype, q, (T, H, D))
+    hko = None if k_out is None else _heads(k_out, "k_out", q.dtype, q, (T, Hk, D))
+    sl = data = nb = bs = 0
+    if cache is not None:
+        if cache.n_kv_heads != Hk or cache.head_dim != D:
+            raise ValueError(f"the cache holds {cache.n_kv_heads} heads of {cache.head_dim}, not {Hk} of {D}")
+        sl, data, nb, bs = _slots(slots, T, q), _cache(cache, q), cache.n_blocks, cache.block_size
+    check(lib().sbm_qk_norm_rope(
+        C.byref(hq), C.byref(hk), hv and C.byref(hv), w[0], w[1], pos, rp, rows, rot, eps, T, H, Hk, D, C.byref(ho),
+        hko and C.byref(hko), sl, data, nb, bs, flags, _error(error, q), _stream(stream)))
+
+
+def _slots(slots, n: int, like):
+    import torch
+    if slots.numel() != n:
+        raise ValueError(f"slots must hold {n} elements")
+    return _dev(slots, "slots", torch.int32, like)
+
+
+def _cache(cache: KVCache, like):
+    import torch
+    d = cache.data
+    if d.dim() != 3 or d.shape[2] != cache.block_size * cache.head_dim * 17 // 16:
+        raise ValueError(f"a cache of {tuple(d.shape)} bytes holds no blocks of {cache.block_size} x {cache.head_dim}")
+    return _dev(d, "cache", torch.uint8, like)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions, rope, eps: float = 1e-6, neighbours: bool = False, q_out=None,
+                 k_out=None, error=None, stream=None):
+    """Norm of each head of q [T, heads, D] and k [T, kv_heads, D] by its weight
+    [D] (None: ones) and rotation by rope[positions[t]] (rope_table; None: no
+    rotation; neighbours: pairs (2i, 2i + 1) instead of halves), in one launch
+    (sbm_qk_norm_rope).  Returns (q_out, k_out); they may be q and k."""
+    import torch
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _qk_norm_rope(q, k, None, q_weight, k_weight, positions, rope, eps, neighbours, q_out, k_out, None, None, error,
+                  stream)
+    return q_out, k_out
+
+
+def qk_norm_rope_store(q, k, v, q_weight, k_weight, positions, rope, slots, cache: KVCache, eps: float = 1e-6,
+                       neighbours: bool = False, q_out=None, k_out=None, error=None, stream=None):
+    """qk_norm_rope whose keys go, with the values v, into the 4-bit cache at
+    slots[t] (negative: nowhere) in the same launch; k_out: the keys too.
+    Returns q_out."""
+    import torch
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours, q_out, k_out, slots, cache, error,
+                  stream)
+    return q_out
+
+
+def kv_load(cache: KVCache, slots, dtype=None, k=None, v=None, error=None, stream=None):
+    """The cached tokens at slots as values (sbm_kv_load): k, v [n, kv_heads, D]
+    in float16 (or bfloat16); a negative slot gives zeros."""
+    import torch
+    dtype = dtype or (torch.float16 if k is None else k.dtype)
+    n = slots.numel()
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=slots.device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=slots.device)
+    for t in (k, v):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"k and v must be {shape}, not {tuple(t.shape)}")
+    check(lib().sbm_kv_load(_cache(cache, slots), cache.n_blocks, cache.n_kv_heads, cache.block_size, cache.head_dim,
+                            _slots(slots, n, slots), n, _dev(k, "k", dtype, slots), _dev(v, "v", dtype, slots),
+                            _x_flag(k), _error(error, slots), _stream(stream)))
+    return k, v
+
+
+def attention_workspace_bytes(n_requests: int, n_tokens: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(lib().sbm_attention_kv4_workspace_bytes(n_requests, n_tokens, n_heads, n_kv_heads, head_dim))
+
+
+def alloc_attention_workspace(n_requests: int, n_tokens: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                              device="cuda"):
+    """Zeroed workspace of the attention (it must start zeroed; every call
+    leaves it ready for the next)."""
+    import torch
+    n = attention_workspace_bytes(n_requests, n_tokens, n_heads, n_kv_heads, head_dim)
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: float = None, out=None, lse=None,
+                  return_lse: bool = False, workspace=None, error=None, stream=None):
+    """Attention of each request's last tokens over its cached ones
+    (sbm_attention_kv4): q [T, heads, D], of request r the rows cu_q[r] ..
+    cu_q[r + 1] (cu_q None: one token each), which see the request's kv_lens[r]
+    tokens up to their own.  scale: 1 / sqrt(D) by default.  Returns out [T,
+    heads, D], or (out, lse fp32 [T, heads]) with return_lse or an lse buffer."""
+    import torch
+    i32 = torch.int32
+    T, H, D = q.shape
+    R = kv_lens.numel()
+    if cache.head_dim != D or H % cache.n_kv_heads:
+        raise ValueError(f"the cache holds {cache.n_kv_heads} heads of {cache.head_dim}; q has {H} of {D}")
+    if block_table.dim() != 2 or block_table.shape[0] != R or (cu_q is not None and cu_q.numel() != R + 1):
+        raise ValueError("kv_lens, block_table and cu_q must be of the same requests")
+    hq = _heads(q, "q", None, None)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    elif tuple(out.shape) != (T, H, D):
+        raise ValueError(f"out must be {(T, H, D)}, not {tuple(out.shape)}")
+    if lse is None and return_lse:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    elif lse is not None and tuple(lse.shape) != (T, H):
+        raise ValueError(f"lse must be {(T, H)}, not {tuple(lse.shape)}")
+    if workspace is None:
+        workspace = alloc_attention_workspace(R, T, H, cache.n_kv_heads, D, q.device)
+    check(lib().sbm_attention_kv4(
+        C.byref(hq), _cache(cache, q), cache.n_blocks, cache.block_size, _dev(block_table, "block_table", i32, q),
+        block_table.shape[1], _dev(kv_lens, "kv_lens", i32, q), 0 if cu_q is None else _dev(cu_q, "cu_q", i32, q), R, T,
+        H, cache.n_kv_heads, D, D ** -0.5 if scale is None else scale, _dev(out, "out", q.dtype, q),
+        0 if lse is None else _dev(lse, "lse", torch.float32, q), _x_flag(q), _dev(workspace, "workspace", torch.uint8, q),
+        workspace.numel(), _error(error, q), _stream(stream)))
+    return out if lse is None else (out, lse)
+
 # ------------------------------------------------------------------ synthetic stacks
 
 def build_trie(words: np.ndarray) -> np.ndarray:
