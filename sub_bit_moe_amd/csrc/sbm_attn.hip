@@ -1,8 +1,8 @@
 // Attention over the 4-bit paged cache.
 //
-// A wave takes 16 rows (query heads of one key head, and their tokens) as the
-// columns of the matrix products, and walks the cached tokens 32 at a time,
-// everything in registers:
+// attn_few_kernel: the token axis shared out.  A wave takes 16 rows (query heads
+// of one key head, and their tokens) as the columns of the matrix products, and
+// walks the cached tokens 32 at a time, everything in registers:
 //   S^T [32 tokens x 16 rows] = K Q^T   two v_mfma_f32_16x16x32 per 32 dimensions
 //   P^T = exp2(S^T - m)                 the running maximum m of a row (= lane & 15)
 //   O^T [D x 16] += V^T P^T             one v_mfma_f32_16x16x32 per 16 dimensions
@@ -31,6 +31,11 @@ constexpr int kAWaves = kAThreads / 64;
 constexpr float kBias = 8.f, kSlack = 7.f;
 constexpr float kLowest = -3.0e38f;       // m before the first score
 constexpr float kLn2 = 0.693147180559945309f;
+// The few-row kernel's share of a request's tokens: kStep for a workgroup at a
+// time, 32 for each of its waves.
+constexpr int kStep = 32 * kAWaves;
+constexpr int kMinSteps = 2;              // a workgroup's least work, in steps
+constexpr int kCounters = 2048;           // of the workspace, before the partial results
 constexpr uint32_t kErrBlock = 1, kErrLength = 2, kErrCuQ = 4;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -46,7 +51,10 @@ struct AttnArgs {
   uint16_t* out;
   float* lse;
   uint32_t* error;
-  float scale2;          // scale * log2(e)
+  uint32_t* counters;    // zero between calls
+  float* parts;          // partial outputs, maxima and sums
+  float scale2;          // |scale| * log2(e)
+  uint32_t flip;         // 0x80008000 with a negative scale: the sign goes into the queries
   int32_t n_blocks, shift, width, n_requests, n_tokens, heads, kv_heads, group;
 };
 
@@ -70,32 +78,104 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 __device__ __forceinline__ float exponent(uint32_t s) { return __uint_as_float(s << 23); }
 
+// Partial results cross workgroups on other XCDs, whose L2 caches do not see each
+// other's writes: they are written through and read past the caches (agent scope).
+__device__ __forceinline__ void put2(float* p, float a, float b) {
+  const uint64_t v = (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+  __hip_atomic_store((uint64_t*)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 get2(const float* p) {
+  const uint64_t v = __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ void put1(float* p, float a) {
+  __hip_atomic_store((uint32_t*)p, __float_as_uint(a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float get1(const float* p) {
+  return __uint_as_float(__hip_atomic_load((const uint32_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+
+// One request as a call gives it, every length bounded.
+struct Request {
+  int q0, n, kv;               // first token, tokens, cached tokens
+};
+
+__device__ __forceinline__ Request request(const AttnArgs& a, int r, uint32_t* bad) {
+  Request q{r, 1, a.kv_lens[r]};
+  if (a.cu_q) {
+    q.q0 = a.cu_q[r];
+    const int q1 = a.cu_q[r + 1];
+    if (q.q0 < 0 || q1 < q.q0 || q1 > a.n_tokens) {
+      *bad |= kErrCuQ;
+      q.q0 = q.n = 0;
+    } else {
+      q.n = q1 - q.q0;
+    }
+  }
+  const int64_t most = (int64_t)a.width << a.shift;
+  if (q.kv > most) {
+    *bad |= kErrLength;
+    q.kv = (int)most;
+  }
+  q.kv = max(q.kv, 0);
+  return q;
+}
+
+// Inclusive sum over the workgroup; *total: of all of it.
+__device__ __forceinline__ uint64_t scan_add(uint64_t v, uint64_t* s_wave, uint64_t* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t u = __shfl_up(v, d, 64);
+    if (lane >= d) v += u;
+  }
+  __syncthreads();
+  if (lane == 63) s_wave[wave] = v;
+  __syncthreads();
+  uint64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kAWaves; ++w) {
+    if (w < wave) before += s_wave[w];
+    all += s_wave[w];
+  }
+  *total = all;
+  return v + before;
+}
+
+// Where 32 tokens are: their two halves' blocks (-1: none), the same in all lanes.
+struct Pages {
+  int32_t b[2];
+};
+
+__device__ __forceinline__ Pages pages(const AttnArgs& a, const int32_t* table, int t0, int end) {
+  Pages p;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) p.b[x] = t0 + 16 * x < end ? table[(t0 + 16 * x) >> a.shift] : -1;
+  return p;
+}
+
 // What a wave has read of 32 cached tokens.
 template <int D>
 struct Raw {
   uint32_t k[2][D / 32];       // a lane's D / 4 K codes of token (lane & 15), both halves
   uint32_t ks[2];              // their scale bytes (one, or two with D = 256)
   uint32_t v[2][4][D > 128 ? 2 : 1];   // D / 16 V codes of tokens 4g + i
-  uint32_t vs[2][4];           // the scale byte of each (in the low byte)
+  uint32_t vs[2][D / 32];      // the scale bytes of tokens 4g .. 4g + 3
   bool ok[2];                  // the block exists (the same in all lanes)
 };
 
-// Where the 32 tokens from t0 are (t0 a multiple of 32); `end`: the tokens that there are.
 template <int D>
-__device__ __forceinline__ void load_tokens(Raw<D>& r, const AttnArgs& a, const int32_t* table, int kh, int t0,
-                                            int end, int lane) {
+__device__ __forceinline__ void load_tokens(Raw<D>& r, const AttnArgs& a, Pages p, int kh, int t0, int lane) {
   const int m = lane & 15, g = lane >> 4;
   const int bs = 1 << a.shift;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int t = t0 + 16 * x;
-    int32_t b = t < end ? table[t >> a.shift] : 0;
-    b = __builtin_amdgcn_readfirstlane(b);
+    int32_t b = __builtin_amdgcn_readfirstlane(p.b[x]);
     r.ok[x] = (uint32_t)b < (uint32_t)a.n_blocks;
-    if (!r.ok[x]) b = 0;
-    const int row = t & (bs - 1);                  // t past the end stays inside block 0's rows
+    if (!r.ok[x]) b = 0;                           // hidden tokens: read, and not used
+    const int row = (t0 + 16 * x) & (bs - 1);
     const uint8_t* rec = a.cache + ((int64_t)b * a.kv_heads + kh) * kv_record_bytes(bs, D);
-    const uint8_t* kc = rec + (row + m) * (D / 2) + g * (D / 8);
+    const uint8_t* kc = rec + row * (D / 2) + (m * (D / 2) + g * (D / 8));
     if constexpr (D == 64) {
       const uint2 w = *(const uint2*)kc;
       r.k[x][0] = w.x, r.k[x][1] = w.y;
@@ -106,12 +186,11 @@ __device__ __forceinline__ void load_tokens(Raw<D>& r, const AttnArgs& a, const 
         r.k[x][4 * i] = w.x, r.k[x][4 * i + 1] = w.y, r.k[x][4 * i + 2] = w.z, r.k[x][4 * i + 3] = w.w;
       }
     }
-    const uint8_t* ks = rec + bs * D + (row + m) * (D / 32);
+    const uint8_t* ks = rec + bs * D + row * (D / 32) + m * (D / 32);
     if constexpr (D == 64) r.ks[x] = ks[g >> 1];
     else if constexpr (D == 128) r.ks[x] = ks[g];
     else r.ks[x] = *(const uint16_t*)(ks + 2 * g);
-    const uint8_t* vc = rec + bs * (D / 2) + (row + 4 * g) * (D / 2) + m * (D / 32);
-    const uint8_t* vs = rec + bs * D + bs * (D / 32) + (row + 4 * g) * (D / 32);
+    const uint8_t* vc = rec + bs * (D / 2) + row * (D / 2) + (4 * g * (D / 2) + m * (D / 32));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (D == 64) {
@@ -122,26 +201,55 @@ __device__ __forceinline__ void load_tokens(Raw<D>& r, const AttnArgs& a, const 
         const uint2 w = *(const uint2*)(vc + i * (D / 2));
         r.v[x][i][0] = w.x, r.v[x][i][1] = w.y;
       }
-      r.vs[x][i] = vs[i * (D / 32) + m * (D / 16) / 32];
+    }
+    const uint8_t* vs = rec + bs * D + bs * (D / 32) + row * (D / 32) + 4 * g * (D / 32);
+    if constexpr (D == 64) {
+      const uint2 w = *(const uint2*)vs;
+      r.vs[x][0] = w.x, r.vs[x][1] = w.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 128; ++i) {
+        const uint4 w = *(const uint4*)(vs + 16 * i);
+        r.vs[x][4 * i] = w.x, r.vs[x][4 * i + 1] = w.y, r.vs[x][4 * i + 2] = w.z, r.vs[x][4 * i + 3] = w.w;
+      }
     }
   }
 }
 
-// 16 kNQ rows of one key head: queries, running maxima, sums and outputs.
-template <typename T, int D, int kNQ>
+// The scale of four tokens' values in the exponents of s (sign and mantissa hold
+// other scales' bits, which v_cvt_scalef32 does not look at): byte `which` of each
+// token's D / 32.
+template <int D>
+__device__ __forceinline__ void value_scales(const uint32_t* vs, int which, uint32_t* s) {
+  if constexpr (D == 64) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = __builtin_amdgcn_alignbit(vs[i >> 1], vs[i >> 1], 8 * ((i & 1) * 2 + which) + 9);
+  } else if constexpr (D == 128) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = __builtin_amdgcn_alignbit(vs[i], vs[i], 8 * which + 9);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = which & 4 ? vs[2 * i + 1] : vs[2 * i];
+      s[i] = __builtin_amdgcn_alignbit(w, w, 8 * (which & 3) + 9);
+    }
+  }
+}
+
+// 16 rows of one key head: queries, running maxima, sums and outputs.
+template <int D>
 struct Rows {
-  static constexpr int E = D / 16;
-  u32x4 q[kNQ][D / 32];
-  f32x4 o[kNQ][E];
-  float m[kNQ], l[kNQ];
-  int last[kNQ];               // the last position that the lane's row sees, -1: none
+  u32x4 q[D / 32];
+  f32x4 o[D / 16];
+  float m, l;
+  int last;                    // the last position that the lane's row sees, -1: none
 };
 
 // NaN for the rows that see a token whose values have one, where that token
 // went into the products as if it had none (a masked step, some rows not seeing it).
-template <typename T, int D, int kNQ>
-__device__ __forceinline__ void nan_values(Rows<T, D, kNQ>& s, const AttnArgs& a, const int32_t* table, int kh, int t0,
-                                        int end, int lane) {
+template <int D>
+__device__ __forceinline__ void nan_values(Rows<D>& s, const AttnArgs& a, const int32_t* table, int kh, int t0, int end,
+                                        int lane) {
   const int bs = 1 << a.shift, g = lane >> 4;
   for (int t = t0; t < min(t0 + 32, end); ++t) {
     const int32_t b = table[t >> a.shift];
@@ -151,108 +259,88 @@ __device__ __forceinline__ void nan_values(Rows<T, D, kNQ>& s, const AttnArgs& a
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // rows 4g + i of an output tile are dimensions (4g + i) D / 16 and on
-      if (vs[(4 * g + i) * (D / 16) / 32] != kScaleNaN) continue;
+      if (vs[(4 * g + i) * (D / 16) / 32] != kScaleNaN || t > s.last) continue;
 #pragma unroll
-      for (int c = 0; c < kNQ; ++c) {
-        if (t > s.last[c]) continue;
-#pragma unroll
-        for (int e = 0; e < D / 16; ++e) s.o[c][e][i] = NAN;
-      }
+      for (int e = 0; e < D / 16; ++e) s.o[e][i] = NAN;
     }
   }
 }
 
-template <typename T, int D, int kNQ>
-__device__ __forceinline__ void step(Rows<T, D, kNQ>& s, Raw<D>& r, const AttnArgs& a, const int32_t* table,
-                                     int kh, int t0, int end, int first, int lane) {
+template <typename T, int D>
+__device__ __forceinline__ void step(Rows<D>& s, const Raw<D>& r, const AttnArgs& a, const int32_t* table, int kh, int t0,
+                                     int end, int first, int lane) {
   constexpr int E = D / 16;
-  const int g = lane >> 4;
+  const int g = lane >> 4, m = lane & 15;
   // some token of the 32 is hidden from some row (`first`: the first row's last position)
   const bool masked = t0 + 31 > first || !r.ok[0] || !r.ok[1];
   // K Q^T
-  f32x4 sc[kNQ][2];
-#pragma unroll
-  for (int c = 0; c < kNQ; ++c) sc[c][0] = sc[c][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 sc[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
+    sc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kk = 0; kk < D / 32; ++kk) {
       const float ks = exponent(D == 256 ? (r.ks[x] >> (kk / 4 * 8)) & 255u : r.ks[x]);
       const uint32_t w = r.k[x][kk];
       const u32x4 k = {cvt_fp4<T, 0>(w, ks), cvt_fp4<T, 1>(w, ks), cvt_fp4<T, 2>(w, ks), cvt_fp4<T, 3>(w, ks)};
-#pragma unroll
-      for (int c = 0; c < kNQ; ++c) sc[c][x] = mfma<T>(k, s.q[c][kk], sc[c][x]);
+      sc[x] = mfma<T>(k, s.q[kk], sc[x]);
     }
   }
+  uint32_t vs[8];
+  value_scales<D>(r.vs[0], m * (D / 16) / 32, vs);
+  value_scales<D>(r.vs[1], m * (D / 16) / 32, vs + 4);
   bool odd_v = false;            // a NaN among the values of tokens that not every row sees
+  float z[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) z[j] = sc[j >> 2][j & 3];
+  uint32_t hidden = 0;           // bit j: the row does not see it
   if (masked) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = t0 + 16 * x + 4 * g + i;
-        const bool there = r.ok[x] && t < end;
-        odd_v = odd_v || (there && r.vs[x][i] == kScaleNaN);
-        // 0 * NaN is NaN: what is not seen has to be finite
-        if (!there || r.vs[x][i] == kScaleNaN) r.vs[x][i] = 127;
+    for (int j = 0; j < 8; ++j) {
+      const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
+      const bool there = r.ok[j >> 2] && t < end, nan = (vs[j] & 0x7F800000u) == 0x7F800000u;
+      odd_v = odd_v || (there && nan);
+      if (!there || nan) vs[j] = 0x3F800000u;      // 0 * NaN is NaN: what is not seen has to be finite
+      if (t > s.last || !r.ok[j >> 2]) {
+        hidden |= 1u << j;
+        z[j] = -INFINITY;
       }
     }
   }
   // P^T = exp2(scale2 * S^T - m)
-  u32x4 p[kNQ];
+  float top = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7]))) * a.scale2;
+  if (__any(top > s.m + (kBias + kSlack))) {
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const float to = fmaxf(s.m, top - kBias), by = __builtin_amdgcn_exp2f(s.m - to);
+    s.m = to;
+    s.l *= by;
 #pragma unroll
-  for (int c = 0; c < kNQ; ++c) {
-    float z[8], top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = sc[c][j >> 2][j & 3] * a.scale2;
-    if (masked) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
-        if (t > s.last[c] || !r.ok[j >> 2]) z[j] = -INFINITY;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, z[j]);
-    if (__any(top > s.m[c] + (kBias + kSlack))) {
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float m = fmaxf(s.m[c], top - kBias), by = __builtin_amdgcn_exp2f(s.m[c] - m);
-      s.m[c] = m;
-      s.l[c] *= by;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s.o[c][e] *= by;
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      z[j] = __builtin_amdgcn_exp2f(z[j] - s.m[c]);
-      sum += z[j];
-    }
-    s.l[c] += sum;
-    // rounded to the values' type: off by half a step of it, as the output is
-    p[c] = u32x4{pack2<T>(z[0], z[1]), pack2<T>(z[2], z[3]), pack2<T>(z[4], z[5]), pack2<T>(z[6], z[7])};
+    for (int e = 0; e < E; ++e) s.o[e] *= by;
   }
-  // V^T P^T
-  float vs[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) vs[j] = exponent(r.vs[j >> 2][j & 3]);
+  for (int j = 0; j < 8; ++j) z[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j], a.scale2, -s.m));
+  if (masked) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = hidden >> j & 1u ? 0.f : z[j];      // a scale of 0 too
+  }
+  s.l += ((z[0] + z[1]) + (z[2] + z[3])) + ((z[4] + z[5]) + (z[6] + z[7]));
+  // rounded to the values' type: off by half a step of it, as the output is
+  const u32x4 p = {pack2<T>(z[0], z[1]), pack2<T>(z[2], z[3]), pack2<T>(z[4], z[5]), pack2<T>(z[6], z[7])};
+  // V^T P^T
   auto pair = [&](auto byte) {               // dimensions 2 byte and 2 byte + 1 of the lane's E
     constexpr int kB = decltype(byte)::value;
     uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = cvt_fp4<T, kB & 3>(r.v[j >> 2][j & 3][kB >> 2], vs[j]);
+    for (int j = 0; j < 8; ++j) w[j] = cvt_fp4<T, kB & 3>(r.v[j >> 2][j & 3][kB >> 2], __uint_as_float(vs[j]));
     u32x4 lo, hi;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       lo[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x05040100u);
       hi[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x07060302u);
     }
-#pragma unroll
-    for (int c = 0; c < kNQ; ++c) {
-      s.o[c][2 * kB] = mfma<T>(lo, p[c], s.o[c][2 * kB]);
-      s.o[c][2 * kB + 1] = mfma<T>(hi, p[c], s.o[c][2 * kB + 1]);
-    }
+    s.o[2 * kB] = mfma<T>(lo, p, s.o[2 * kB]);
+    s.o[2 * kB + 1] = mfma<T>(hi, p, s.o[2 * kB + 1]);
   };
   pair(std::integral_constant<int, 0>{});
   pair(std::integral_constant<int, 1>{});
@@ -266,107 +354,240 @@ __device__ __forceinline__ void step(Rows<T, D, kNQ>& s, Raw<D>& r, const AttnAr
     pair(std::integral_constant<int, 6>{});
     pair(std::integral_constant<int, 7>{});
   }
-  if (masked && __any(odd_v)) nan_values<T, D, kNQ>(s, a, table, kh, t0, end, lane);
+  if (masked && __any(odd_v)) nan_values<D>(s, a, table, kh, t0, end, lane);
 }
 
-template <typename T, int D, int kNQ>
-__device__ __forceinline__ void init_rows(Rows<T, D, kNQ>& s, const AttnArgs& a, int kh, int q0, int n, int kv,
-                                          int row0, int lane) {
-  const int g = lane >> 4;
+template <int D>
+__device__ __forceinline__ void init_rows(Rows<D>& s, const AttnArgs& a, int kh, const Request& rq, int row0, int lane) {
+  const int g = lane >> 4, row = row0 + (lane & 15), i = row / a.group;
+  s.last = i < rq.n ? min(rq.kv - rq.n + i, rq.kv - 1) : -1;
+  s.m = kLowest;
+  s.l = 0.f;
 #pragma unroll
-  for (int c = 0; c < kNQ; ++c) {
-    const int row = row0 + 16 * c + (lane & 15), i = row / a.group;
-    s.last[c] = i < n ? min(kv - n + i, kv - 1) : -1;
-    s.m[c] = kLowest;
-    s.l[c] = 0.f;
+  for (int e = 0; e < D / 16; ++e) s.o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint16_t* q =
+      a.q + (int64_t)(rq.q0 + min(i, rq.n - 1)) * a.q_ts + (int64_t)(kh * a.group + row % a.group) * a.q_hs;
 #pragma unroll
-    for (int e = 0; e < D / 16; ++e) s.o[c][e] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint16_t* q = a.q + (int64_t)(q0 + min(i, n - 1)) * a.q_ts + (int64_t)(kh * a.group + row % a.group) * a.q_hs;
-#pragma unroll
-    for (int kk = 0; kk < D / 32; ++kk) s.q[c][kk] = *(const u32x4*)(q + (D / 4) * g + 8 * kk);
-  }
+  for (int kk = 0; kk < D / 32; ++kk) s.q[kk] = *(const u32x4*)(q + (D / 4) * g + 8 * kk) ^ a.flip;
 }
 
-template <typename T, int D, int kNQ>
-__device__ __forceinline__ void write_rows(Rows<T, D, kNQ>& s, const AttnArgs& a, int kh, int q0, int n, int row0,
-                                           int lane) {
-  constexpr int E = D / 16;
-  const int g = lane >> 4;
-#pragma unroll
-  for (int c = 0; c < kNQ; ++c) {
-    float l = s.l[c];
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    const int row = row0 + 16 * c + (lane & 15), i = row / a.group;
-    if (i >= n) continue;
-    const int64_t at = (int64_t)(q0 + i) * a.heads + kh * a.group + row % a.group;
-    const float by = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* out = a.out + at * D + (D / 4) * g;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t w[E / 2];
-#pragma unroll
-      for (int e = 0; e < E; e += 2) w[e / 2] = pack2<T>(s.o[c][e][j] * by, s.o[c][e + 1][j] * by);
-#pragma unroll
-      for (int e = 0; e < E / 2; e += 2) *(uint2*)(out + E * j + 2 * e) = make_uint2(w[e], w[e + 1]);
-    }
-    if (a.lse && g == 0) a.lse[at] = l == 0.f ? -INFINITY : (s.m[c] + __log2f(l)) * kLn2;
-  }
-}
+// Waves on a SIMD, by the registers that 32 tokens being read and 32 being worked on take.
+constexpr int few_waves(int dim) { return dim == 64 ? 4 : dim == 128 ? 3 : 2; }
+template <int D>
+constexpr int kFewPart = 16 * D + 32;      // floats of a partial result: O [16][D], m [16], l [16]
 
-// One workgroup for each request and key head, its waves taking 16 rows at a time.
+// A row's outputs are stored, four neighbouring dimensions at a time.
 template <typename T, int D>
-__global__ __launch_bounds__(kAThreads) void attn_kernel(AttnArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = blockIdx.x, kh = blockIdx.y;
+__device__ __forceinline__ void store4(const AttnArgs& a, int kh, const Request& rq, int row, int d, float4 o, float m,
+                                       float l) {
+  const int64_t at = (int64_t)(rq.q0 + row / a.group) * a.heads + kh * a.group + row % a.group;
+  const float by = l == 0.f ? 0.f : 1.f / l;
+  *(uint2*)(a.out + at * D + d) = make_uint2(pack2<T>(o.x * by, o.y * by), pack2<T>(o.z * by, o.w * by));
+  if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
+// The work of all requests is a row of steps: for each request, 16 rows of it,
+// key head and kStep of its tokens.  Every workgroup takes an equal run of them,
+// whatever the lengths, its waves 32 tokens each; a run's first and last 16 rows may be
+// shared with neighbours, whose partial results the last one of them to end joins.
+// Bound by HBM with long caches (the codes are read once, K and V of 32 tokens
+// ahead), by latency with short ones.
+template <typename T, int D>
+__global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnArgs a) {
+  constexpr int kPad = D + 4;
+  __shared__ __align__(16) float s_o[kAWaves][16][kPad];
+  __shared__ float s_m[kAWaves][16], s_l[kAWaves][16];
+  __shared__ uint64_t s_wave[kAWaves], s_at[2];
+  __shared__ int s_r;
+  __shared__ uint32_t s_last;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), R = a.n_requests;
   // tokens of no request
-  const int c0 = a.cu_q ? min(max(a.cu_q[0], 0), a.n_tokens) : 0;
-  const int c1 = a.cu_q ? min(max(a.cu_q[a.n_requests], 0), a.n_tokens) : a.n_tokens;
-  for (int t = r; t < a.n_tokens; t += a.n_requests) {
-    if (t >= c0 && t < c1) continue;
-    for (int d = threadIdx.x; d < a.group * D; d += kAThreads)
-      a.out[((int64_t)t * a.heads + kh * a.group) * D + d] = 0;
-    if (a.lse)
-      for (int h = threadIdx.x; h < a.group; h += kAThreads) a.lse[(int64_t)t * a.heads + kh * a.group + h] = -INFINITY;
-  }
-  int q0 = r, n = 1;
   if (a.cu_q) {
-    q0 = a.cu_q[r];
-    const int q1 = a.cu_q[r + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.n_tokens) {
-      if (threadIdx.x == 0 && a.error) atomicOr(a.error, kErrCuQ);
-      return;
+    const int c0 = min(max(a.cu_q[0], 0), a.n_tokens), c1 = min(max(a.cu_q[R], 0), a.n_tokens);
+    for (int t = blockIdx.x; t < a.n_tokens; t += gridDim.x) {
+      if (t >= c0 && t < c1) continue;
+      for (int d = tid; d < a.heads * D; d += kAThreads) a.out[(int64_t)t * a.heads * D + d] = 0;
+      if (a.lse)
+        for (int h = tid; h < a.heads; h += kAThreads) a.lse[(int64_t)t * a.heads + h] = -INFINITY;
     }
-    n = q1 - q0;
   }
-  int kv = a.kv_lens[r];
-  if (kv > (int64_t)a.width << a.shift) {
-    if (threadIdx.x == 0 && a.error) atomicOr(a.error, kErrLength);
-    kv = (int)((int64_t)a.width << a.shift);
+  // the steps of a request: one at least for each 16 rows, so that rows without tokens are written too
+  auto steps_of = [&](int r) -> uint64_t {
+    if (r >= R) return 0;
+    uint32_t bad = 0;
+    const Request q = request(a, r, &bad);
+    if (bad && blockIdx.x == 0 && a.error) atomicOr(a.error, bad);
+    const uint32_t tiles = ((uint32_t)q.n * (uint32_t)a.group + 15u) / 16u;
+    return (uint64_t)tiles * (uint32_t)a.kv_heads * max((uint32_t)(q.kv + kStep - 1) / kStep, 1u);
+  };
+  uint64_t total = 0, sum = 0, mine = 0, upto = 0;
+  for (int base = 0; base < R; base += kAThreads) {
+    mine = steps_of(base + tid);
+    upto = scan_add(mine, s_wave, &sum);
+    total += sum;
   }
-  kv = max(kv, 0);
-  const int32_t* table = a.table + (int64_t)r * a.width;
-  for (int row0 = 16 * wave; row0 < n * a.group; row0 += 16 * kAWaves) {
-    Rows<T, D, 1> s;
-    init_rows(s, a, kh, q0, n, kv, row0, lane);
-    const int first = max(kv - n + row0 / a.group, -1);
-    const int end = kv - n + min((row0 + 15) / a.group, n - 1) + 1;
-    for (int t0 = 0; t0 < end; t0 += 32) {
-      Raw<D> raw;
-      load_tokens<D>(raw, a, table, kh, t0, end, lane);
-      if ((!raw.ok[0] || !raw.ok[1]) && lane == 0 && a.error) atomicOr(a.error, kErrBlock);
-      step(s, raw, a, table, kh, t0, end, first, lane);
+  const uint64_t per = max((total + gridDim.x - 1) / gridDim.x, (uint64_t)kMinSteps);
+  uint64_t pos = per * blockIdx.x;
+  const uint64_t stop = min(pos + per, total);
+  if (pos >= stop) return;
+  sum = 0;
+  for (int base = 0; base < R; base += kAThreads) {
+    if (R > kAThreads) {
+      uint64_t all;
+      mine = steps_of(base + tid);
+      upto = sum + scan_add(mine, s_wave, &all);
+      sum += all;
     }
-    write_rows(s, a, kh, q0, n, row0, lane);
+    if (pos < upto && pos >= upto - mine) {
+      s_r = base + tid;
+      s_at[0] = upto - mine;
+    }
+  }
+  __syncthreads();
+  int r = __builtin_amdgcn_readfirstlane(s_r);
+  uint64_t r_at = s_at[0];                           // the request's first step
+  while (pos < stop) {
+    uint32_t bad = 0;
+    const Request rq = request(a, r, &bad);
+    const uint32_t steps = max((uint32_t)(rq.kv + kStep - 1) / kStep, 1u);
+    const uint64_t tiles = ((uint32_t)rq.n * (uint32_t)a.group + 15u) / 16u, size = tiles * (uint32_t)a.kv_heads * steps;
+    if (pos >= r_at + size) {                        // on to the next request that has rows
+      r_at += size;
+      ++r;
+      continue;
+    }
+    const uint64_t item = (pos - r_at) / steps, item_at = r_at + item * steps;
+    const int kh = (int)(item % (uint32_t)a.kv_heads), row0 = (int)(item / (uint32_t)a.kv_heads) * 16;
+    const int s0 = (int)(pos - item_at), s1 = (int)min((uint64_t)steps, stop - item_at);
+    pos = item_at + s1;
+    const int32_t* table = a.table + (int64_t)r * a.width;
+    const int nr = min(rq.n * a.group - row0, 16);
+    const int first = max(rq.kv - rq.n + row0 / a.group, -1);
+    const int end = rq.kv - rq.n + (row0 + nr - 1) / a.group + 1;
+    Rows<D> s;
+    init_rows(s, a, kh, rq, row0, lane);
+    {
+      const int stop_t = min(end, s1 * kStep);
+      int t0 = s0 * kStep + 32 * wave;
+      if (t0 < stop_t) {
+        Raw<D> ra, rb;
+        load_tokens<D>(ra, a, pages(a, table, t0, end), kh, t0, lane);
+        Pages next = pages(a, table, t0 + kStep, end);
+        bool hole = false;
+        while (true) {
+          // the tokens after these are read while these are worked on
+          if (t0 + kStep < stop_t) load_tokens<D>(rb, a, next, kh, t0 + kStep, lane);
+          next = pages(a, table, t0 + 2 * kStep, end);
+          hole |= !ra.ok[0] || (!ra.ok[1] && t0 + 16 < end);
+          step<T, D>(s, ra, a, table, kh, t0, end, first, lane);
+          t0 += kStep;
+          if (t0 >= stop_t) break;
+          if (t0 + kStep < stop_t) load_tokens<D>(ra, a, next, kh, t0 + kStep, lane);
+          next = pages(a, table, t0 + 2 * kStep, end);
+          hole |= !rb.ok[0] || (!rb.ok[1] && t0 + 16 < end);
+          step<T, D>(s, rb, a, table, kh, t0, end, first, lane);
+          t0 += kStep;
+          if (t0 >= stop_t) break;
+        }
+        if (hole && lane == 0 && a.error) atomicOr(a.error, kErrBlock);
+      }
+    }
+    // the waves' results, joined
+    const int rl = lane & 15, g = lane >> 4;
+    s.l += __shfl_xor(s.l, 16, 64);
+    s.l += __shfl_xor(s.l, 32, 64);
+    __syncthreads();                                 // the item before is stored
+    if (g == 0) {
+      s_m[wave][rl] = s.m;
+      s_l[wave][rl] = s.l;
+    }
+    __syncthreads();
+    float m = s_m[0][rl];
+#pragma unroll
+    for (int w = 1; w < kAWaves; ++w) m = fmaxf(m, s_m[w][rl]);
+    const float by = __builtin_amdgcn_exp2f(s.m - m);
+    if (rl < nr) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < D / 16; e += 4)
+          *(float4*)&s_o[wave][rl][(D / 4) * g + (D / 16) * j + e] =
+              make_float4(s.o[e][j] * by, s.o[e + 1][j] * by, s.o[e + 2][j] * by, s.o[e + 3][j] * by);
+    }
+    __syncthreads();
+    const bool whole = s0 == 0 && s1 == (int)steps;
+    const uint64_t b0 = item_at / per, b1 = (item_at + steps - 1) / per;       // the workgroups that share the rows
+    float* part = a.parts + (2 * (uint64_t)blockIdx.x + (blockIdx.x == b0 ? 1 : 0)) * kFewPart<D>;
+    for (int e = tid; e < nr * (D / 4); e += kAThreads) {
+      const int row = e / (D / 4), d = e % (D / 4) * 4;
+      float top = s_m[0][row];
+#pragma unroll
+      for (int w = 1; w < kAWaves; ++w) top = fmaxf(top, s_m[w][row]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAWaves; ++w) {
+        const float4 v = *(const float4*)&s_o[w][row][d];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        l += s_l[w][row] * __builtin_amdgcn_exp2f(s_m[w][row] - top);
+      }
+      if (whole) {
+        store4<T, D>(a, kh, rq, row0 + row, d, o, top, l);
+      } else {
+        put2(part + row * D + d, o.x, o.y);
+        put2(part + row * D + d + 2, o.z, o.w);
+        if (d == 0) {
+          put1(part + 16 * D + row, top);
+          put1(part + 16 * D + 16 + row, l);
+        }
+      }
+    }
+    if (whole) continue;
+    __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0): the parts have been written
+    __syncthreads();
+    if (tid == 0) {
+      const uint32_t n = (uint32_t)(b1 - b0);
+      s_last = __hip_atomic_fetch_add(a.counters + b0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n;
+      if (s_last) __hip_atomic_store(a.counters + b0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (!s_last) continue;
+    // in the order of the tokens, whoever joins
+    const float* p0 = a.parts + (2 * b0 + 1) * kFewPart<D>;
+    const int np = (int)(b1 - b0) + 1;
+    auto at = [&](int p) { return p == 0 ? p0 : p0 + (2 * (int64_t)p - 1) * kFewPart<D>; };
+    for (int e = tid; e < nr * (D / 4); e += kAThreads) {
+      const int row = e / (D / 4), d = e % (D / 4) * 4;
+      float top = kLowest;
+      for (int p = 0; p < np; ++p) top = fmaxf(top, get1(at(p) + 16 * D + row));
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l = 0.f;
+#pragma unroll 4
+      for (int p = 0; p < np; ++p) {
+        const float* v = at(p);
+        const float w = __builtin_amdgcn_exp2f(get1(v + 16 * D + row) - top);
+        const float2 x = get2(v + row * D + d), y = get2(v + row * D + d + 2);
+        o.x += w * x.x, o.y += w * x.y, o.z += w * y.x, o.w += w * y.y;
+        l += w * get1(v + 16 * D + 16 + row);
+      }
+      store4<T, D>(a, kh, rq, row0 + row, d, o, top, l);
+    }
   }
 }
+
+// Workgroups of the few-row kernel at most: as many as the chip holds at once.
+constexpr int few_wgs(int32_t head_dim) { return 256 * few_waves(head_dim); }
 
 template <typename T>
 void launch_attn(const AttnArgs& a, int32_t head_dim, hipStream_t s) {
-  const dim3 grid((unsigned)a.n_requests, (unsigned)a.kv_heads), threads(kAThreads);
-  if (head_dim == 64) hipLaunchKernelGGL((attn_kernel<T, 64>), grid, threads, 0, s, a);
-  else if (head_dim == 128) hipLaunchKernelGGL((attn_kernel<T, 128>), grid, threads, 0, s, a);
-  else hipLaunchKernelGGL((attn_kernel<T, 256>), grid, threads, 0, s, a);
+  // no more workgroups than the longest requests that the table allows would need
+  const int64_t steps = std::max<int64_t>((((int64_t)a.width << a.shift) + kStep - 1) / kStep, 1);
+  const int64_t tiles = ((int64_t)a.n_tokens * a.group + 15) / 16 + a.n_requests;
+  const int64_t most = std::min<int64_t>(tiles * a.kv_heads, 1 << 20) * steps;
+  const dim3 grid((unsigned)std::min<int64_t>((most + kMinSteps - 1) / kMinSteps, few_wgs(head_dim))), threads(kAThreads);
+  if (head_dim == 64) hipLaunchKernelGGL((attn_few_kernel<T, 64>), grid, threads, 0, s, a);
+  else if (head_dim == 128) hipLaunchKernelGGL((attn_few_kernel<T, 128>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((attn_few_kernel<T, 256>), grid, threads, 0, s, a);
 }
 
 }  // namespace
@@ -381,7 +602,8 @@ size_t sbm_attention_kv4_workspace_bytes(int32_t n_requests, int32_t n_tokens, i
   if (n_requests < 0 || n_tokens < 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads ||
       !kv_shape_ok(16, head_dim))
     return 0;
-  return 16;
+  const size_t part = 16 * (size_t)head_dim + 32;
+  return sizeof(uint32_t) * kCounters + sizeof(float) * part * 2 * few_wgs(head_dim);
 }
 
 int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks, int32_t block_size,
@@ -412,7 +634,8 @@ int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks
   const size_t need = sbm_attention_kv4_workspace_bytes(n_requests, n_tokens, n_heads, n_kv_heads, head_dim);
   if (workspace_bytes < need) return fail(SBM_ENOSPACE, "workspace %zu < %zu bytes", workspace_bytes, need);
   AttnArgs a{(const uint16_t*)q->data, q->token_stride, q->head_stride, cache, block_table, kv_lens, cu_q, out, lse,
-             error, scale * 1.44269504088896341f, n_blocks, __builtin_ctz((unsigned)block_size), table_width,
+             error, (uint32_t*)workspace, (float*)((uint32_t*)workspace + kCounters), fabsf(scale) * 1.44269504088896341f,
+             scale < 0.f ? 0x80008000u : 0u, n_blocks, __builtin_ctz((unsigned)block_size), table_width,
              n_requests, n_tokens, n_heads, n_kv_heads, n_heads / n_kv_heads};
   if (flags & SBM_F_IN_BF16) launch_attn<__bf16>(a, head_dim, (hipStream_t)stream);
   else launch_attn<_Float16>(a, head_dim, (hipStream_t)stream);
