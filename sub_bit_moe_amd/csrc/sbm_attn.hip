@@ -55,7 +55,9 @@ constexpr int kTileRows = 32 * kAWaves;
 constexpr int kTileWgs = 512;
 // Rows (tokens x heads of one key head) of a request up to which the few-row kernel takes it.
 constexpr int kFewRows = 64;
-constexpr int kCounters = 2048;           // of the workspace, before the partial results
+// Counters of the workspace, before the partial results: three levels of joins for each kernel.
+constexpr int kLevels = 3, kFewCounters = 1024;
+constexpr int kCounters = kLevels * (kFewCounters + kTileWgs);
 constexpr uint32_t kErrBlock = 1, kErrLength = 2, kErrCuQ = 4;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -109,13 +111,6 @@ __device__ __forceinline__ float2 get2(const float* p) {
   const uint64_t v = __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
-__device__ __forceinline__ void put1(float* p, float a) {
-  __hip_atomic_store((uint32_t*)p, __float_as_uint(a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float get1(const float* p) {
-  return __uint_as_float(__hip_atomic_load((const uint32_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-}
-
 // One request as a call gives it, every length bounded.
 struct Request {
   int q0, n, kv;               // first token, tokens, cached tokens
@@ -251,7 +246,7 @@ __device__ __forceinline__ void value_scales(const uint32_t* vs, int which, uint
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t w = which & 4 ? vs[2 * i + 1] : vs[2 * i];
+      const uint32_t w0 = vs[2 * i], w1 = vs[2 * i + 1], w = which & 4 ? w1 : w0;
       s[i] = __builtin_amdgcn_alignbit(w, w, 8 * (which & 3) + 9);
     }
   }
@@ -394,9 +389,6 @@ __device__ __forceinline__ void init_rows(Rows<D>& s, const AttnArgs& a, int kh,
 
 // Waves on a SIMD, by the registers that 32 tokens being read and 32 being worked on take.
 constexpr int few_waves(int dim) { return dim == 64 ? 4 : dim == 128 ? 3 : 2; }
-template <int D>
-constexpr int kFewPart = 16 * D + 32;      // floats of a partial result: O [16][D], m [16], l [16]
-
 // A row's outputs are stored, four neighbouring dimensions at a time.
 template <typename T, int D>
 __device__ __forceinline__ void store4(const AttnArgs& a, int kh, const Request& rq, int row, int d, float4 o, float m,
@@ -405,6 +397,84 @@ __device__ __forceinline__ void store4(const AttnArgs& a, int kh, const Request&
   const float by = l == 0.f ? 0.f : 1.f / l;
   *(uint2*)(a.out + at * D + d) = make_uint2(pack2<T>(o.x * by, o.y * by), pack2<T>(o.z * by, o.w * by));
   if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
+// A partial result: O [kRows][D], then (m, l) [kRows].
+template <int D, int kRows>
+constexpr int kPart = kRows * (D + 2);
+
+// Partial results of the same rows, joined kRadix at a time by the workgroup that is the last of them to end, the joins
+// likewise, until one is left: no workgroup waits, and as the members go in order the result
+// does not depend on who ends last.  p: this workgroup's part, already written, of np > 1; at(p): where part p is, a join's
+// result being where its first part was; counters: zero before and after.  One at a time would read np parts with one
+// workgroup (170 parts of 8 x 256: 300 us).
+template <typename T, int D, int kRows, int kRadix, typename At>
+__device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, uint32_t* counters, int level_stride, float* s_w,
+                                  uint32_t* s_flag, int kh, const Request& rq, int row0, int nr) {
+  float* s_l = s_w + kRadix * kRows;
+  const int tid = threadIdx.x;
+  for (int stride = 1;; stride *= kRadix, counters += level_stride) {
+    const int first = p / kRadix * kRadix, members = min(kRadix, np - first);
+    const bool last_level = np <= kRadix;
+    if (members > 1) {
+      __builtin_amdgcn_s_waitcnt(0x0F70);            // vmcnt(0): the part has been written
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t* c = counters + first * stride;
+        *s_flag = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)members - 1;
+        if (*s_flag) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
+      if (!*s_flag) return;
+      for (int i = tid; i < members * nr; i += kAThreads) {
+        const int k = i / nr, row = i % nr;
+        const float2 ml = get2(at((first + k) * stride) + kRows * D + 2 * row);
+        s_w[k * kRows + row] = ml.x;
+        s_l[k * kRows + row] = ml.y;
+      }
+      __syncthreads();
+      if (tid < nr) {
+        float top = s_w[tid], l = 0.f;
+        for (int k = 1; k < members; ++k) top = fmaxf(top, s_w[k * kRows + tid]);
+        for (int k = 0; k < members; ++k) {
+          const float w = __builtin_amdgcn_exp2f(s_w[k * kRows + tid] - top);
+          l += w * s_l[k * kRows + tid];
+          s_w[k * kRows + tid] = w;
+        }
+        s_l[tid] = l;                                // its own row's, read before
+        s_l[kRows + tid] = top;
+      }
+      __syncthreads();
+      for (int e = tid; e < nr * (D / 4); e += kAThreads) {
+        const int row = e / (D / 4), d = e % (D / 4) * 4;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < members; k0 += 8) {
+          float2 x[8], y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float* v = at((first + min(k0 + k, members - 1)) * stride) + row * D + d;
+            x[k] = get2(v), y[k] = get2(v + 2);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float w = k0 + k < members ? s_w[(k0 + k) * kRows + row] : 0.f;
+            o.x += w * x[k].x, o.y += w * x[k].y, o.z += w * y[k].x, o.w += w * y[k].y;
+          }
+        }
+        if (last_level) {
+          store4<T, D>(a, kh, rq, row0 + row, d, o, s_l[kRows + row], s_l[row]);
+        } else {
+          float* v = at(first * stride) + row * D + d;
+          put2(v, o.x, o.y);
+          put2(v + 2, o.z, o.w);
+        }
+      }
+      if (last_level) return;
+      if (tid < nr) put2(at(first * stride) + kRows * D + 2 * tid, s_l[kRows + tid], s_l[tid]);
+    }
+    p /= kRadix;
+    np = (np + kRadix - 1) / kRadix;
+  }
 }
 
 // The work of all requests is a row of steps: for each request, 16 rows of it,
@@ -540,7 +610,7 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     __syncthreads();
     const bool whole = s0 == 0 && s1 == (int)steps;
     const uint64_t b0 = item_at / per, b1 = (item_at + steps - 1) / per;       // the workgroups that share the rows
-    float* part = a.parts + (2 * (uint64_t)blockIdx.x + (blockIdx.x == b0 ? 1 : 0)) * kFewPart<D>;
+    float* part = a.parts + (2 * (uint64_t)blockIdx.x + (blockIdx.x == b0 ? 1 : 0)) * kPart<D, 16>;
     for (int e = tid; e < nr * (D / 4); e += kAThreads) {
       const int row = e / (D / 4), d = e % (D / 4) * 4;
       float top = s_m[0][row];
@@ -559,42 +629,14 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
       } else {
         put2(part + row * D + d, o.x, o.y);
         put2(part + row * D + d + 2, o.z, o.w);
-        if (d == 0) {
-          put1(part + 16 * D + row, top);
-          put1(part + 16 * D + 16 + row, l);
-        }
+        if (d == 0) put2(part + 16 * D + 2 * row, top, l);
       }
     }
     if (whole) continue;
-    __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0): the parts have been written
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t n = (uint32_t)(b1 - b0);
-      s_last = __hip_atomic_fetch_add(a.counters + b0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n;
-      if (s_last) __hip_atomic_store(a.counters + b0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (!s_last) continue;
-    // in the order of the tokens, whoever joins
-    const float* p0 = a.parts + (2 * b0 + 1) * kFewPart<D>;
-    const int np = (int)(b1 - b0) + 1;
-    auto at = [&](int p) { return p == 0 ? p0 : p0 + (2 * (int64_t)p - 1) * kFewPart<D>; };
-    for (int e = tid; e < nr * (D / 4); e += kAThreads) {
-      const int row = e / (D / 4), d = e % (D / 4) * 4;
-      float top = kLowest;
-      for (int p = 0; p < np; ++p) top = fmaxf(top, get1(at(p) + 16 * D + row));
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float l = 0.f;
-#pragma unroll 4
-      for (int p = 0; p < np; ++p) {
-        const float* v = at(p);
-        const float w = __builtin_amdgcn_exp2f(get1(v + 16 * D + row) - top);
-        const float2 x = get2(v + row * D + d), y = get2(v + row * D + d + 2);
-        o.x += w * x.x, o.y += w * x.y, o.z += w * y.x, o.w += w * y.y;
-        l += w * get1(v + 16 * D + 16 + row);
-      }
-      store4<T, D>(a, kh, rq, row0 + row, d, o, top, l);
-    }
+    float* p0 = a.parts + (2 * b0 + 1) * kPart<D, 16>;
+    join<T, D, 16, 16>(a, [&](int p) { return p == 0 ? p0 : p0 + (2 * (int64_t)p - 1) * kPart<D, 16>; },
+                       (int)(blockIdx.x - b0), (int)(b1 - b0) + 1, a.counters + b0, kFewCounters, &s_o[0][0][0], &s_last, kh,
+                       rq, row0, nr);
   }
 }
 
@@ -861,15 +903,15 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, const Request& q) {
   return s;
 }
 
-// With fewer rows than the chip takes the tokens are split; their partial results are joined by the last to end.
+// With fewer rows than the chip takes the tokens are split, kMinTiles to a part at least.
+constexpr uint32_t kMinTiles = 4;
 __device__ __forceinline__ uint32_t parts_of(const Share& s, uint64_t total) {
-  return (uint32_t)max((uint64_t)s.steps * kTileWgs / max(total, (uint64_t)1), (uint64_t)1);
+  const uint64_t parts = (uint64_t)s.steps * kTileWgs / max(total, (uint64_t)1);
+  return (uint32_t)max(min(parts, (uint64_t)(s.steps / kMinTiles)), (uint64_t)1);
 }
 
-constexpr int tile_part(int dim) { return kTileRows * (dim + 2); }       // floats: O, m, l
-
 template <typename T, int D>
-__global__ __launch_bounds__(kAThreads, 2) void attn_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kAThreads, D == 256 ? 1 : 2) void attn_tile_kernel(AttnArgs a) {
   constexpr int kTokens = Tile<D>::kTokens;
   __shared__ __align__(16) Tile<D> s_tile[2];
   __shared__ uint64_t s_wave[kAWaves];
@@ -998,8 +1040,9 @@ __global__ __launch_bounds__(kAThreads, 2) void attn_tile_kernel(AttnArgs a) {
   }
   const uint32_t item = unit / (uint32_t)a.kv_heads / parts * (uint32_t)a.kv_heads + (uint32_t)kh;
   const uint32_t slot0 = s_unit[2] + item * parts;
-  float* mine = a.parts + (int64_t)(slot0 + part) * tile_part(D);
+  float* p0 = a.parts + (int64_t)slot0 * kPart<D, kTileRows>;
   if (valid) {
+    float* mine = p0 + (int64_t)part * kPart<D, kTileRows>;
     float* o = mine + (row - row0) * D + 16 * h;
 #pragma unroll
     for (int db = 0; db < D / 32; ++db)
@@ -1010,33 +1053,9 @@ __global__ __launch_bounds__(kAThreads, 2) void attn_tile_kernel(AttnArgs a) {
       }
     if (h == 0) put2(mine + kTileRows * D + 2 * (row - row0), s.m, s.l);
   }
-  __builtin_amdgcn_s_waitcnt(0x0F70);                  // vmcnt(0): the part has been written
-  __syncthreads();
-  if (tid == 0) {
-    uint32_t* c = a.counters + kCounters / 2 + slot0;
-    s_unit[0] = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
-    if (s_unit[0]) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  if (!s_unit[0]) return;
-  const float* p0 = a.parts + (int64_t)slot0 * tile_part(D);
-  for (int e = tid; e < nr * (D / 4); e += kAThreads) {
-    const int rw = e / (D / 4), d = e % (D / 4) * 4;
-    float top = kLowest;
-    for (uint32_t p = 0; p < parts; ++p) top = fmaxf(top, get2(p0 + p * tile_part(D) + kTileRows * D + 2 * rw).x);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (uint32_t p = 0; p < parts; ++p) {
-      const float* v = p0 + p * tile_part(D);
-      const float2 ml = get2(v + kTileRows * D + 2 * rw);
-      const float w = __builtin_amdgcn_exp2f(ml.x - top);
-      const float2 x = get2(v + rw * D + d), y = get2(v + rw * D + d + 2);
-      o.x += w * x.x, o.y += w * x.y, o.z += w * y.x, o.w += w * y.y;
-      l += w * ml.y;
-    }
-    store4<T, D>(a, kh, rq, row0 + rw, d, o, top, l);
-  }
+  join<T, D, kTileRows, 8>(a, [&](int p) { return p0 + (int64_t)p * kPart<D, kTileRows>; }, part, (int)parts,
+                           a.counters + kLevels * kFewCounters + slot0, kTileWgs, (float*)&s_tile[0], &s_unit[0], kh, rq,
+                           row0, nr);
 }
 
 // ------------------------------------------------------------------ launches
@@ -1085,7 +1104,7 @@ size_t sbm_attention_kv4_workspace_bytes(int32_t n_requests, int32_t n_tokens, i
       !kv_shape_ok(16, head_dim))
     return 0;
   // the two kernels run one after the other
-  const size_t few = (16 * (size_t)head_dim + 32) * 2 * few_wgs(head_dim), tile = (size_t)tile_part(head_dim) * kTileWgs;
+  const size_t row = (size_t)head_dim + 2, few = 16 * row * 2 * few_wgs(head_dim), tile = kTileRows * row * kTileWgs;
   return sizeof(uint32_t) * kCounters + sizeof(float) * std::max(few, tile);
 }
 
