@@ -666,37 +666,40 @@ __device__ __forceinline__ f32x16 mfma_k(u32x4 k, const uint32_t* q, f32x16 c, u
 
 constexpr int kPieces = 4;
 
-// 32 dimensions of a row as kPieces x 32 numbers of 6 bits; returns the pieces' scale bytes.
+// 32 dimensions of a row as kPieces x 32 numbers of 6 bits; returns the pieces' scale bytes.  Each conversion
+// rounds what the ones before left to a multiple of 1/8 of its scale, up to 2.
 template <typename T>
 __device__ __forceinline__ uint32_t split_query(const uint16_t* q, uint32_t flip, uint32_t (&out)[kPieces][6]) {
-  float v[32];
+  typedef float f32x32 __attribute__((ext_vector_type(32)));
+  typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+  f32x16 even, odd;
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const u32x4 w = *(const u32x4*)(q + 8 * i) ^ flip;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint16_t u = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-      if constexpr (__is_same(T, __bf16)) v[8 * i + j] = __uint_as_float((uint32_t)u << 16);
-      else v[8 * i + j] = (float)__builtin_bit_cast(_Float16, u);
-      top = max(top, __float_as_uint(v[8 * i + j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (__is_same(T, __bf16)) {
+        even[4 * i + j] = __uint_as_float(w[j] << 16);
+        odd[4 * i + j] = __uint_as_float(w[j] & 0xFFFF0000u);
+      } else {
+        even[4 * i + j] = (float)__builtin_bit_cast(_Float16, (uint16_t)w[j]);
+        odd[4 * i + j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[j] >> 16));
+      }
+      top = max(top, max(__float_as_uint(even[4 * i + j]) & 0x7FFFFFFFu, __float_as_uint(odd[4 * i + j]) & 0x7FFFFFFFu));
     }
   }
   const uint32_t e = max(top >> 23, 16u);            // the last piece's scale is 2^-126 or more
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = ldexpf(v[i], 127 - (int)e);
-#pragma unroll
   for (int p = 0; p < kPieces; ++p) {
+    const float scale = exponent(e - 5 * p);
+    const u32x6 c = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, scale);     // the two in turn
 #pragma unroll
-    for (int i = 0; i < 6; ++i) out[p][i] = 0;
+    for (int i = 0; i < 6; ++i) out[p][i] = c[i];
+    if (p + 1 == kPieces) break;
+    const f32x32 got = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(c, scale);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float n = rintf(v[i] * 8.f);              // -16 .. 16
-      v[i] = (v[i] - n * 0.125f) * 32.f;              // exact
-      const uint32_t c = (uint32_t)fabsf(n) | (__float_as_uint(n) >> 31 << 5);
-      out[p][6 * i / 32] |= c << (6 * i % 32);
-      if (6 * i % 32 > 26) out[p][6 * i / 32 + 1] |= c >> (32 - 6 * i % 32);
-    }
+    for (int i = 0; i < 16; ++i) even[i] -= got[2 * i], odd[i] -= got[2 * i + 1];       // exact
   }
   // an infinity or a NaN among them: NaN
   return top >= 0x7F800000u ? 0xFFFFFFFFu : e * 0x01010101u - (15u << 24 | 10u << 16 | 5u << 8);
