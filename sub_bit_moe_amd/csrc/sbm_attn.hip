@@ -102,14 +102,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float exponent(uint32_t s) { return __uint_as_float(s << 23); }
 
 // Partial results cross workgroups on other XCDs, whose L2 caches do not see each
-// other's writes: they are written through and read past the caches (agent scope).
+// other's writes: they are written through (agent scope), and read after an acquire of that scope.
 __device__ __forceinline__ void put2(float* p, float a, float b) {
   const uint64_t v = (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
   __hip_atomic_store((uint64_t*)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float2 get2(const float* p) {
-  const uint64_t v = __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 // One request as a call gives it, every length bounded.
 struct Request {
@@ -137,14 +133,23 @@ __device__ __forceinline__ Request request(const AttnArgs& a, int r, uint32_t* b
   return q;
 }
 
+// v of the lane that DPP control kCtrl names, 0 where there is none (or the row mask leaves the lane out).
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ uint64_t from_lane(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, kCtrl, kRowMask, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), kCtrl, kRowMask, 0xF, true);
+  return (uint64_t)hi << 32 | lo;
+}
+
 // Inclusive sum over the workgroup; *total: of all of it.
 __device__ __forceinline__ uint64_t scan_add(uint64_t v, uint64_t* s_wave, uint64_t* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t u = __shfl_up(v, d, 64);
-    if (lane >= d) v += u;
-  }
+  v += from_lane<0x111, 0xF>(v);                       // within rows of 16 lanes
+  v += from_lane<0x112, 0xF>(v);
+  v += from_lane<0x114, 0xF>(v);
+  v += from_lane<0x118, 0xF>(v);
+  v += from_lane<0x142, 0xA>(v);                       // the last lane of rows 0 and 2 to rows 1 and 3
+  v += from_lane<0x143, 0xC>(v);                       // lane 31 to rows 2 and 3
   __syncthreads();
   if (lane == 63) s_wave[wave] = v;
   __syncthreads();
@@ -156,6 +161,11 @@ __device__ __forceinline__ uint64_t scan_add(uint64_t v, uint64_t* s_wave, uint6
   }
   *total = all;
   return v + before;
+}
+
+// Most quotients here are of small numbers, and the division of 64 bits is over a hundred instructions.
+__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
+  return (a | b) >> 32 ? a / b : (uint64_t)((uint32_t)a / (uint32_t)b);
 }
 
 // Where 32 tokens are: their two halves' blocks (-1: none), the same in all lanes.
@@ -426,9 +436,10 @@ __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, ui
       }
       __syncthreads();
       if (!*s_flag) return;
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
       for (int i = tid; i < members * nr; i += kAThreads) {
         const int k = i / nr, row = i % nr;
-        const float2 ml = get2(at((first + k) * stride) + kRows * D + 2 * row);
+        const float2 ml = *(const float2*)(at((first + k) * stride) + kRows * D + 2 * row);
         s_w[k * kRows + row] = ml.x;
         s_l[k * kRows + row] = ml.y;
       }
@@ -445,28 +456,40 @@ __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, ui
         s_l[kRows + tid] = top;
       }
       __syncthreads();
-      for (int e = tid; e < nr * (D / 4); e += kAThreads) {
-        const int row = e / (D / 4), d = e % (D / 4) * 4;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < members; k0 += 8) {
-          float2 x[8], y[8];
+      constexpr int kB = 4;                            // four elements' loads in flight
+      for (int e0 = tid; e0 < nr * (D / 4); e0 += kB * kAThreads) {
+        float4 o[kB];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float* v = at((first + min(k0 + k, members - 1)) * stride) + row * D + d;
-            x[k] = get2(v), y[k] = get2(v + 2);
+        for (int b = 0; b < kB; ++b) o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < members; k0 += 4) {
+          float4 x[4][kB];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float* v = at((first + min(k0 + k, members - 1)) * stride);
+#pragma unroll
+            for (int b = 0; b < kB; ++b) x[k][b] = *(const float4*)(v + 4 * min(e0 + b * kAThreads, nr * (D / 4) - 1));
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float w = k0 + k < members ? s_w[(k0 + k) * kRows + row] : 0.f;
-            o.x += w * x[k].x, o.y += w * x[k].y, o.z += w * y[k].x, o.w += w * y[k].y;
+          for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int b = 0; b < kB; ++b) {
+              const int row = min(e0 + b * kAThreads, nr * (D / 4) - 1) / (D / 4);
+              const float w = k0 + k < members ? s_w[(k0 + k) * kRows + row] : 0.f;
+              o[b].x += w * x[k][b].x, o[b].y += w * x[k][b].y, o[b].z += w * x[k][b].z, o[b].w += w * x[k][b].w;
+            }
           }
         }
-        if (last_level) {
-          store4<T, D>(a, kh, rq, row0 + row, d, o, s_l[kRows + row], s_l[row]);
-        } else {
-          float* v = at(first * stride) + row * D + d;
-          put2(v, o.x, o.y);
-          put2(v + 2, o.z, o.w);
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+          const int e = e0 + b * kAThreads, row = e / (D / 4);
+          if (e >= nr * (D / 4)) break;
+          if (last_level) {
+            store4<T, D>(a, kh, rq, row0 + row, e % (D / 4) * 4, o[b], s_l[kRows + row], s_l[row]);
+          } else {
+            float* v = at(first * stride) + 4 * e;
+            put2(v, o[b].x, o[b].y);
+            put2(v + 2, o[b].z, o[b].w);
+          }
         }
       }
       if (last_level) return;
@@ -518,7 +541,7 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     upto = scan_add(mine, s_wave, &sum);
     total += sum;
   }
-  const uint64_t per = max((total + gridDim.x - 1) / gridDim.x, (uint64_t)kMinSteps);
+  const uint64_t per = max(quotient(total + gridDim.x - 1, gridDim.x), (uint64_t)kMinSteps);
   uint64_t pos = per * blockIdx.x;
   const uint64_t stop = min(pos + per, total);
   if (pos >= stop) return;
@@ -549,8 +572,8 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
       ++r;
       continue;
     }
-    const uint64_t item = (pos - r_at) / steps, item_at = r_at + item * steps;
-    const int kh = (int)(item % (uint32_t)a.kv_heads), row0 = (int)(item / (uint32_t)a.kv_heads) * 16;
+    const uint64_t item = quotient(pos - r_at, steps), item_at = r_at + item * steps, row_tile = quotient(item, (uint32_t)a.kv_heads);
+    const int kh = (int)(item - row_tile * (uint32_t)a.kv_heads), row0 = (int)row_tile * 16;
     const int s0 = (int)(pos - item_at), s1 = (int)min((uint64_t)steps, stop - item_at);
     pos = item_at + s1;
     const int32_t* table = a.table + (int64_t)r * a.width;
@@ -609,7 +632,7 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     }
     __syncthreads();
     const bool whole = s0 == 0 && s1 == (int)steps;
-    const uint64_t b0 = item_at / per, b1 = (item_at + steps - 1) / per;       // the workgroups that share the rows
+    const uint64_t b0 = quotient(item_at, per), b1 = quotient(item_at + steps - 1, per);       // the workgroups that share the rows
     float* part = a.parts + (2 * (uint64_t)blockIdx.x + (blockIdx.x == b0 ? 1 : 0)) * kPart<D, 16>;
     for (int e = tid; e < nr * (D / 4); e += kAThreads) {
       const int row = e / (D / 4), d = e % (D / 4) * 4;
@@ -907,9 +930,9 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, const Request& q) {
 }
 
 // With fewer rows than the chip takes the tokens are split, kMinTiles to a part at least.
-constexpr uint32_t kMinTiles = 4;
+constexpr uint32_t kMinTiles = 8;
 __device__ __forceinline__ uint32_t parts_of(const Share& s, uint64_t total) {
-  const uint64_t parts = (uint64_t)s.steps * kTileWgs / max(total, (uint64_t)1);
+  const uint64_t parts = quotient((uint64_t)s.steps * kTileWgs, max(total, (uint64_t)1));
   return (uint32_t)max(min(parts, (uint64_t)(s.steps / kMinTiles)), (uint64_t)1);
 }
 
