@@ -31,6 +31,7 @@
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "sbm_kv4.h"
 
@@ -51,13 +52,14 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kStep = 32 * kAWaves;
 constexpr int kMinSteps = 2;              // a workgroup's least work, in steps
 // The tile kernel: rows of a workgroup, and workgroups among which a few long rows are split.
-constexpr int kTileRows = 32 * kAWaves;
-constexpr int kTileWgs = 512;
+constexpr int kTileThreads = 256;
+constexpr int kTileRows = kTileThreads / 2;
+constexpr int tile_slots(int dim) { return dim == 256 ? 256 : 512; }
 // Rows (tokens x heads of one key head) of a request up to which the few-row kernel takes it.
 constexpr int kFewRows = 64;
 // Counters of the workspace, before the partial results: three levels of joins for each kernel.
 constexpr int kLevels = 3, kFewCounters = 1024;
-constexpr int kCounters = kLevels * (kFewCounters + kTileWgs);
+constexpr int kCounters = kLevels * (kFewCounters + tile_slots(64));
 constexpr uint32_t kErrBlock = 1, kErrLength = 2, kErrCuQ = 4;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -76,8 +78,9 @@ struct AttnArgs {
   uint32_t* error;
   uint32_t* counters;    // zero between calls
   float* parts;          // partial outputs, maxima and sums
-  float scale2;          // |scale| * log2(e)
+  float scale2;          // |scale| * log2(e); with a scale of 0: 1, and queries times 0
   uint32_t flip;         // 0x80008000 with a negative scale: the sign goes into the queries
+  bool zero;
   int32_t n_blocks, shift, width, n_requests, n_tokens, heads, kv_heads, group;
 };
 
@@ -100,6 +103,19 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 __device__ __forceinline__ float exponent(uint32_t s) { return __uint_as_float(s << 23); }
+
+// Eight of a query's dimensions, with the scale's sign.
+template <typename T>
+__device__ __forceinline__ u32x4 load_query(const AttnArgs& a, const uint16_t* q) {
+  u32x4 w = *(const u32x4*)q ^ a.flip;
+  if (a.zero) {
+    constexpr uint32_t kInf = __is_same(T, __bf16) ? 0x7F80u : 0x7C00u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = ((w[i] & 0x7FFFu) >= kInf ? 0x7FFFu : 0u) | ((w[i] >> 16 & 0x7FFFu) >= kInf ? 0x7FFF0000u : 0u);
+  }
+  return w;
+}
 
 // Partial results cross workgroups on other XCDs, whose L2 caches do not see each
 // other's writes: they are written through (agent scope), and read after an acquire of that scope.
@@ -141,21 +157,33 @@ __device__ __forceinline__ uint64_t from_lane(uint64_t v) {
   return (uint64_t)hi << 32 | lo;
 }
 
-// Inclusive sum over the workgroup; *total: of all of it.
-__device__ __forceinline__ uint64_t scan_add(uint64_t v, uint64_t* s_wave, uint64_t* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Inclusive sum over the wave.
+__device__ __forceinline__ uint64_t wave_scan_add(uint64_t v) {
   v += from_lane<0x111, 0xF>(v);                       // within rows of 16 lanes
   v += from_lane<0x112, 0xF>(v);
   v += from_lane<0x114, 0xF>(v);
   v += from_lane<0x118, 0xF>(v);
   v += from_lane<0x142, 0xA>(v);                       // the last lane of rows 0 and 2 to rows 1 and 3
   v += from_lane<0x143, 0xC>(v);                       // lane 31 to rows 2 and 3
+  return v;
+}
+
+__device__ __forceinline__ uint64_t of_lane(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+}
+
+// Inclusive sum over the workgroup; *total: of all of it.
+template <int kWaves = kAWaves>
+__device__ __forceinline__ uint64_t scan_add(uint64_t v, uint64_t* s_wave, uint64_t* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  v = wave_scan_add(v);
   __syncthreads();
   if (lane == 63) s_wave[wave] = v;
   __syncthreads();
   uint64_t before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kAWaves; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     if (w < wave) before += s_wave[w];
     all += s_wave[w];
   }
@@ -168,15 +196,30 @@ __device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
   return (a | b) >> 32 ? a / b : (uint64_t)((uint32_t)a / (uint32_t)b);
 }
 
+template <typename F, int... kI>
+__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, kI...>) {
+  (f(std::integral_constant<int, kI>{}), ...);
+}
+
+// Keeps a value where it is computed.
+template <typename V>
+__device__ __forceinline__ void pin(V& v) { asm volatile("" : "+v"(v)); }
+
 // Where 32 tokens are: their two halves' blocks (-1: none), the same in all lanes.
 struct Pages {
   int32_t b[2];
 };
 
+// Read by the scalar unit: a vector load's wait, which is in order, would be for the tokens read before it too.
 __device__ __forceinline__ Pages pages(const AttnArgs& a, const int32_t* table, int t0, int end) {
+  typedef const __attribute__((address_space(4))) int32_t* Constant;
+  const Constant held = (Constant)(uintptr_t)table;
   Pages p;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) p.b[x] = t0 + 16 * x < end ? table[(t0 + 16 * x) >> a.shift] : -1;
+  for (int x = 0; x < 2; ++x) {
+    const int t = __builtin_amdgcn_readfirstlane(t0 + 16 * x);
+    p.b[x] = t < end ? held[t >> a.shift] : -1;
+  }
   return p;
 }
 
@@ -192,50 +235,52 @@ struct Raw {
 
 template <int D>
 __device__ __forceinline__ void load_tokens(Raw<D>& r, const AttnArgs& a, Pages p, int kh, int t0, int lane) {
-  const int m = lane & 15, g = lane >> 4;
+  const uint32_t m = lane & 15, g = lane >> 4;
   const int bs = 1 << a.shift;
+  // offsets of 32 bits to addresses of the scalar unit (pinned, or the compiler keeps them as pairs)
+  uint32_t ko = m * (D / 2) + g * (D / 8), kso = m * (D / 32) + (D == 64 ? g >> 1 : D == 128 ? g : 2 * g);
+  uint32_t vo = 4 * g * (D / 2) + m * (D / 32), vso = 4 * g * (D / 32);
+  pin(ko), pin(kso), pin(vo), pin(vso);
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     int32_t b = __builtin_amdgcn_readfirstlane(p.b[x]);
     r.ok[x] = (uint32_t)b < (uint32_t)a.n_blocks;
     if (!r.ok[x]) b = 0;                           // hidden tokens: read, and not used
     const int row = (t0 + 16 * x) & (bs - 1);
-    const uint8_t* rec = a.cache + ((int64_t)b * a.kv_heads + kh) * kv_record_bytes(bs, D);
-    const uint8_t* kc = rec + row * (D / 2) + (m * (D / 2) + g * (D / 8));
+    const uint8_t* rec =
+        a.cache + (uint64_t)((uint32_t)b * (uint32_t)a.kv_heads + (uint32_t)kh) * (uint32_t)kv_record_bytes(bs, D);
+    const uint8_t *kc = rec + row * (D / 2), *vc = kc + bs * (D / 2), *ks = rec + bs * D + row * (D / 32);
+    const uint8_t* vs = ks + bs * (D / 32);
     if constexpr (D == 64) {
-      const uint2 w = *(const uint2*)kc;
+      const uint2 w = *(const uint2*)(kc + ko);
       r.k[x][0] = w.x, r.k[x][1] = w.y;
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
-        const uint4 w = *(const uint4*)(kc + 16 * i);
+        const uint4 w = *(const uint4*)(kc + ko + 16 * i);
         r.k[x][4 * i] = w.x, r.k[x][4 * i + 1] = w.y, r.k[x][4 * i + 2] = w.z, r.k[x][4 * i + 3] = w.w;
       }
     }
-    const uint8_t* ks = rec + bs * D + row * (D / 32) + m * (D / 32);
-    if constexpr (D == 64) r.ks[x] = ks[g >> 1];
-    else if constexpr (D == 128) r.ks[x] = ks[g];
-    else r.ks[x] = *(const uint16_t*)(ks + 2 * g);
-    const uint8_t* vc = rec + bs * (D / 2) + row * (D / 2) + (4 * g * (D / 2) + m * (D / 32));
+    if constexpr (D == 256) r.ks[x] = *(const uint16_t*)(ks + kso);
+    else r.ks[x] = ks[kso];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (D == 64) {
-        r.v[x][i][0] = *(const uint16_t*)(vc + i * (D / 2));
+        r.v[x][i][0] = *(const uint16_t*)(vc + vo + i * (D / 2));
       } else if constexpr (D == 128) {
-        r.v[x][i][0] = *(const uint32_t*)(vc + i * (D / 2));
+        r.v[x][i][0] = *(const uint32_t*)(vc + vo + i * (D / 2));
       } else {
-        const uint2 w = *(const uint2*)(vc + i * (D / 2));
+        const uint2 w = *(const uint2*)(vc + vo + i * (D / 2));
         r.v[x][i][0] = w.x, r.v[x][i][1] = w.y;
       }
     }
-    const uint8_t* vs = rec + bs * D + bs * (D / 32) + row * (D / 32) + 4 * g * (D / 32);
     if constexpr (D == 64) {
-      const uint2 w = *(const uint2*)vs;
+      const uint2 w = *(const uint2*)(vs + vso);
       r.vs[x][0] = w.x, r.vs[x][1] = w.y;
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
-        const uint4 w = *(const uint4*)(vs + 16 * i);
+        const uint4 w = *(const uint4*)(vs + vso + 16 * i);
         r.vs[x][4 * i] = w.x, r.vs[x][4 * i + 1] = w.y, r.vs[x][4 * i + 2] = w.z, r.vs[x][4 * i + 3] = w.w;
       }
     }
@@ -319,7 +364,6 @@ __device__ __forceinline__ void step(Rows<D>& s, const Raw<D>& r, const AttnArgs
   float z[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) z[j] = sc[j >> 2][j & 3];
-  uint32_t hidden = 0;           // bit j: the row does not see it
   if (masked) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -327,10 +371,7 @@ __device__ __forceinline__ void step(Rows<D>& s, const Raw<D>& r, const AttnArgs
       const bool there = r.ok[j >> 2] && t < end, nan = (vs[j] & 0x7F800000u) == 0x7F800000u;
       odd_v = odd_v || (there && nan);
       if (!there || nan) vs[j] = 0x3F800000u;      // 0 * NaN is NaN: what is not seen has to be finite
-      if (t > s.last || !r.ok[j >> 2]) {
-        hidden |= 1u << j;
-        z[j] = -INFINITY;
-      }
+      if (t > s.last || !r.ok[j >> 2]) z[j] = -INFINITY;
     }
   }
   // P^T = exp2(scale2 * S^T - m)
@@ -346,10 +387,6 @@ __device__ __forceinline__ void step(Rows<D>& s, const Raw<D>& r, const AttnArgs
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) z[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j], a.scale2, -s.m));
-  if (masked) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = hidden >> j & 1u ? 0.f : z[j];      // a scale of 0 too
-  }
   s.l += ((z[0] + z[1]) + (z[2] + z[3])) + ((z[4] + z[5]) + (z[6] + z[7]));
   // rounded to the values' type: off by half a step of it, as the output is
   const u32x4 p = {pack2<T>(z[0], z[1]), pack2<T>(z[2], z[3]), pack2<T>(z[4], z[5]), pack2<T>(z[6], z[7])};
@@ -383,7 +420,7 @@ __device__ __forceinline__ void step(Rows<D>& s, const Raw<D>& r, const AttnArgs
   if (masked && __any(odd_v)) nan_values<D>(s, a, table, kh, t0, end, lane);
 }
 
-template <int D>
+template <typename T, int D>
 __device__ __forceinline__ void init_rows(Rows<D>& s, const AttnArgs& a, int kh, const Request& rq, int row0, int lane) {
   const int g = lane >> 4, row = row0 + (lane & 15), i = row / a.group;
   s.last = i < rq.n ? min(rq.kv - rq.n + i, rq.kv - 1) : -1;
@@ -394,11 +431,12 @@ __device__ __forceinline__ void init_rows(Rows<D>& s, const AttnArgs& a, int kh,
   const uint16_t* q =
       a.q + (int64_t)(rq.q0 + min(i, rq.n - 1)) * a.q_ts + (int64_t)(kh * a.group + row % a.group) * a.q_hs;
 #pragma unroll
-  for (int kk = 0; kk < D / 32; ++kk) s.q[kk] = *(const u32x4*)(q + (D / 4) * g + 8 * kk) ^ a.flip;
+  for (int kk = 0; kk < D / 32; ++kk) s.q[kk] = load_query<T>(a, q + (D / 4) * g + 8 * kk);
 }
 
-// Waves on a SIMD, by the registers that 32 tokens being read and 32 being worked on take.
-constexpr int few_waves(int dim) { return dim == 64 ? 4 : dim == 128 ? 3 : 2; }
+// How many times 32 tokens a wave has under way, and waves on a SIMD, by the registers that takes.
+constexpr int few_ring(int dim) { return dim == 256 ? 1 : 2; }
+constexpr int few_waves(int dim) { return dim == 64 ? 3 : 2; }
 // A row's outputs are stored, four neighbouring dimensions at a time.
 template <typename T, int D>
 __device__ __forceinline__ void store4(const AttnArgs& a, int kh, const Request& rq, int row, int d, float4 o, float m,
@@ -418,7 +456,7 @@ constexpr int kPart = kRows * (D + 2);
 // does not depend on who ends last.  p: this workgroup's part, already written, of np > 1; at(p): where part p is, a join's
 // result being where its first part was; counters: zero before and after.  One at a time would read np parts with one
 // workgroup (170 parts of 8 x 256: 300 us).
-template <typename T, int D, int kRows, int kRadix, typename At>
+template <typename T, int D, int kRows, int kRadix, int kThreads, typename At>
 __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, uint32_t* counters, int level_stride, float* s_w,
                                   uint32_t* s_flag, int kh, const Request& rq, int row0, int nr) {
   float* s_l = s_w + kRadix * kRows;
@@ -437,7 +475,7 @@ __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, ui
       __syncthreads();
       if (!*s_flag) return;
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-      for (int i = tid; i < members * nr; i += kAThreads) {
+      for (int i = tid; i < members * nr; i += kThreads) {
         const int k = i / nr, row = i % nr;
         const float2 ml = *(const float2*)(at((first + k) * stride) + kRows * D + 2 * row);
         s_w[k * kRows + row] = ml.x;
@@ -457,7 +495,7 @@ __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, ui
       }
       __syncthreads();
       constexpr int kB = 4;                            // four elements' loads in flight
-      for (int e0 = tid; e0 < nr * (D / 4); e0 += kB * kAThreads) {
+      for (int e0 = tid; e0 < nr * (D / 4); e0 += kB * kThreads) {
         float4 o[kB];
 #pragma unroll
         for (int b = 0; b < kB; ++b) o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -467,13 +505,13 @@ __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, ui
           for (int k = 0; k < 4; ++k) {
             const float* v = at((first + min(k0 + k, members - 1)) * stride);
 #pragma unroll
-            for (int b = 0; b < kB; ++b) x[k][b] = *(const float4*)(v + 4 * min(e0 + b * kAThreads, nr * (D / 4) - 1));
+            for (int b = 0; b < kB; ++b) x[k][b] = *(const float4*)(v + 4 * min(e0 + b * kThreads, nr * (D / 4) - 1));
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
 #pragma unroll
             for (int b = 0; b < kB; ++b) {
-              const int row = min(e0 + b * kAThreads, nr * (D / 4) - 1) / (D / 4);
+              const int row = min(e0 + b * kThreads, nr * (D / 4) - 1) / (D / 4);
               const float w = k0 + k < members ? s_w[(k0 + k) * kRows + row] : 0.f;
               o[b].x += w * x[k][b].x, o[b].y += w * x[k][b].y, o[b].z += w * x[k][b].z, o[b].w += w * x[k][b].w;
             }
@@ -481,7 +519,7 @@ __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, ui
         }
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
-          const int e = e0 + b * kAThreads, row = e / (D / 4);
+          const int e = e0 + b * kThreads, row = e / (D / 4);
           if (e >= nr * (D / 4)) break;
           if (last_level) {
             store4<T, D>(a, kh, rq, row0 + row, e % (D / 4) * 4, o[b], s_l[kRows + row], s_l[row]);
@@ -511,7 +549,7 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
   constexpr int kPad = D + 4;
   __shared__ __align__(16) float s_o[kAWaves][16][kPad];
   __shared__ float s_m[kAWaves][16], s_l[kAWaves][16];
-  __shared__ uint64_t s_wave[kAWaves], s_at[2];
+  __shared__ uint64_t s_wave[kAWaves], s_at;
   __shared__ int s_r;
   __shared__ uint32_t s_last;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), R = a.n_requests;
@@ -535,32 +573,41 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     const uint32_t tiles = ((uint32_t)q.n * (uint32_t)a.group + 15u) / 16u;
     return (uint64_t)tiles * (uint32_t)a.kv_heads * max((uint32_t)(q.kv + kStep - 1) / kStep, 1u);
   };
-  uint64_t total = 0, sum = 0, mine = 0, upto = 0;
-  for (int base = 0; base < R; base += kAThreads) {
-    mine = steps_of(base + tid);
-    upto = scan_add(mine, s_wave, &sum);
-    total += sum;
-  }
-  const uint64_t per = max(quotient(total + gridDim.x - 1, gridDim.x), (uint64_t)kMinSteps);
-  uint64_t pos = per * blockIdx.x;
-  const uint64_t stop = min(pos + per, total);
-  if (pos >= stop) return;
-  sum = 0;
-  for (int base = 0; base < R; base += kAThreads) {
-    if (R > kAThreads) {
-      uint64_t all;
-      mine = steps_of(base + tid);
-      upto = sum + scan_add(mine, s_wave, &all);
-      sum += all;
+  uint64_t total = 0, pos, stop, per, r_at;            // r_at: the request's first step
+  int r;
+  auto share = [&] {
+    per = max(quotient(total + gridDim.x - 1, gridDim.x), (uint64_t)kMinSteps);
+    pos = per * blockIdx.x;
+    stop = min(pos + per, total);
+  };
+  if (R <= 64) {                                       // every wave for itself
+    const uint64_t mine = steps_of(lane), upto = wave_scan_add(mine);
+    total = of_lane(upto, 63);
+    share();
+    if (pos >= stop) return;
+    r = (int)__builtin_ctzll(__ballot(pos < upto && pos >= upto - mine));
+    r_at = of_lane(upto - mine, r);
+  } else {
+    uint64_t sum = 0;
+    for (int base = 0; base < R; base += kAThreads) {
+      scan_add(steps_of(base + tid), s_wave, &sum);
+      total += sum;
     }
-    if (pos < upto && pos >= upto - mine) {
-      s_r = base + tid;
-      s_at[0] = upto - mine;
+    share();
+    if (pos >= stop) return;
+    uint64_t before = 0;
+    for (int base = 0; base < R; base += kAThreads) {
+      const uint64_t mine = steps_of(base + tid), upto = before + scan_add(mine, s_wave, &sum);
+      before += sum;
+      if (pos < upto && pos >= upto - mine) {
+        s_r = base + tid;
+        s_at = upto - mine;
+      }
     }
+    __syncthreads();
+    r = __builtin_amdgcn_readfirstlane(s_r);
+    r_at = s_at;
   }
-  __syncthreads();
-  int r = __builtin_amdgcn_readfirstlane(s_r);
-  uint64_t r_at = s_at[0];                           // the request's first step
   while (pos < stop) {
     uint32_t bad = 0;
     const Request rq = request(a, r, &bad);
@@ -581,30 +628,31 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     const int first = max(rq.kv - rq.n + row0 / a.group, -1);
     const int end = rq.kv - rq.n + (row0 + nr - 1) / a.group + 1;
     Rows<D> s;
-    init_rows(s, a, kh, rq, row0, lane);
+    init_rows<T, D>(s, a, kh, rq, row0, lane);
     {
       const int stop_t = min(end, s1 * kStep);
       int t0 = s0 * kStep + 32 * wave;
       if (t0 < stop_t) {
-        Raw<D> ra, rb;
-        load_tokens<D>(ra, a, pages(a, table, t0, end), kh, t0, lane);
-        Pages next = pages(a, table, t0 + kStep, end);
+        constexpr int kRing = few_ring(D);
+        Raw<D> raw[kRing];
+        Pages next = pages(a, table, t0, end);
+        each([&](auto i) {
+          constexpr int x = decltype(i)::value;
+          if (x == 0 || t0 + x * kStep < stop_t) load_tokens<D>(raw[x], a, next, kh, t0 + x * kStep, lane);
+          next = pages(a, table, t0 + (x + 1) * kStep, end);
+        }, std::make_integer_sequence<int, kRing>{});
         bool hole = false;
-        while (true) {
-          // the tokens after these are read while these are worked on
-          if (t0 + kStep < stop_t) load_tokens<D>(rb, a, next, kh, t0 + kStep, lane);
-          next = pages(a, table, t0 + 2 * kStep, end);
-          hole |= !ra.ok[0] || (!ra.ok[1] && t0 + 16 < end);
-          step<T, D>(s, ra, a, table, kh, t0, end, first, lane);
+        // the tokens after these are read while these are worked on
+        auto turn = [&](auto i) {
+          Raw<D>& r = raw[decltype(i)::value];
+          if (t0 >= stop_t) return;
+          hole |= !r.ok[0] || (!r.ok[1] && t0 + 16 < end);
+          step<T, D>(s, r, a, table, kh, t0, end, first, lane);
+          if (t0 + kRing * kStep < stop_t) load_tokens<D>(r, a, next, kh, t0 + kRing * kStep, lane);
+          next = pages(a, table, t0 + (kRing + 1) * kStep, end);
           t0 += kStep;
-          if (t0 >= stop_t) break;
-          if (t0 + kStep < stop_t) load_tokens<D>(ra, a, next, kh, t0 + kStep, lane);
-          next = pages(a, table, t0 + 2 * kStep, end);
-          hole |= !rb.ok[0] || (!rb.ok[1] && t0 + 16 < end);
-          step<T, D>(s, rb, a, table, kh, t0, end, first, lane);
-          t0 += kStep;
-          if (t0 >= stop_t) break;
-        }
+        };
+        while (t0 < stop_t) each(turn, std::make_integer_sequence<int, kRing>{});
         if (hole && lane == 0 && a.error) atomicOr(a.error, kErrBlock);
       }
     }
@@ -657,7 +705,7 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     }
     if (whole) continue;
     float* p0 = a.parts + (2 * b0 + 1) * kPart<D, 16>;
-    join<T, D, 16, 16>(a, [&](int p) { return p == 0 ? p0 : p0 + (2 * (int64_t)p - 1) * kPart<D, 16>; },
+    join<T, D, 16, 16, kAThreads>(a, [&](int p) { return p == 0 ? p0 : p0 + (2 * (int64_t)p - 1) * kPart<D, 16>; },
                        (int)(blockIdx.x - b0), (int)(b1 - b0) + 1, a.counters + b0, kFewCounters, &s_o[0][0][0], &s_last, kh,
                        rq, row0, nr);
   }
@@ -687,19 +735,22 @@ __device__ __forceinline__ f32x16 mfma_k(u32x4 k, const uint32_t* q, f32x16 c, u
                                                          (int)qs);
 }
 
-constexpr int kPieces = 4;
+// Pieces of a query: 5 bits each below the largest of its 32 dimensions.  Three hold what bf16 has of all that are above
+// 1/64 of it, and the rest to 2^-14 of it; fp16 takes four.
+template <typename T>
+constexpr int kPieces = __is_same(T, __bf16) ? 3 : 4;
 
 // 32 dimensions of a row as kPieces x 32 numbers of 6 bits; returns the pieces' scale bytes.  Each conversion
 // rounds what the ones before left to a multiple of 1/8 of its scale, up to 2.
 template <typename T>
-__device__ __forceinline__ uint32_t split_query(const uint16_t* q, uint32_t flip, uint32_t (&out)[kPieces][6]) {
+__device__ __forceinline__ uint32_t split_query(const AttnArgs& a, const uint16_t* q, uint32_t (&out)[kPieces<T>][6]) {
   typedef float f32x32 __attribute__((ext_vector_type(32)));
   typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
   f32x16 even, odd;
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const u32x4 w = *(const u32x4*)(q + 8 * i) ^ flip;
+    const u32x4 w = load_query<T>(a, q + 8 * i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if constexpr (__is_same(T, __bf16)) {
@@ -714,12 +765,12 @@ __device__ __forceinline__ uint32_t split_query(const uint16_t* q, uint32_t flip
   }
   const uint32_t e = max(top >> 23, 16u);            // the last piece's scale is 2^-126 or more
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p) {
+  for (int p = 0; p < kPieces<T>; ++p) {
     const float scale = exponent(e - 5 * p);
     const u32x6 c = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, scale);     // the two in turn
 #pragma unroll
     for (int i = 0; i < 6; ++i) out[p][i] = c[i];
-    if (p + 1 == kPieces) break;
+    if (p + 1 == kPieces<T>) break;
     const f32x32 got = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(c, scale);
 #pragma unroll
     for (int i = 0; i < 16; ++i) even[i] -= got[2 * i], odd[i] -= got[2 * i + 1];       // exact
@@ -731,13 +782,15 @@ __device__ __forceinline__ uint32_t split_query(const uint16_t* q, uint32_t flip
 // The workgroup's tile in LDS.  K: [token / 32][dimension / 64][64 lanes][16 bytes], V: [token / 16]
 // [dimension / 32][64 lanes][16 bytes], a lane's 16 bytes being its operand; lanes are swapped within eights so that
 // neither the writes below nor the reads meet in a bank.
+constexpr int tile_units(int dim) { return dim == 256 ? 2 : 1; }       // what a thread brings: two with wide heads, for 64 tokens
 template <int D>
 struct Tile {
-  static constexpr int kTokens = 8192 / D;
-  uint8_t k[4096], v[16384], ks[256];
+  static constexpr int kUnits = tile_units(D), kTokens = 32 * kTileThreads * kUnits / D;
+  uint8_t k[kTokens * D / 2], v[kTokens * D * 2], ks[kTokens * D / 32];
 };
 
-// What a thread brings of a tile: 16 bytes and one scale of a K row, and 8 dimensions of 4 V rows, all of one block.
+// One unit of a tile: 16 bytes and one scale of a K row, and 8 dimensions of 4 V rows, all of one block.  A wave's units
+// are of one block too (two with D = 64), so that its address is made by the scalar unit.
 template <int D>
 struct Fetch {
   uint4 k;
@@ -745,42 +798,67 @@ struct Fetch {
   bool ok;
 };
 
+// The blocks of a wave's unit: of its lanes' 16 tokens.
 template <int D>
-__device__ __forceinline__ void fetch(Fetch<D>& f, const AttnArgs& a, int32_t b, int kh, int t0, int tid) {
+struct Blocks {
+  int32_t b[D == 64 ? 2 : 1];
+};
+
+template <int D>
+__device__ __forceinline__ void fetch(Fetch<D>& f, const AttnArgs& a, const Blocks<D>& blocks, int kh, int t0, int unit) {
   const int bs = 1 << a.shift;
-  f.ok = (uint32_t)b < (uint32_t)a.n_blocks;
-  if (!f.ok) b = 0;                                   // hidden tokens: read, and not used
-  const int row = (t0 + 16 * (tid / (D / 2))) & (bs - 1);                    // the thread's 16 tokens
-  const uint8_t* rec = a.cache + ((int64_t)b * a.kv_heads + kh) * kv_record_bytes(bs, D);
-  const int kt = tid / (D / 32) % 16, kx = tid % (D / 32);
-  f.k = *(const uint4*)(rec + (row + kt) * (D / 2) + 16 * kx);
-  f.ks = rec[bs * D + (row + kt) * (D / 32) + kx];
-  const int u = tid >> 1, c = u % (D / 8), run = row + 8 * (tid & 1) + 4 * (u / (D / 8) & 1);
-  const uint8_t* vc = rec + bs * (D / 2) + run * (D / 2) + 4 * c;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f.v[i] = *(const uint32_t*)(vc + i * (D / 2));
-  const uint8_t* vs = rec + bs * D + bs * (D / 32) + run * (D / 32);
+  // a block's K codes from the 16 tokens on; hidden tokens: read, and not used
+  auto record = [&](int32_t b, bool* ok) {
+    b = __builtin_amdgcn_readfirstlane(b);
+    *ok = (uint32_t)b < (uint32_t)a.n_blocks;
+    return a.cache + (uint64_t)((uint32_t)(*ok ? b : 0) * (uint32_t)a.kv_heads + (uint32_t)kh) * (uint32_t)kv_record_bytes(bs, D);
+  };
+  const int unit0 = __builtin_amdgcn_readfirstlane(unit);
+  const uint8_t* rec = record(blocks.b[0], &f.ok);
+  int row = (t0 + 16 * (unit0 / (D / 2))) & (bs - 1);                        // the unit's 16 tokens
   if constexpr (D == 64) {
-    const uint2 w = *(const uint2*)vs;
+    bool ok;
+    const uint8_t* other = record(blocks.b[1], &ok);
+    const int row1 = (t0 + 16 * (unit0 / 32 + 1)) & (bs - 1);
+    const bool second = unit & 32;
+    rec = second ? other : rec;
+    row = second ? row1 : row;
+    f.ok = second ? ok : f.ok;
+  }
+  const uint8_t* scales = rec + bs * D + row * (D / 32);
+  // offsets of 32 bits to an address of the scalar unit (pinned, or the compiler keeps them as pairs)
+  uint32_t ko = unit % (D / 2);
+  const uint32_t u = unit >> 1, c = u % (D / 8);
+  uint32_t run = 8 * (unit & 1) + 4 * (u / (D / 8) & 1), vo = run * (D / 2) + 4 * c;
+  run *= D / 32;
+  pin(ko), pin(run), pin(vo);
+  f.k = *(const uint4*)(rec + row * (D / 2) + 16 * ko);
+  f.ks = scales[ko];
+  const uint8_t* vc = rec + bs * (D / 2) + row * (D / 2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.v[i] = *(const uint32_t*)(vc + vo + i * (D / 2));
+  const uint8_t* vs = scales + bs * (D / 32);
+  if constexpr (D == 64) {
+    const uint2 w = *(const uint2*)(vs + run);
     f.vs[0] = w.x, f.vs[1] = w.y;
   } else {
 #pragma unroll
     for (int i = 0; i < D / 128; ++i) {
-      const uint4 w = *(const uint4*)(vs + 16 * i);
+      const uint4 w = *(const uint4*)(vs + run + 16 * i);
       f.vs[4 * i] = w.x, f.vs[4 * i + 1] = w.y, f.vs[4 * i + 2] = w.z, f.vs[4 * i + 3] = w.w;
     }
   }
 }
 
-// The fetched part into LDS, V converted.  border: some row of the workgroup does not see all of the tile.  Returns what
-// the waves have to know: bit 0 .. 7: the 16 tokens without a block, bit 8: a NaN among V that went in as 1.
-template <typename T, int D>
-__device__ __forceinline__ uint32_t put_tile(Tile<D>& tile, const Fetch<D>& f, int t0, int end, bool border, int tid) {
-  const int kt = tid / (D / 32), kx = tid % (D / 32);
-  *(uint4*)(tile.k + ((kt >> 5) * (D / 64) + (kx >> 1)) * 1024 + (((kt & 31) ^ (kx * (256 / D))) + 32 * (kx & 1)) * 16) = f.k;
-  tile.ks[tid] = (uint8_t)f.ks;
-  const int u = tid >> 1, c = u % (D / 8), h = u / (D / 8) & 1, tb = tid / (D / 2), half = tid & 1;
-  uint32_t sc[4], note = 0;
+// The fetched part into LDS, V converted, in kPutSteps steps after the first.
+// border: some row of the workgroup does not see all of the tile.  Returns what
+// the waves have to know: a bit for each 16 tokens without a block, kNoteNaN: a NaN among V that went in as 1.
+constexpr uint32_t kNoteNaN = 1u << 31;
+constexpr int kPutSteps = 5;
+template <int D>
+__device__ __forceinline__ uint32_t prepare_values(const Fetch<D>& f, uint32_t (&sc)[4], int t0, int end, bool border, int unit) {
+  const int u = unit >> 1, c = u % (D / 8), h = u / (D / 8) & 1, tb = unit / (D / 2), half = unit & 1;
+  uint32_t note = 0;
   value_scales<D>(f.vs, c >> 2, sc);
   if (!f.ok) note = 1u << tb;
   if (border || !f.ok) {
@@ -788,41 +866,46 @@ __device__ __forceinline__ uint32_t put_tile(Tile<D>& tile, const Fetch<D>& f, i
     for (int i = 0; i < 4; ++i) {
       const bool there = f.ok && t0 + 16 * tb + 8 * half + 4 * h + i < end;
       const bool nan = (sc[i] & 0x7F800000u) == 0x7F800000u;
-      if (there && nan) note |= 256u;
+      if (there && nan) note |= kNoteNaN;
       if (!there || nan) sc[i] = 0x3F800000u;         // 0 * NaN is NaN: what is not seen has to be finite
     }
   }
-  const int db = c >> 2;
-  uint8_t* to = tile.v + (tb * (D / 32) + db) * 1024 + 32 * 16 * h + 8 * half;
-  auto pair = [&](auto byte) {                         // dimensions 2 byte and 2 byte + 1 of the thread's 8
-    constexpr int kB = decltype(byte)::value;
+  return note;
+}
+
+template <int kStepNo, typename T, int D>
+__device__ __forceinline__ void put_tile(Tile<D>& tile, const Fetch<D>& f, const uint32_t (&sc)[4], int unit) {
+  if constexpr (kStepNo == 0) {
+    const int kt = unit / (D / 32), kx = unit % (D / 32);
+    *(uint4*)(tile.k + ((kt >> 5) * (D / 64) + (kx >> 1)) * 1024 + (((kt & 31) ^ (kx * (256 / D))) + 32 * (kx & 1)) * 16) = f.k;
+    tile.ks[unit] = (uint8_t)f.ks;
+  } else {
+    constexpr int kB = kStepNo - 1;                    // dimensions 2 kB and 2 kB + 1 of the thread's 8
+    const int u = unit >> 1, c = u % (D / 8), h = u / (D / 8) & 1, tb = unit / (D / 2), half = unit & 1, db = c >> 2;
+    uint8_t* to = tile.v + (tb * (D / 32) + db) * 1024 + 32 * 16 * h + 8 * half;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = cvt_fp4<T, kB>(f.v[i], __uint_as_float(sc[i]));
     // dimension 8 (c & 3) + j of the 32 is in lane (j & 3) * 8 + 2 (c & 3) + j / 4
-    const int lo = ((2 * kB & 3) * 8 + 2 * (c & 3) + (kB >> 1)) ^ (db & 1), hi = lo ^ 8;
-    *(uint2*)(to + 16 * lo) = make_uint2(__builtin_amdgcn_perm(w[1], w[0], 0x05040100u), __builtin_amdgcn_perm(w[3], w[2], 0x05040100u));
-    *(uint2*)(to + 16 * hi) = make_uint2(__builtin_amdgcn_perm(w[1], w[0], 0x07060302u), __builtin_amdgcn_perm(w[3], w[2], 0x07060302u));
-  };
-  pair(std::integral_constant<int, 0>{});
-  pair(std::integral_constant<int, 1>{});
-  pair(std::integral_constant<int, 2>{});
-  pair(std::integral_constant<int, 3>{});
-  return note;
+    to += 16 * (2 * (c & 3) + ((kB >> 1) ^ (db & 1)));
+    constexpr int kLo = 16 * 8 * (2 * kB & 3), kHi = kLo ^ 128;
+    *(uint2*)(to + kLo) = make_uint2(__builtin_amdgcn_perm(w[1], w[0], 0x05040100u), __builtin_amdgcn_perm(w[3], w[2], 0x05040100u));
+    *(uint2*)(to + kHi) = make_uint2(__builtin_amdgcn_perm(w[1], w[0], 0x07060302u), __builtin_amdgcn_perm(w[3], w[2], 0x07060302u));
+  }
 }
 
 // A wave's 32 rows.
-template <int D>
+template <typename T, int D>
 struct TileRows {
-  uint32_t q[D / 64][kPieces][6], qs[D / 64];
+  uint32_t q[D / 64][kPieces<T>][6], qs[D / 64];
   f32x16 o[D / 32];
   float m, l;
   int last;
 };
 
 // As nan_values.  o[db][i] is dimension 32 db + 16 h + 4 (i % 4) + i / 4.
-template <int D>
-__device__ __forceinline__ void tile_nan_values(TileRows<D>& s, const AttnArgs& a, const int32_t* table, int kh, int t0,
+template <typename T, int D>
+__device__ __forceinline__ void tile_nan_values(TileRows<T, D>& s, const AttnArgs& a, const int32_t* table, int kh, int t0,
                                              int end) {
   const int bs = 1 << a.shift;
   for (int t = t0; t < min(t0 + Tile<D>::kTokens, end); ++t) {
@@ -839,77 +922,130 @@ __device__ __forceinline__ void tile_nan_values(TileRows<D>& s, const AttnArgs& 
   }
 }
 
-// 32 tokens of the tile for a wave's rows.
-template <typename T, int D>
-__device__ __forceinline__ void tile_step(TileRows<D>& s, const Tile<D>& tile, int sub, int t0, bool masked, uint32_t note,
-                                          float scale2, int lane) {
+// K of 32 tokens of the tile as a lane takes it.
+template <int D>
+struct KeyOperand {
+  u32x4 k[D / 64];
+  uint32_t ks[D == 256 ? 2 : 1];
+};
+
+template <int D>
+__device__ __forceinline__ KeyOperand<D> tile_keys(const Tile<D>& tile, int sub, int lane) {
   const int tl = lane & 31, h = lane >> 5;
-  f32x16 z = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const uint8_t* ksp = tile.ks + (32 * sub + tl) * (D / 32);
-  uint32_t ks[2] = {0, 0};
+  KeyOperand<D> o;
+#pragma unroll
+  for (int kb = 0; kb < D / 64; ++kb)
+    o.k[kb] = *(const u32x4*)(tile.k + (sub * (D / 64) + kb) * 1024 + ((tl ^ ((2 * kb + h) * (256 / D))) + 32 * h) * 16);
+  const uint8_t* ks = tile.ks + (32 * sub + tl) * (D / 32);
   if constexpr (D == 64) {
-    ks[0] = *(const uint16_t*)ksp >> (8 * h);
+    o.ks[0] = *(const uint16_t*)ks >> (8 * h);
   } else {
-    ks[0] = *(const uint32_t*)ksp >> (8 * h);
-    if constexpr (D == 256) ks[1] = *(const uint32_t*)(ksp + 4) >> (8 * h);
+    o.ks[0] = *(const uint32_t*)ks >> (8 * h);
+    if constexpr (D == 256) o.ks[1] = *(const uint32_t*)(ks + 4) >> (8 * h);
   }
-  auto dims = [&](auto block) {
-    constexpr int kb = decltype(block)::value, kByte = kb % 2 * 2;
-    const u32x4 k = *(const u32x4*)(tile.k + (sub * (D / 64) + kb) * 1024 + ((tl ^ ((2 * kb + h) * (256 / D))) + 32 * h) * 16);
-    z = mfma_k<kByte, 3>(k, s.q[kb][3], z, ks[kb / 2], s.qs[kb]);
-    z = mfma_k<kByte, 2>(k, s.q[kb][2], z, ks[kb / 2], s.qs[kb]);
-    z = mfma_k<kByte, 1>(k, s.q[kb][1], z, ks[kb / 2], s.qs[kb]);
-    z = mfma_k<kByte, 0>(k, s.q[kb][0], z, ks[kb / 2], s.qs[kb]);
+  return o;
+}
+
+// A tile for a wave's rows.  A wave issues in order and a matrix instruction takes 32 cycles, so instructions that do
+// not wait for it are put between any two: the next tile's reads between the first products (`load`), the
+// exponentials of 32 tokens between the products of the next 32, their maximum between the products of V, and between
+// the last of those the next tile's conversion (`prepare`, then `put`).  The scheduling barriers keep this order.  What the
+// matrix unit needs is read from LDS some products ahead.
+template <typename T, int D, typename Load, typename Prepare, typename Put>
+__device__ __forceinline__ void tile_products(TileRows<T, D>& s, const Tile<D>& tile, int t0, bool masked, uint32_t note,
+                                              float scale2, int lane, Load load, Prepare prepare, Put put) {
+  constexpr int kSubs = Tile<D>::kTokens / 32;
+  constexpr int kP = kPieces<T>, kS = D / 64 * kP, kG = D / 16, kHalf = kG / 2;      // products for 32 tokens: scores, values
+  const int h = lane >> 5;
+  const f32x16 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  KeyOperand<D> keys = tile_keys<D>(tile, 0, lane);
+  auto product = [&](auto g, f32x16& z) {              // one of the scores'
+    constexpr int kb = decltype(g)::value / kP, kPiece = kP - 1 - decltype(g)::value % kP;
+    z = mfma_k<kb % 2 * 2, kPiece>(keys.k[kb], s.q[kb][kPiece], z, keys.ks[kb / 2], s.qs[kb]);
   };
-  dims(std::integral_constant<int, 0>{});
-  if constexpr (D > 64) dims(std::integral_constant<int, 1>{});
-  if constexpr (D > 128) {
-    dims(std::integral_constant<int, 2>{});
-    dims(std::integral_constant<int, 3>{});
-  }
-  uint32_t hidden = 0;
-  if (masked) {
+  auto mask = [&](f32x16& z, int sub) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int t = 32 * sub + 8 * (i >> 2) + 4 * h + (i & 3);
-      if (t0 + t > s.last || (note >> (2 * sub + (i >> 3)) & 1u)) {
-        hidden |= 1u << i;
-        z[i] = -INFINITY;
-      }
+      if (t0 + t > s.last || (note >> (2 * sub + (i >> 3)) & 1u)) z[i] = -INFINITY;
     }
+  };
+  auto raise = [&](float top) {
+    top *= scale2;
+    if (__any(top > s.m + (kBias + kSlack))) {
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float to = fmaxf(s.m, top - kBias), by = __builtin_amdgcn_exp2f(s.m - to);
+      s.m = to;
+      s.l *= by;
+#pragma unroll
+      for (int db = 0; db < D / 32; ++db) s.o[db] *= by;
+    }
+  };
+  f32x16 z = zero;
+  __builtin_amdgcn_sched_barrier(0);
+  each([&](auto gi) {
+    product(gi, z);
+    if constexpr (decltype(gi)::value == 0) load();
+    __builtin_amdgcn_sched_barrier(0);
+  }, std::make_integer_sequence<int, kS>{});
+  if (masked) mask(z, 0);
+  {
+    float top = fmaxf(z[0], z[1]);
+#pragma unroll
+    for (int i = 2; i < 16; ++i) top = fmaxf(top, z[i]);
+    raise(top);
   }
-  float top = z[0];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
-  top *= scale2;
-  if (__any(top > s.m + (kBias + kSlack))) {
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const float to = fmaxf(s.m, top - kBias), by = __builtin_amdgcn_exp2f(s.m - to);
-    s.m = to;
-    s.l *= by;
+  for (int sub = 0; sub < kSubs; ++sub) {
+    const bool more = sub + 1 < kSubs;
+    f32x16 next = zero;
+    float sum[2] = {0.f, 0.f};
+    u32x4 p[2], v[kHalf];                              // p: rounded to the values' type: off by half a step of it, as the output is
+    auto value_at = [&](int x, int db) {
+      return *(const u32x4*)(tile.v + ((2 * sub + x) * kHalf + db) * 1024 + ((lane ^ (db & 1)) * 16));
+    };
+    if (more) keys = tile_keys<D>(tile, sub + 1, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    each([&](auto gi) {
+      constexpr int g = decltype(gi)::value;
+      if (more) product(gi, next);
 #pragma unroll
-    for (int db = 0; db < D / 32; ++db) s.o[db] *= by;
-  }
+      for (int i = 16 * g / kS; i < 16 * (g + 1) / kS; ++i) {
+        z[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i], scale2, -s.m));
+        sum[i & 1] += z[i];
+        if (i & 1) {
+          uint32_t w = pack2<T>(z[i - 1], z[i]);
+          pin(w);
+          p[i >> 3][(i >> 1) & 3] = w;
+        }
+      }
+      if constexpr (kS - 1 - g < kHalf) v[kS - 1 - g] = value_at(0, kS - 1 - g);
+      __builtin_amdgcn_sched_barrier(0);
+    }, std::make_integer_sequence<int, kS>{});
+    s.l += sum[0] + sum[1];
+    if (more && masked) mask(next, sub + 1);
+    if (!more) prepare();
+    float top = -INFINITY;
+    each([&](auto gi) {
+      constexpr int g = decltype(gi)::value, x = g / kHalf, db = g % kHalf, kE = 16 / kHalf;
+      s.o[db] = mfma32<T>(v[db], p[x], s.o[db]);
+      if constexpr (x == 0) v[db] = value_at(1, db);
+      else if (more) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i], scale2, -s.m));
-  if (masked) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = hidden >> i & 1u ? 0.f : z[i];       // a scale of 0 too
-  }
-  float sum[4] = {z[0], z[1], z[2], z[3]};
-#pragma unroll
-  for (int i = 4; i < 16; ++i) sum[i & 3] += z[i];
-  s.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-  // rounded to the values' type: off by half a step of it, as the output is
-  u32x4 p[2];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) p[j >> 2][j & 3] = pack2<T>(z[2 * j], z[2 * j + 1]);
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-#pragma unroll
-    for (int db = 0; db < D / 32; ++db) {
-      const u32x4 v = *(const u32x4*)(tile.v + ((2 * sub + x) * (D / 32) + db) * 1024 + ((lane ^ (db & 1)) * 16));
-      s.o[db] = mfma32<T>(v, p[x], s.o[db]);
+        for (int i = kE * db; i < kE * db + kE; ++i) top = fmaxf(top, next[i]);
+        pin(top);
+      }
+      if (!more) {
+        // kPutSteps * kUnits steps over the kG products
+        constexpr int kAll = kPutSteps * Tile<D>::kUnits;
+        each([&](auto k) { put(std::integral_constant<int, kAll * g / kG + decltype(k)::value>{}); },
+             std::make_integer_sequence<int, kAll * (g + 1) / kG - kAll * g / kG>{});
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }, std::make_integer_sequence<int, kG>{});
+    if (more) {
+      raise(top);
+      z = next;
     }
   }
 }
@@ -931,17 +1067,18 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, const Request& q) {
 
 // With fewer rows than the chip takes the tokens are split, kMinTiles to a part at least.
 constexpr uint32_t kMinTiles = 8;
+template <int D>
 __device__ __forceinline__ uint32_t parts_of(const Share& s, uint64_t total) {
-  const uint64_t parts = quotient((uint64_t)s.steps * kTileWgs, max(total, (uint64_t)1));
+  const uint64_t parts = quotient((uint64_t)s.steps * tile_slots(D), max(total, (uint64_t)1));
   return (uint32_t)max(min(parts, (uint64_t)(s.steps / kMinTiles)), (uint64_t)1);
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(kAThreads, D == 256 ? 1 : 2) void attn_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kernel(AttnArgs a) {
   constexpr int kTokens = Tile<D>::kTokens;
   __shared__ __align__(16) Tile<D> s_tile[2];
-  __shared__ uint64_t s_wave[kAWaves];
-  __shared__ uint32_t s_note[3], s_unit[4];
+  __shared__ uint64_t s_wave[kTileThreads / 64];
+  __shared__ uint32_t s_note[4], s_unit[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), R = a.n_requests;
   // which request's which part this workgroup has
   uint32_t bad = 0;
@@ -949,37 +1086,56 @@ __global__ __launch_bounds__(kAThreads, D == 256 ? 1 : 2) void attn_tile_kernel(
     if (r >= R) return Share{0, 0, 1};
     return share_of<D>(a, request(a, r, &bad));
   };
-  uint64_t total = 0, sum = 0;
-  for (int base = 0; base < R; base += kAThreads) {
-    const Share s = share(base + tid);
-    scan_add((uint64_t)s.tiles * s.steps * (uint32_t)a.kv_heads, s_wave, &sum);
-    total += sum;
-  }
-  if (bad && blockIdx.x == 0 && a.error) atomicOr(a.error, bad);
-  // requests that overlap may be more than the grid has workgroups for: then no rows are shared by several
-  if (__syncthreads_or((int)(bad & kErrCuQ))) total = ~0ull;
-  if (tid == 0) s_unit[0] = 0xFFFFFFFFu;
-  if (tid < 3) s_note[tid] = 0;
-  uint64_t units = 0, split = 0;
-  for (int base = 0; base < R; base += kAThreads) {
-    Share s = share(base + tid);
-    s.parts = parts_of(s, total);
-    const uint64_t mine = (uint64_t)s.tiles * (uint32_t)a.kv_heads * s.parts, shared = s.parts > 1 ? mine : 0;
-    const uint64_t upto = units + scan_add(mine, s_wave, &sum);
-    units += sum;
-    const uint64_t slots = split + scan_add(shared, s_wave, &sum);
-    split += sum;
-    if (blockIdx.x < upto && blockIdx.x >= upto - mine) {
-      s_unit[0] = (uint32_t)(base + tid);
-      s_unit[1] = (uint32_t)(blockIdx.x - (upto - mine));
-      s_unit[2] = (uint32_t)(slots - shared);
-      s_unit[3] = s.parts;
+  if (tid < 4) s_note[tid] = 0;
+  int r;
+  uint32_t unit, slots0, parts;
+  if (R <= 64) {                                       // every wave for itself
+    Share s = share(lane);
+    if (bad && blockIdx.x == 0 && wave == 0 && a.error) atomicOr(a.error, bad);
+    uint64_t total = of_lane(wave_scan_add((uint64_t)s.tiles * s.steps * (uint32_t)a.kv_heads), 63);
+    // requests that overlap may be more than the grid has workgroups for: then no rows are shared by several
+    if (__any(bad & kErrCuQ)) total = 1ull << 60;
+    s.parts = parts_of<D>(s, total);
+    const uint64_t mine = (uint64_t)s.tiles * (uint32_t)a.kv_heads * s.parts, upto = wave_scan_add(mine);
+    const uint64_t shared = s.parts > 1 ? mine : 0, slots = wave_scan_add(shared);
+    const uint64_t here = __ballot(blockIdx.x < upto && blockIdx.x >= upto - mine);
+    if (!here) return;
+    r = (int)__builtin_ctzll(here);
+    unit = (uint32_t)(blockIdx.x - of_lane(upto - mine, r));
+    slots0 = (uint32_t)of_lane(slots - shared, r);
+    parts = (uint32_t)__builtin_amdgcn_readlane((int)s.parts, r);
+    __syncthreads();
+  } else {
+    uint64_t total = 0, sum = 0;
+    for (int base = 0; base < R; base += kTileThreads) {
+      const Share s = share(base + tid);
+      scan_add<kTileThreads / 64>((uint64_t)s.tiles * s.steps * (uint32_t)a.kv_heads, s_wave, &sum);
+      total += sum;
     }
+    if (bad && blockIdx.x == 0 && a.error) atomicOr(a.error, bad);
+    if (__syncthreads_or((int)(bad & kErrCuQ))) total = 1ull << 60;
+    if (tid == 0) s_unit[0] = 0xFFFFFFFFu;
+    uint64_t units = 0, split = 0;
+    for (int base = 0; base < R; base += kTileThreads) {
+      Share s = share(base + tid);
+      s.parts = parts_of<D>(s, total);
+      const uint64_t mine = (uint64_t)s.tiles * (uint32_t)a.kv_heads * s.parts, shared = s.parts > 1 ? mine : 0;
+      const uint64_t upto = units + scan_add<kTileThreads / 64>(mine, s_wave, &sum);
+      units += sum;
+      const uint64_t slots = split + scan_add<kTileThreads / 64>(shared, s_wave, &sum);
+      split += sum;
+      if (blockIdx.x < upto && blockIdx.x >= upto - mine) {
+        s_unit[0] = (uint32_t)(base + tid);
+        s_unit[1] = (uint32_t)(blockIdx.x - (upto - mine));
+        s_unit[2] = (uint32_t)(slots - shared);
+        s_unit[3] = s.parts;
+      }
+    }
+    __syncthreads();
+    if (s_unit[0] == 0xFFFFFFFFu) return;
+    r = __builtin_amdgcn_readfirstlane((int)s_unit[0]);
+    unit = s_unit[1], slots0 = s_unit[2], parts = s_unit[3];
   }
-  __syncthreads();
-  if (s_unit[0] == 0xFFFFFFFFu) return;
-  const int r = __builtin_amdgcn_readfirstlane((int)s_unit[0]);
-  const uint32_t unit = s_unit[1], parts = s_unit[3];
   const Request rq = request(a, r, &bad);
   const int kh = (int)(unit % (uint32_t)a.kv_heads), part = (int)(unit / (uint32_t)a.kv_heads % parts);
   const int n_tiles = (int)share_of<D>(a, rq).tiles;
@@ -992,7 +1148,7 @@ __global__ __launch_bounds__(kAThreads, D == 256 ? 1 : 2) void attn_tile_kernel(
   const int all = (end + kTokens - 1) / kTokens;
   const int j0 = (int)((int64_t)all * part / parts), j1 = (int)((int64_t)all * (part + 1) / parts);
 
-  TileRows<D> s;
+  TileRows<T, D> s;
   const int row = row0 + 32 * wave + (lane & 31), i = row / a.group, h = lane >> 5;
   const int wave_first = __builtin_amdgcn_readfirstlane(max(rq.kv - rq.n + (row0 + 32 * wave) / a.group, -1));
   const int wave_last =
@@ -1007,39 +1163,66 @@ __global__ __launch_bounds__(kAThreads, D == 256 ? 1 : 2) void attn_tile_kernel(
   {
     const uint16_t* q = a.q + (int64_t)(rq.q0 + min(i, rq.n - 1)) * a.q_ts + (int64_t)(kh * a.group + row % a.group) * a.q_hs;
 #pragma unroll
-    for (int kb = 0; kb < D / 64; ++kb) s.qs[kb] = split_query<T>(q + 64 * kb + 32 * h, a.flip, s.q[kb]);
+    for (int kb = 0; kb < D / 64; ++kb) s.qs[kb] = split_query<T>(a, q + 64 * kb + 32 * h, s.q[kb]);
   }
-  auto block_at = [&](int j) {                         // of the thread's 16 tokens in tile j
-    const int t = j * kTokens + 16 * (tid / (D / 2));
-    return j < j1 && t < end ? table[t >> a.shift] : -1;
+  constexpr int kUnits = Tile<D>::kUnits;
+  auto blocks_at = [&](int j, Blocks<D> (&b)[kUnits]) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+      for (int x = 0; x < (D == 64 ? 2 : 1); ++x) {
+        const int t = j * kTokens + 16 * ((64 * wave + u * kTileThreads) / (D / 2) + x);
+        // always read: a wait at the end of a branch would be for the tile's loads too
+        const int32_t held = table[min(t, end - 1) >> a.shift];
+        b[u].b[x] = t < end ? held : -1;
+      }
   };
-  Fetch<D> f;
-  auto store = [&](int j) {
+  Fetch<D> f[kUnits];
+  auto load = [&](int j, const Blocks<D> (&b)[kUnits]) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) fetch<D>(f[u], a, b[u], kh, j * kTokens, tid + u * kTileThreads);
+  };
+  uint32_t sc[kUnits][4];
+  auto prepare = [&](int j) {
     const int t0 = j * kTokens;
-    uint32_t note = put_tile<T, D>(s_tile[j & 1], f, t0, end, t0 + kTokens - 1 > first, tid);
-    if (note) {
-      if ((note & 255u) && t0 + 16 * (tid / (D / 2)) < end && a.error) atomicOr(a.error, kErrBlock);
-      atomicOr(&s_note[j % 3], note);
+    uint32_t note = 0;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int unit = tid + u * kTileThreads;
+      note |= prepare_values<D>(f[u], sc[u], t0, end, t0 + kTokens - 1 > first, unit);
+      if (!f[u].ok && t0 + 16 * (unit / (D / 2)) < end && a.error) atomicOr(a.error, kErrBlock);
     }
+    if (note) atomicOr(&s_note[j & 3], note);
+  };
+  auto put = [&](auto step, int j) {
+    constexpr int u = decltype(step)::value / kPutSteps;
+    put_tile<decltype(step)::value % kPutSteps, T, D>(s_tile[j & 1], f[u], sc[u], tid + u * kTileThreads);
+  };
+  auto put_all = [&](int j) {
+    each([&](auto step) { put(step, j); }, std::make_integer_sequence<int, kPutSteps * kUnits>{});
   };
   if (j0 < j1) {
-    fetch<D>(f, a, block_at(j0), kh, j0 * kTokens, tid);
-    int32_t next = block_at(j0 + 1);
-    store(j0);
+    Blocks<D> next[kUnits];
+    blocks_at(j0, next);
+    load(j0, next);
+    blocks_at(j0 + 1, next);
+    prepare(j0);
+    put_all(j0);
     __syncthreads();
     for (int j = j0; j < j1; ++j) {
       const int t0 = j * kTokens;
-      // the next tile is read while this one is worked on
-      if (j + 1 < j1) fetch<D>(f, a, next, kh, t0 + kTokens, tid);
-      next = block_at(j + 2);
-      const uint32_t note = s_note[j % 3];
-      if (tid == 0) s_note[(j + 2) % 3] = 0;
-      const bool masked = t0 + kTokens - 1 > wave_first || (note & 255u);
-#pragma unroll
-      for (int sub = 0; sub < kTokens / 32; ++sub)
-        if (t0 + 32 * sub <= wave_last) tile_step<T, D>(s, s_tile[j & 1], sub, t0, masked, note, a.scale2, lane);
-      if (note & 256u) tile_nan_values<D>(s, a, table, kh, t0, end);
-      if (j + 1 < j1) store(j + 1);
+      const uint32_t note = __builtin_amdgcn_readfirstlane(s_note[j & 3]);
+      if (tid == 0) s_note[(j + 2) & 3] = 0;
+      const bool masked = t0 + kTokens - 1 > wave_first || note;
+      // the next tile is read and converted while this one is worked on; past the last, the last again
+      const int jn = min(j + 1, j1 - 1);
+      tile_products<T, D>(s, s_tile[j & 1], t0, masked, note, a.scale2, lane,
+                          [&] {
+                            load(jn, next);
+                            blocks_at(j + 2, next);
+                          },
+                          [&] { prepare(jn); }, [&](auto step) { put(step, j + 1); });
+      if (note & kNoteNaN) tile_nan_values<T, D>(s, a, table, kh, t0, end);
       __syncthreads();
     }
   }
@@ -1065,7 +1248,7 @@ __global__ __launch_bounds__(kAThreads, D == 256 ? 1 : 2) void attn_tile_kernel(
     return;
   }
   const uint32_t item = unit / (uint32_t)a.kv_heads / parts * (uint32_t)a.kv_heads + (uint32_t)kh;
-  const uint32_t slot0 = s_unit[2] + item * parts;
+  const uint32_t slot0 = slots0 + item * parts;
   float* p0 = a.parts + (int64_t)slot0 * kPart<D, kTileRows>;
   if (valid) {
     float* mine = p0 + (int64_t)part * kPart<D, kTileRows>;
@@ -1079,8 +1262,8 @@ __global__ __launch_bounds__(kAThreads, D == 256 ? 1 : 2) void attn_tile_kernel(
       }
     if (h == 0) put2(mine + kTileRows * D + 2 * (row - row0), s.m, s.l);
   }
-  join<T, D, kTileRows, 8>(a, [&](int p) { return p0 + (int64_t)p * kPart<D, kTileRows>; }, part, (int)parts,
-                           a.counters + kLevels * kFewCounters + slot0, kTileWgs, (float*)&s_tile[0], &s_unit[0], kh, rq,
+  join<T, D, kTileRows, 8, kTileThreads>(a, [&](int p) { return p0 + (int64_t)p * kPart<D, kTileRows>; }, part, (int)parts,
+                           a.counters + kLevels * kFewCounters + slot0, tile_slots(64), (float*)&s_tile[0], &s_unit[0], kh, rq,
                            row0, nr);
 }
 
@@ -1090,8 +1273,8 @@ __global__ __launch_bounds__(kAThreads, D == 256 ? 1 : 2) void attn_tile_kernel(
 constexpr int few_wgs(int32_t head_dim) { return 256 * few_waves(head_dim); }
 
 // The tile kernel's workgroups at most: 128 rows each, the last of a request fewer, and those that split the tokens.
-int64_t tile_units(int64_t n_requests, int64_t rows, int64_t kv_heads) {
-  return (rows / kTileRows + std::min(n_requests, rows / (kFewRows + 1))) * kv_heads + kTileWgs;
+int64_t tile_wgs(int64_t n_requests, int64_t rows, int64_t kv_heads, int32_t dim) {
+  return (rows / kTileRows + std::min(n_requests, rows / (kFewRows + 1))) * kv_heads + tile_slots(dim);
 }
 
 template <typename T, int D>
@@ -1106,8 +1289,8 @@ void launch_attn(const AttnArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((attn_few_kernel<T, D>), dim3((unsigned)grid), dim3(kAThreads), 0, s, a);
   }
   if (a.cu_q ? rows > kFewRows : a.group > kFewRows)
-    hipLaunchKernelGGL((attn_tile_kernel<T, D>), dim3((unsigned)tile_units(a.n_requests, rows, a.kv_heads)),
-                       dim3(kAThreads), 0, s, a);
+    hipLaunchKernelGGL((attn_tile_kernel<T, D>), dim3((unsigned)tile_wgs(a.n_requests, rows, a.kv_heads, D)),
+                       dim3(kTileThreads), 0, s, a);
 }
 
 template <typename T>
@@ -1130,7 +1313,7 @@ size_t sbm_attention_kv4_workspace_bytes(int32_t n_requests, int32_t n_tokens, i
       !kv_shape_ok(16, head_dim))
     return 0;
   // the two kernels run one after the other
-  const size_t row = (size_t)head_dim + 2, few = 16 * row * 2 * few_wgs(head_dim), tile = kTileRows * row * kTileWgs;
+  const size_t row = (size_t)head_dim + 2, few = 16 * row * 2 * few_wgs(head_dim), tile = (size_t)kTileRows * row * tile_slots(head_dim);
   return sizeof(uint32_t) * kCounters + sizeof(float) * std::max(few, tile);
 }
 
@@ -1150,7 +1333,8 @@ int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks
   if ((int64_t)table_width * block_size > 0x7FFFFF00)
     return fail(SBM_ERANGE, "%d blocks of %d tokens in one request", table_width, block_size);
   if ((int64_t)n_tokens * (n_heads / n_kv_heads) > 0x7FFFFF00) return fail(SBM_ERANGE, "too many rows");
-  if (tile_units(n_requests, (int64_t)n_tokens * (n_heads / n_kv_heads), n_kv_heads) > (1 << 23))
+  if ((int64_t)n_blocks * n_kv_heads > 0x7FFFFFFF) return fail(SBM_ERANGE, "%d blocks of %d heads", n_blocks, n_kv_heads);
+  if (tile_wgs(n_requests, (int64_t)n_tokens * (n_heads / n_kv_heads), n_kv_heads, head_dim) > (1 << 22))
     return fail(SBM_ERANGE, "too many rows");
   if (!cu_q && n_tokens != n_requests)
     return fail(SBM_EINVAL, "without cu_q each request has one token: n_tokens=%d, n_requests=%d", n_tokens, n_requests);
@@ -1164,8 +1348,8 @@ int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks
   const size_t need = sbm_attention_kv4_workspace_bytes(n_requests, n_tokens, n_heads, n_kv_heads, head_dim);
   if (workspace_bytes < need) return fail(SBM_ENOSPACE, "workspace %zu < %zu bytes", workspace_bytes, need);
   AttnArgs a{(const uint16_t*)q->data, q->token_stride, q->head_stride, cache, block_table, kv_lens, cu_q, out, lse,
-             error, (uint32_t*)workspace, (float*)((uint32_t*)workspace + kCounters), fabsf(scale) * 1.44269504088896341f,
-             scale < 0.f ? 0x80008000u : 0u, n_blocks, __builtin_ctz((unsigned)block_size), table_width,
+             error, (uint32_t*)workspace, (float*)((uint32_t*)workspace + kCounters),
+             scale == 0.f ? 1.f : fabsf(scale) * 1.44269504088896341f, scale < 0.f ? 0x80008000u : 0u, scale == 0.f, n_blocks, __builtin_ctz((unsigned)block_size), table_width,
              n_requests, n_tokens, n_heads, n_kv_heads, n_heads / n_kv_heads};
   if (flags & SBM_F_IN_BF16) launch_attn<__bf16>(a, head_dim, (hipStream_t)stream);
   else launch_attn<_Float16>(a, head_dim, (hipStream_t)stream);
