@@ -196,9 +196,15 @@ __device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
   return (a | b) >> 32 ? a / b : (uint64_t)((uint32_t)a / (uint32_t)b);
 }
 
+// f(0), f(1), ... as constants; a bool f ends it with false.
 template <typename F, int... kI>
-__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, kI...>) {
-  (f(std::integral_constant<int, kI>{}), ...);
+__device__ __forceinline__ bool each(F&& f, std::integer_sequence<int, kI...>) {
+  if constexpr (std::is_same_v<decltype(f(std::integral_constant<int, 0>{})), bool>) {
+    return (f(std::integral_constant<int, kI>{}) && ...);
+  } else {
+    (f(std::integral_constant<int, kI>{}), ...);
+    return true;
+  }
 }
 
 // Keeps a value where it is computed.
@@ -218,7 +224,8 @@ __device__ __forceinline__ Pages pages(const AttnArgs& a, const int32_t* table, 
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int t = __builtin_amdgcn_readfirstlane(t0 + 16 * x);
-    p.b[x] = t < end ? held[t >> a.shift] : -1;
+    const int32_t b = held[min(t, end - 1) >> a.shift];
+    p.b[x] = t < end ? b : -1;
   }
   return p;
 }
@@ -633,26 +640,29 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
       const int stop_t = min(end, s1 * kStep);
       int t0 = s0 * kStep + 32 * wave;
       if (t0 < stop_t) {
+        // The tokens after these are read while these are worked on.  Past the last the reads go on (to block 0, which
+        // is in the caches by then): a wait counts what was issued since, so that has to be the same on every way.
         constexpr int kRing = few_ring(D);
         Raw<D> raw[kRing];
-        Pages next = pages(a, table, t0, end);
+        Pages next = pages(a, table, t0, stop_t);
         each([&](auto i) {
           constexpr int x = decltype(i)::value;
-          if (x == 0 || t0 + x * kStep < stop_t) load_tokens<D>(raw[x], a, next, kh, t0 + x * kStep, lane);
-          next = pages(a, table, t0 + (x + 1) * kStep, end);
+          load_tokens<D>(raw[x], a, next, kh, t0 + x * kStep, lane);
+          next = pages(a, table, t0 + (x + 1) * kStep, stop_t);
+          return true;
         }, std::make_integer_sequence<int, kRing>{});
         bool hole = false;
-        // the tokens after these are read while these are worked on
         auto turn = [&](auto i) {
           Raw<D>& r = raw[decltype(i)::value];
-          if (t0 >= stop_t) return;
-          hole |= !r.ok[0] || (!r.ok[1] && t0 + 16 < end);
+          hole |= !r.ok[0] || (!r.ok[1] && t0 + 16 < stop_t);
           step<T, D>(s, r, a, table, kh, t0, end, first, lane);
-          if (t0 + kRing * kStep < stop_t) load_tokens<D>(r, a, next, kh, t0 + kRing * kStep, lane);
-          next = pages(a, table, t0 + (kRing + 1) * kStep, end);
+          load_tokens<D>(r, a, next, kh, t0 + kRing * kStep, lane);
+          next = pages(a, table, t0 + (kRing + 1) * kStep, stop_t);
           t0 += kStep;
+          return t0 < stop_t;
         };
-        while (t0 < stop_t) each(turn, std::make_integer_sequence<int, kRing>{});
+        while (each(turn, std::make_integer_sequence<int, kRing>{})) {
+        }
         if (hole && lane == 0 && a.error) atomicOr(a.error, kErrBlock);
       }
     }
