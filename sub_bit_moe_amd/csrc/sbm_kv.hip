@@ -164,6 +164,7 @@ struct QkArgs {
   uint32_t* error;
   double eps;
   int32_t rope_rows, rot, n_tokens, heads, kv_heads, n_blocks, shift, neighbours;
+  int32_t per_token;     // log2 of the groups of lanes that a token has in a workgroup
 };
 
 template <typename T>
@@ -208,48 +209,93 @@ __device__ __forceinline__ uint16_t round_once(double y) {
   return round_once<T>((float)__builtin_bit_cast(double, b));
 }
 
-// Norm and rotation of the eight elements from d0 of one head; C: the type it is computed in.
-template <typename T, typename C, int D, bool kVec>
-__device__ __forceinline__ void norm_rope8(const uint16_t* head, const uint16_t* w, const float* rope, int d0,
-                                           const QkArgs& a, uint16_t* out) {
-  constexpr int L = D / 8;
-  uint16_t raw[8], other[8], wr[8], wo[8];
-  load8<kVec>(head + d0, raw);
-  const int half = a.rot >> 1;
-  const bool turn = d0 < a.rot, split = turn && !a.neighbours;
-  const int p0 = d0 < half ? d0 + half : d0 - half;         // the partners' dimensions
-  if (split) load8<kVec>(head + p0, other);
+// v summed over groups of kL lanes, in all of them.
+template <int kCtrl>
+__device__ __forceinline__ float other_lane(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), kCtrl, 0xF, 0xF, true));
+}
+template <int kCtrl>
+__device__ __forceinline__ double other_lane(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <int kL, typename C>
+__device__ __forceinline__ C group_sum(C v) {
+  v += other_lane<0xB1>(v);                        // neighbours, neighbouring pairs, mirrored eights and sixteens
+  v += other_lane<0x4E>(v);
+  v += other_lane<0x141>(v);
+  if constexpr (kL > 8) v += other_lane<0x140>(v);
+  if constexpr (kL > 16) v += __shfl_xor(v, 16, 64);
+  return v;
+}
+
+// 1 / sqrt(x): the hardware's estimate and one step of third order (2^-23 to below 2^-60).
+__device__ __forceinline__ double inverse_root(double x) {
+  const double y = __builtin_amdgcn_rsq(x), e = __builtin_fma(-x * y, y, 1.0);
+  const double z = __builtin_fma(y * e, __builtin_fma(e, 0.375, 0.5), y);
+  return x == 0. || x == (double)INFINITY ? y : z;
+}
+__device__ __forceinline__ float inverse_root(float x) {
+  if (!(x > 1e-30f && x < 1e30f)) return 1.f / sqrtf(x);
+  const float y = __builtin_amdgcn_rsqf(x), e = __builtin_fmaf(-x * y, y, 1.f);
+  return __builtin_fmaf(y * e, 0.5f, y);
+}
+
+// What a lane keeps of its token and its eight dimensions for all the heads it takes.
+struct QkLane {
+  float cos[8], sin[8];
+  int d0, p0;                // its first dimension, and that of the partners (halves)
+  bool turn, split, low;     // rotated; with partners eight apart or more; those are the higher ones
+};
+
+// Eight weights, and their partners'.
+struct QkWeights {
+  uint16_t w[8], other[8];
+};
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void load_weights(QkWeights& q, const uint16_t* w, const QkLane& l) {
+  constexpr uint16_t kOne = __is_same(T, __bf16) ? 0x3F80 : 0x3C00;
+  if (w) {
+    load8<kVec>(w + l.d0, q.w);
+    load8<kVec>(w + l.p0, q.other);
+  } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) wr[j] = w ? w[d0 + j] : 0;
-  if (split) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) wo[j] = w ? w[p0 + j] : 0;
+    for (int j = 0; j < 8; ++j) q.w[j] = q.other[j] = kOne;
   }
+}
+
+// Norm and rotation of a lane's eight elements of one head; C: the type it is computed in.
+template <typename T, typename C, int D, bool kVec>
+__device__ __forceinline__ void norm_rope8(const uint16_t* head, const QkWeights& w, const QkLane& l, const QkArgs& a,
+                                           uint16_t* out) {
+  uint16_t raw[8], other[8];
+  load8<kVec>(head + l.d0, raw);
+  if (l.split) load8<kVec>(head + l.p0, other);
   C ss = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const C x = (C)to_f32<T>(raw[j]);
     ss += x * x;
   }
-#pragma unroll
-  for (int m = 1; m < L; m <<= 1) ss += __shfl_xor(ss, m, 64);
-  const C inv = (C)1 / sqrt(ss / (C)D + (C)a.eps);
+  ss = group_sum<D / 8>(ss);
+  const C inv = inverse_root(ss * ((C)1 / (C)D) + (C)a.eps);
   C y[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = (C)to_f32<T>(raw[j]) * inv * (w ? (C)to_f32<T>(wr[j]) : (C)1);
-  if (split) {
-    const float* cs = rope + (d0 < half ? d0 : d0 - half);
+  for (int j = 0; j < 8; ++j) y[j] = (C)to_f32<T>(raw[j]) * inv * (C)to_f32<T>(w.w[j]);
+  if (l.split) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const C z = (C)to_f32<T>(other[j]) * inv * (w ? (C)to_f32<T>(wo[j]) : (C)1);
-      const C c = (C)cs[j], s = (C)cs[half + j];
-      y[j] = d0 < half ? y[j] * c - z * s : y[j] * c + z * s;
+      const C z = (C)to_f32<T>(other[j]) * inv * (C)to_f32<T>(w.other[j]);
+      const C c = (C)l.cos[j], s = (C)l.sin[j];
+      y[j] = l.low ? y[j] * c - z * s : y[j] * c + z * s;
     }
-  } else if (turn) {
-    const float* cs = rope + (d0 >> 1);
+  } else if (l.turn) {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      const C c = (C)cs[j >> 1], s = (C)cs[half + (j >> 1)];
+      const C c = (C)l.cos[j >> 1], s = (C)l.sin[j >> 1];
       const C u = y[j], v = y[j + 1];
       y[j] = u * c - v * s;
       y[j + 1] = v * c + u * s;
@@ -291,16 +337,26 @@ __device__ __forceinline__ uint32_t quantise8(const uint16_t* x, uint32_t* scale
   return codes;
 }
 
-// D / 8 lanes hold a head (16-byte accesses), a wave 512 / D heads of a token.
-// Bound by HBM for prompts, by latency for a few tokens.
+// D / 8 lanes hold a head (16-byte accesses) and take every so-manieth head of one token, so that its cosines and sines
+// and the weights are read once for all of them.  Bound by HBM for prompts, by latency for a few tokens (whose heads are
+// shared out over gridDim.y).
 template <typename T, int D, bool kVec>
 __global__ __launch_bounds__(kQThreads) void qk_kernel(QkArgs a) {
-  constexpr int L = D / 8;
-  const uint32_t per_token = (uint32_t)(a.heads + a.kv_heads + (a.cache ? a.kv_heads : 0));
-  const uint32_t unit = blockIdx.x * (kQThreads / L) + threadIdx.x / L;
-  const uint32_t t = unit / per_token, h = unit - t * per_token;
-  if (t >= (uint32_t)a.n_tokens) return;
-  const int d0 = (int)(threadIdx.x % L) * 8;
+  constexpr int L = D / 8, kGroups = kQThreads / L;
+  const uint32_t group = threadIdx.x / L;
+  const uint32_t t = blockIdx.x * ((uint32_t)kGroups >> a.per_token) + (group >> a.per_token);
+  uint32_t h = (group & ((1u << a.per_token) - 1u)) + (blockIdx.y << a.per_token);
+  const uint32_t step = gridDim.y << a.per_token;
+  const uint32_t heads = (uint32_t)a.heads, kv_heads = (uint32_t)a.kv_heads;
+  const uint32_t all = heads + kv_heads + (a.cache ? kv_heads : 0);
+  if (t >= (uint32_t)a.n_tokens || h >= all) return;
+  QkLane l;
+  l.d0 = (int)(threadIdx.x % L) * 8;
+  const int half = a.rot >> 1;
+  l.turn = l.d0 < a.rot;
+  l.split = l.turn && !a.neighbours;
+  l.low = l.d0 < half;
+  l.p0 = !l.split ? l.d0 : l.low ? l.d0 + half : l.d0 - half;
   const float* rope = a.rope;
   bool ok = true;
   if (a.rot) {
@@ -312,36 +368,60 @@ __global__ __launch_bounds__(kQThreads) void qk_kernel(QkArgs a) {
   if (a.cache) {
     slot = a.slots[t];
     if (slot >= ((int64_t)a.n_blocks << a.shift)) {
-      if (h == 0 && d0 == 0 && a.error) atomicAdd(a.error, 1u);
+      if (h == 0 && l.d0 == 0 && a.error) atomicAdd(a.error, 1u);
       slot = -1;
     }
   }
   if (!ok) {
-    if (h == 0 && d0 == 0 && a.error) atomicAdd(a.error, 1u);
+    if (h == 0 && l.d0 == 0 && a.error) atomicAdd(a.error, 1u);
     return;
+  }
+  if (l.turn) {
+    // neighbours: four of each
+    const float* cs = rope + (a.neighbours ? l.d0 >> 1 : l.low ? l.d0 : l.d0 - half);
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      if (j && a.neighbours) break;
+      if constexpr (kVec) {
+        const float4 c = *(const float4*)(cs + j), s = *(const float4*)(cs + half + j);
+        l.cos[j] = c.x, l.cos[j + 1] = c.y, l.cos[j + 2] = c.z, l.cos[j + 3] = c.w;
+        l.sin[j] = s.x, l.sin[j + 1] = s.y, l.sin[j + 2] = s.z, l.sin[j + 3] = s.w;
+      } else {
+#pragma unroll
+        for (int k = j; k < j + 4; ++k) l.cos[k] = cs[k], l.sin[k] = cs[half + k];
+      }
+    }
   }
   uint16_t y[8];
-  if (h < (uint32_t)a.heads) {
-    norm_rope8<T, float, D, kVec>(a.q + t * a.q_ts + h * a.q_hs, a.qw, rope, d0, a, y);
-    store8<kVec>(a.q_out + t * a.qo_ts + h * a.qo_hs + d0, y);
-    return;
+  if (h < heads) {
+    QkWeights w;
+    load_weights<T, kVec>(w, a.qw, l);
+    for (; h < heads; h += step) {
+      norm_rope8<T, float, D, kVec>(a.q + t * a.q_ts + h * a.q_hs, w, l, a, y);
+      store8<kVec>(a.q_out + t * a.qo_ts + h * a.qo_hs + l.d0, y);
+    }
   }
-  const uint32_t kh = (h - (uint32_t)a.heads) % (uint32_t)a.kv_heads;
-  const bool is_v = h >= (uint32_t)(a.heads + a.kv_heads);
-  if (is_v) {
-    if (slot < 0) return;
-    load8<kVec>(a.v + t * a.v_ts + kh * a.v_hs + d0, y);
-  } else {
-    norm_rope8<T, double, D, kVec>(a.k + t * a.k_ts + kh * a.k_hs, a.kw, rope, d0, a, y);
-    if (a.k_out) store8<kVec>(a.k_out + t * a.ko_ts + kh * a.ko_hs + d0, y);
-    if (slot < 0) return;
-  }
-  uint32_t scale;
-  const uint32_t codes = quantise8<T>(y, &scale);
+  if (h >= all) return;
+  QkWeights w;
+  load_weights<T, kVec>(w, a.kw, l);
   const int64_t bs = 1ll << a.shift, row = slot & (bs - 1);
-  uint8_t* rec = a.cache + ((slot >> a.shift) * a.kv_heads + kh) * kv_record_bytes((int32_t)bs, D);
-  *(uint32_t*)(rec + (is_v ? bs * (D / 2) : 0) + row * (D / 2) + d0 / 2) = codes;
-  if ((d0 & 31) == 0) rec[bs * D + (is_v ? bs * (D / 32) : 0) + row * (D / 32) + d0 / 32] = (uint8_t)scale;
+  for (; h < all; h += step) {
+    const bool is_v = h >= heads + kv_heads;
+    const uint32_t kh = h - heads - (is_v ? kv_heads : 0);
+    if (is_v) {
+      if (slot < 0) return;
+      load8<kVec>(a.v + t * a.v_ts + kh * a.v_hs + l.d0, y);
+    } else {
+      norm_rope8<T, double, D, kVec>(a.k + t * a.k_ts + kh * a.k_hs, w, l, a, y);
+      if (a.k_out) store8<kVec>(a.k_out + t * a.ko_ts + kh * a.ko_hs + l.d0, y);
+      if (slot < 0) continue;
+    }
+    uint32_t scale;
+    const uint32_t codes = quantise8<T>(y, &scale);
+    uint8_t* rec = a.cache + ((slot >> a.shift) * a.kv_heads + kh) * kv_record_bytes((int32_t)bs, D);
+    *(uint32_t*)(rec + (is_v ? bs * (D / 2) : 0) + row * (D / 2) + l.d0 / 2) = codes;
+    if ((l.d0 & 31) == 0) rec[bs * D + (is_v ? bs * (D / 32) : 0) + row * (D / 32) + l.d0 / 32] = (uint8_t)scale;
+  }
 }
 
 // ------------------------------------------------------------------ the cache's reader
@@ -382,11 +462,20 @@ bool vec_ok(const void* p, int64_t ts, int64_t hs) {
   return !p || (((uintptr_t)p & 15u) == 0 && ts % 8 == 0 && hs % 8 == 0);
 }
 
+// Workgroups that fill the chip: with fewer tokens their heads are shared out.
+constexpr int64_t kQFull = 1024;
+
 template <typename T, int D>
-void launch_qk(const QkArgs& a, bool vec, hipStream_t s) {
-  constexpr int L = D / 8, U = kQThreads / L;
-  const int64_t units = (int64_t)a.n_tokens * (a.heads + a.kv_heads + (a.cache ? a.kv_heads : 0));
-  const dim3 grid((unsigned)((units + U - 1) / U));
+void launch_qk(QkArgs a, bool vec, hipStream_t s) {
+  constexpr int kGroups = kQThreads / (D / 8);
+  const int64_t all = a.heads + a.kv_heads + (a.cache ? a.kv_heads : 0);
+  // as many groups of lanes for a token as it has heads, a workgroup's at most
+  a.per_token = 0;
+  while ((1 << a.per_token) < kGroups && (1 << a.per_token) < all) ++a.per_token;
+  const int64_t tokens = kGroups >> a.per_token, x = (a.n_tokens + tokens - 1) / tokens;
+  const int64_t rounds = (all + (1 << a.per_token) - 1) >> a.per_token;
+  const int64_t y = std::min<int64_t>(std::min<int64_t>(rounds, std::max<int64_t>(kQFull / x, 1)), 65535);
+  const dim3 grid((unsigned)x, (unsigned)y);
   if (vec) hipLaunchKernelGGL((qk_kernel<T, D, true>), grid, dim3(kQThreads), 0, s, a);
   else hipLaunchKernelGGL((qk_kernel<T, D, false>), grid, dim3(kQThreads), 0, s, a);
 }
@@ -472,8 +561,8 @@ int sbm_qk_norm_rope(const sbm_heads* q, const sbm_heads* k, const sbm_heads* v,
            (uint16_t*)q_out->data, (uint16_t*)ko.data, q_out->token_stride, q_out->head_stride, ko.token_stride,
            ko.head_stride, positions, rope, slots, cache, error, eps, rope_rows, rot_dim, n_tokens, n_heads,
            n_kv_heads, n_blocks, cache ? __builtin_ctz((unsigned)block_size) : 0,
-           (flags & SBM_F_NEIGHBOURS) ? 1 : 0};
-  bool vec = true;
+           (flags & SBM_F_NEIGHBOURS) ? 1 : 0, 0};
+  bool vec = (((uintptr_t)rope | (uintptr_t)q_weight | (uintptr_t)k_weight) & 15u) == 0;
   for (const sbm_heads* p : {q, k, (const sbm_heads*)&vv, q_out, (const sbm_heads*)&ko})
     vec = vec && vec_ok(p->data, p->token_stride, p->head_stride);
   hipStream_t s = (hipStream_t)stream;
