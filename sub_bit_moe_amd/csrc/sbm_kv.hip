@@ -269,11 +269,8 @@ __device__ __forceinline__ void load_weights(QkWeights& q, const uint16_t* w, co
 
 // Norm and rotation of a lane's eight elements of one head; C: the type it is computed in.
 template <typename T, typename C, int D, bool kVec>
-__device__ __forceinline__ void norm_rope8(const uint16_t* head, const QkWeights& w, const QkLane& l, const QkArgs& a,
-                                           uint16_t* out) {
-  uint16_t raw[8], other[8];
-  load8<kVec>(head + l.d0, raw);
-  if (l.split) load8<kVec>(head + l.p0, other);
+__device__ __forceinline__ void norm_rope8(const uint16_t* raw, const uint16_t* other, const QkWeights& w, const QkLane& l,
+                                           const QkArgs& a, uint16_t* out) {
   C ss = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -341,7 +338,7 @@ __device__ __forceinline__ uint32_t quantise8(const uint16_t* x, uint32_t* scale
 // and the weights are read once for all of them.  Bound by HBM for prompts, by latency for a few tokens (whose heads are
 // shared out over gridDim.y).
 template <typename T, int D, bool kVec>
-__global__ __launch_bounds__(kQThreads) void qk_kernel(QkArgs a) {
+__global__ __launch_bounds__(kQThreads, 4) void qk_kernel(QkArgs a) {
   constexpr int L = D / 8, kGroups = kQThreads / L;
   const uint32_t group = threadIdx.x / L;
   const uint32_t t = blockIdx.x * ((uint32_t)kGroups >> a.per_token) + (group >> a.per_token);
@@ -396,10 +393,25 @@ __global__ __launch_bounds__(kQThreads) void qk_kernel(QkArgs a) {
   if (h < heads) {
     QkWeights w;
     load_weights<T, kVec>(w, a.qw, l);
-    for (; h < heads; h += step) {
-      norm_rope8<T, float, D, kVec>(a.q + t * a.q_ts + h * a.q_hs, w, l, a, y);
-      store8<kVec>(a.q_out + t * a.qo_ts + h * a.qo_hs + l.d0, y);
+    // kAhead heads are read together
+    constexpr int kAhead = 2;
+    for (; h < heads; h += kAhead * step) {
+      uint16_t raw[kAhead][8], other[kAhead][8];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const uint32_t at = h + i * step < heads ? h + i * step : h;
+        const uint16_t* q = a.q + t * a.q_ts + at * a.q_hs;
+        load8<kVec>(q + l.d0, raw[i]);
+        load8<kVec>(q + l.p0, other[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        norm_rope8<T, float, D, kVec>(raw[i], other[i], w, l, a, y);
+        if (h + i * step < heads) store8<kVec>(a.q_out + t * a.qo_ts + (h + i * step) * a.qo_hs + l.d0, y);
+      }
     }
+    // the first that is not a query's
+    h -= ((h - heads) / step) * step;
   }
   if (h >= all) return;
   QkWeights w;
@@ -412,7 +424,10 @@ __global__ __launch_bounds__(kQThreads) void qk_kernel(QkArgs a) {
       if (slot < 0) return;
       load8<kVec>(a.v + t * a.v_ts + kh * a.v_hs + l.d0, y);
     } else {
-      norm_rope8<T, double, D, kVec>(a.k + t * a.k_ts + kh * a.k_hs, w, l, a, y);
+      uint16_t raw[8], other[8];
+      load8<kVec>(a.k + t * a.k_ts + kh * a.k_hs + l.d0, raw);
+      load8<kVec>(a.k + t * a.k_ts + kh * a.k_hs + l.p0, other);
+      norm_rope8<T, double, D, kVec>(raw, other, w, l, a, y);
       if (a.k_out) store8<kVec>(a.k_out + t * a.ko_ts + kh * a.ko_hs + l.d0, y);
       if (slot < 0) continue;
     }
