@@ -476,6 +476,9 @@ int sbm_kv_load(const uint8_t* cache, int32_t n_blocks, int32_t n_kv_heads, int3
                 const int32_t* slots, int32_t n_tokens, uint16_t* k, uint16_t* v, uint32_t flags, uint32_t* error,
                 void* stream);
 
+/* The bytes at the head of the attention's workspace that the caller zeroes before its first use. */
+#define SBM_ATTENTION_ZEROED 24576
+
 /* Workspace bytes of sbm_attention_kv4. */
 size_t sbm_attention_kv4_workspace_bytes(int32_t n_requests, int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads,
                                          int32_t head_dim);

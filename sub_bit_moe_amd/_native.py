@@ -20,6 +20,7 @@ SBM_F_IMAGE4 = 32
 SBM_F_DETERMINISTIC = 64
 SBM_F_IN_BF16 = 128
 SBM_F_NEIGHBOURS = 256
+SBM_ATTENTION_ZEROED = 24576
 SBM_PLAN_EPOOL = 1
 SBM_PLAN_EWIDTH = 2
 SBM_PLAN_ELENGTH = 4

@@ -7,6 +7,7 @@ used for host buffers, torch tensors for device memory and streams.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -23,10 +24,23 @@ def _ptr(a) -> int:
     return int(a.data_ptr())
 
 
+_current_stream = None
+
+
 def _stream(stream=None) -> int:
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    """The stream's handle; of the current stream without building a Stream object (2.6 us) for it."""
+    if stream is not None:
+        return int(stream.cuda_stream)
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if raw is None or device is None:
+            _current_stream = lambda: int(torch.cuda.current_stream().cuda_stream)   # noqa: E731
+        else:
+            _current_stream = lambda: raw(device())                                  # noqa: E731
+    return _current_stream()
 
 # ------------------------------------------------------------------ dictionary
 
@@ -421,35 +435,43 @@ def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, device="cu
     return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32).to(device)
 
 
-def _dev(t, what: str, dtype=None, like=None, contiguous: bool = True):
-    """A device tensor's address; TypeError / ValueError where it cannot be what the kernels take."""
-    if dtype is not None and t.dtype is not dtype:
+# What the calls below cost the host is what a decode step of few tokens costs, so a tensor's checks are one expression
+# that looks at each property once; the slow path says which of them failed.
+_pack_heads = struct.Struct("Pqq").pack            # sbm_heads: address, token stride, head stride
+
+
+def _dev(t, what: str, dtype, at: int, contiguous: bool = True):
+    """A device tensor's address; TypeError / ValueError where it cannot be what the kernels take.  at: the device's index."""
+    if t.dtype is dtype and t.get_device() == at >= 0 and (not contiguous or t.is_contiguous()):
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on the GPU")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{what} is on {t.device}, not {like.device}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != at:
+        raise ValueError(f"{what} is on {t.device}, not the device of the others" + ("" if at < 0 else f" ({at})"))
+    raise ValueError(f"{what} must be contiguous")
 
 
-def _heads(t, what: str, dtype, like, shape=None):
+def _heads(t, what: str, dtype, at: int, shape):
     """[tokens, heads, head_dim] with any strides but the last as sbm_heads."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    if t.dim() != 3:
         raise ValueError(f"{what} must be [tokens, heads, head_dim] with neighbouring dimensions")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    ts, hs, ds = t.stride()
+    if ds != 1 and t.shape[2] > 1:
+        raise ValueError(f"{what} must be [tokens, heads, head_dim] with neighbouring dimensions")
+    if t.shape != shape:
         raise ValueError(f"{what} is {tuple(t.shape)}, not {tuple(shape)}")
-    return N.Heads(_dev(t, what, dtype, like, False), t.stride(0), t.stride(1))
+    return _pack_heads(_dev(t, what, dtype, at, False), ts, hs)
 
 
-def _error(t, like):
+def _error(t, at: int):
     import torch
     if t is None:
         return 0
     if t.numel() < 1:
         raise ValueError("error must hold one int32")
-    return _dev(t, "error", torch.int32, like)
+    return _dev(t, "error", torch.int32, at)
 
 
 @dataclass
@@ -468,12 +490,30 @@ class KVPlan:
     block_table: object
 
 
+_error_words = {}                                  # (device, stream) -> [zeroed int32 words, how many were given out]
+
+
+def _error_word(at: int):
+    """A zeroed int32 [1] that is given out once: filled 1024 at a time, on the stream that uses them."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():   # the graph zeroes it at each replay
+        return torch.zeros(1, dtype=torch.int32, device=f"cuda:{at}")
+    pool = _error_words.setdefault((at, _stream()), [None, 1024])
+    if pool[1] == 1024:
+        pool[:] = torch.zeros(1024, dtype=torch.int32, device=f"cuda:{at}"), 0
+    pool[1] += 1
+    return pool[0][pool[1] - 1:pool[1]]
+
+
 def alloc_kv_plan(n_requests: int, max_tokens: int, block_table=None, device="cuda") -> KVPlan:
+    """A plan to be filled (kv_plan); its error word is zero, the rest is not."""
     import torch
     n, r = max_tokens, n_requests
-    buf = torch.zeros(3 * n + 2 * r + 3, dtype=torch.int32, device=device if block_table is None else block_table.device)
-    return KVPlan(buf[:n], buf[n:2 * n], buf[2 * n:3 * n], buf[3 * n:3 * n + r + 1], buf[3 * n + r + 1:3 * n + 2 * r + 1],
-                  buf[3 * n + 2 * r + 1:3 * n + 2 * r + 2], buf[3 * n + 2 * r + 2:], block_table)
+    on = torch.device(device) if block_table is None else block_table.device
+    buf = torch.empty(3 * n + 2 * r + 2, dtype=torch.int32, device=on)
+    at = buf.get_device()
+    error = _error_word(at) if at >= 0 else torch.zeros(1, dtype=torch.int32)
+    return KVPlan(*buf.split((n, n, n, r + 1, r, 1)), error, block_table)
 
 
 def kv_plan(context_lens, new_lens, free_blocks, n_free, block_table, n_blocks: int, block_size: int, max_tokens: int,
@@ -491,68 +531,92 @@ def kv_plan(context_lens, new_lens, free_blocks, n_free, block_table, n_blocks: 
         raise ValueError("context_lens, new_lens and block_table must have one row for each request")
     if n_free.numel() != 1:
         raise ValueError("n_free must hold one int32")
+    at = context_lens.get_device()
+    ins = (_dev(context_lens, "context_lens", i32, at), _dev(new_lens, "new_lens", i32, at), R,
+           _dev(free_blocks, "free_blocks", i32, at), free_blocks.numel(), _dev(n_free, "n_free", i32, at),
+           _dev(block_table, "block_table", i32, at))
     if plan is None:
-        plan = alloc_kv_plan(R, max_tokens, block_table)
-    elif plan.slots.numel() < max_tokens or plan.positions.numel() < max_tokens or plan.requests.numel() < max_tokens \
-            or plan.cu_q.numel() < R + 1 or plan.kv_lens.numel() < R:
-        raise ValueError("the plan was made for fewer requests or tokens")
-    plan.block_table = block_table
-    L = context_lens
-    check(lib().sbm_kv_plan(
-        _dev(L, "context_lens", i32), _dev(new_lens, "new_lens", i32, L), R, _dev(free_blocks, "free_blocks", i32, L),
-        free_blocks.numel(), _dev(n_free, "n_free", i32, L), _dev(block_table, "block_table", i32, L),
-        block_table.shape[1], n_blocks, block_size, max_tokens, _dev(plan.slots, "slots", i32, L),
-        _dev(plan.positions, "positions", i32, L), _dev(plan.requests, "requests", i32, L), _dev(plan.cu_q, "cu_q", i32, L),
-        _dev(plan.kv_lens, "kv_lens", i32, L), _dev(plan.n_free, "plan.n_free", i32, L), _error(plan.error, L),
-        _stream(stream)))
+        if stream is None:
+            plan = alloc_kv_plan(R, max_tokens, block_table)
+        else:
+            with torch.cuda.stream(stream):
+                plan = alloc_kv_plan(R, max_tokens, block_table)
+        n = 4 * max_tokens
+        p = plan.cu_q.data_ptr() - 3 * n           # one buffer, in this order
+        outs = (p, p + n, p + 2 * n, p + 3 * n, p + 3 * n + 4 * R + 4, p + 3 * n + 8 * R + 4, plan.error.data_ptr())
+    else:
+        if plan.slots.numel() < max_tokens or plan.positions.numel() < max_tokens or plan.requests.numel() < max_tokens \
+                or plan.cu_q.numel() < R + 1 or plan.kv_lens.numel() < R:
+            raise ValueError("the plan was made for fewer requests or tokens")
+        plan.block_table = block_table
+        outs = (_dev(plan.slots, "slots", i32, at), _dev(plan.positions, "positions", i32, at),
+                _dev(plan.requests, "requests", i32, at), _dev(plan.cu_q, "cu_q", i32, at),
+                _dev(plan.kv_lens, "kv_lens", i32, at), _dev(plan.n_free, "plan.n_free", i32, at), _error(plan.error, at))
+    check(lib().sbm_kv_plan(*ins, block_table.shape[1], n_blocks, block_size, max_tokens, *outs, _stream(stream)))
     return plan
 
 
 def _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours, q_out, k_out, slots, cache, error,
                   stream):
     import torch
+    dtype, at, shape = q.dtype, q.get_device(), q.shape
     flags = _x_flag(q) | (N.SBM_F_NEIGHBOURS if neighbours else 0)
-    hq = _heads(q, "q", None, None)
-    T, H, D = q.shape
-    hk = _heads(k, "k", q.dtype, q, (T, k.shape[1], D))
+    hq = _heads(q, "q", dtype, at, shape)
+    T, H, D = shape
     Hk = k.shape[1]
-    hv = None if v is None else _heads(v, "v", q.dtype, q, (T, Hk, D))
-    w = []
-    for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None and t.numel() != D:
-            raise ValueError(f"{what} must hold {D} elements")
-        w.append(0 if t is None else _dev(t, what, q.dtype, q))
-    pos = rp = rows = rot = 0
+    kshape = (T, Hk, D)
+    hk = _heads(k, "k", dtype, at, kshape)
+    hv = None if v is None else _heads(v, "v", dtype, at, kshape)
+    wq = wk = pos = rp = rows = rot = 0
+    if q_weight is not None:
+        if q_weight.numel() != D:
+            raise ValueError(f"q_weight must hold {D} elements")
+        wq = _dev(q_weight, "q_weight", dtype, at)
+    if k_weight is not None:
+        if k_weight.numel() != D:
+            raise ValueError(f"k_weight must hold {D} elements")
+        wk = _dev(k_weight, "k_weight", dtype, at)
     if rope is not None:
-        rp, rows, rot = _dev(rope, "rope", torch.float32, q), rope.shape[0], rope.shape[1]
+        rows, rot = rope.shape
+        rp = _dev(rope, "rope", torch.float32, at)
         if positions.numel() != T:
             raise ValueError(f"positions must hold {T} elements")
-        pos = _dev(positions, "positions", torch.int32, q)
-    ho = _heads(q_out, "q_out", q.dtype, q, (T, H, D))
-    hko = None if k_out is None else _heads(k_out, "k_out", q.dtype, q, (T, Hk, D))
+        pos = _dev(positions, "positions", torch.int32, at)
+    if q_out is None:
+        q_out = q.new_empty(shape)
+        ho = _pack_heads(q_out.data_ptr(), H * D, D)
+    else:
+        ho = _heads(q_out, "q_out", dtype, at, shape)
+    if k_out is None and cache is None:
+        k_out = q.new_empty(kshape)
+        hko = _pack_heads(k_out.data_ptr(), Hk * D, D)
+    else:
+        hko = None if k_out is None else _heads(k_out, "k_out", dtype, at, kshape)
     sl = data = nb = bs = 0
     if cache is not None:
-        if cache.n_kv_heads != Hk or cache.head_dim != D:
-            raise ValueError(f"the cache holds {cache.n_kv_heads} heads of {cache.head_dim}, not {Hk} of {D}")
-        sl, data, nb, bs = _slots(slots, T, q), _cache(cache, q), cache.n_blocks, cache.block_size
-    check(lib().sbm_qk_norm_rope(
-        C.byref(hq), C.byref(hk), hv and C.byref(hv), w[0], w[1], pos, rp, rows, rot, eps, T, H, Hk, D, C.byref(ho),
-        hko and C.byref(hko), sl, data, nb, bs, flags, _error(error, q), _stream(stream)))
+        data, nb, hc = _cache(cache, at)
+        if hc != Hk or cache.head_dim != D:
+            raise ValueError(f"the cache holds {hc} heads of {cache.head_dim}, not {Hk} of {D}")
+        sl, bs = _slots(slots, T, at), cache.block_size
+    check(lib().sbm_qk_norm_rope(hq, hk, hv, wq, wk, pos, rp, rows, rot, eps, T, H, Hk, D, ho, hko, sl, data, nb, bs, flags,
+                                 _error(error, at), _stream(stream)))
+    return q_out, k_out
 
 
-def _slots(slots, n: int, like):
+def _slots(slots, n: int, at: int):
     import torch
     if slots.numel() != n:
         raise ValueError(f"slots must hold {n} elements")
-    return _dev(slots, "slots", torch.int32, like)
+    return _dev(slots, "slots", torch.int32, at)
 
 
-def _cache(cache: KVCache, like):
+def _cache(cache: KVCache, at: int):
+    """(address, blocks, key heads)"""
     import torch
     d = cache.data
     if d.dim() != 3 or d.shape[2] != cache.block_size * cache.head_dim * 17 // 16:
         raise ValueError(f"a cache of {tuple(d.shape)} bytes holds no blocks of {cache.block_size} x {cache.head_dim}")
-    return _dev(d, "cache", torch.uint8, like)
+    return _dev(d, "cache", torch.uint8, at), d.shape[0], d.shape[1]
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, rope, eps: float = 1e-6, neighbours: bool = False, q_out=None,
@@ -561,14 +625,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, rope, eps: float = 1e-6, n
     [D] (None: ones) and rotation by rope[positions[t]] (rope_table; None: no
     rotation; neighbours: pairs (2i, 2i + 1) instead of halves), in one launch
     (sbm_qk_norm_rope).  Returns (q_out, k_out); they may be q and k."""
-    import torch
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    _qk_norm_rope(q, k, None, q_weight, k_weight, positions, rope, eps, neighbours, q_out, k_out, None, None, error,
-                  stream)
-    return q_out, k_out
+    return _qk_norm_rope(q, k, None, q_weight, k_weight, positions, rope, eps, neighbours, q_out, k_out, None, None, error,
+                         stream)
 
 
 def qk_norm_rope_store(q, k, v, q_weight, k_weight, positions, rope, slots, cache: KVCache, eps: float = 1e-6,
@@ -576,12 +634,8 @@ def qk_norm_rope_store(q, k, v, q_weight, k_weight, positions, rope, slots, cach
     """qk_norm_rope whose keys go, with the values v, into the 4-bit cache at
     slots[t] (negative: nowhere) in the same launch; k_out: the keys too.
     Returns q_out."""
-    import torch
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours, q_out, k_out, slots, cache, error,
-                  stream)
-    return q_out
+    return _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours, q_out, k_out, slots, cache, error,
+                         stream)[0]
 
 
 def kv_load(cache: KVCache, slots, dtype=None, k=None, v=None, error=None, stream=None):
@@ -589,18 +643,17 @@ def kv_load(cache: KVCache, slots, dtype=None, k=None, v=None, error=None, strea
     in float16 (or bfloat16); a negative slot gives zeros."""
     import torch
     dtype = dtype or (torch.float16 if k is None else k.dtype)
-    n = slots.numel()
-    shape = (n, cache.n_kv_heads, cache.head_dim)
+    n, at = slots.numel(), slots.get_device()
+    data, nb, Hk = _cache(cache, at)
+    shape = (n, Hk, cache.head_dim)
     if k is None:
         k = torch.empty(shape, dtype=dtype, device=slots.device)
     if v is None:
         v = torch.empty(shape, dtype=dtype, device=slots.device)
-    for t in (k, v):
-        if tuple(t.shape) != shape:
-            raise ValueError(f"k and v must be {shape}, not {tuple(t.shape)}")
-    check(lib().sbm_kv_load(_cache(cache, slots), cache.n_blocks, cache.n_kv_heads, cache.block_size, cache.head_dim,
-                            _slots(slots, n, slots), n, _dev(k, "k", dtype, slots), _dev(v, "v", dtype, slots),
-                            _x_flag(k), _error(error, slots), _stream(stream)))
+    if k.shape != shape or v.shape != shape:
+        raise ValueError(f"k and v must be {shape}, not {tuple(k.shape)} and {tuple(v.shape)}")
+    check(lib().sbm_kv_load(data, nb, Hk, cache.block_size, cache.head_dim, _slots(slots, n, at), n, _dev(k, "k", dtype, at),
+                            _dev(v, "v", dtype, at), _x_flag(k), _error(error, at), _stream(stream)))
     return k, v
 
 
@@ -610,11 +663,13 @@ def attention_workspace_bytes(n_requests: int, n_tokens: int, n_heads: int, n_kv
 
 def alloc_attention_workspace(n_requests: int, n_tokens: int, n_heads: int, n_kv_heads: int, head_dim: int,
                               device="cuda"):
-    """Zeroed workspace of the attention (it must start zeroed; every call
+    """Workspace of the attention, its head zeroed (it must start so; every call
     leaves it ready for the next)."""
     import torch
-    n = attention_workspace_bytes(n_requests, n_tokens, n_heads, n_kv_heads, head_dim)
-    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+    n = max(attention_workspace_bytes(n_requests, n_tokens, n_heads, n_kv_heads, head_dim), N.SBM_ATTENTION_ZEROED)
+    t = torch.empty(n, dtype=torch.uint8, device=device)
+    t[:N.SBM_ATTENTION_ZEROED].zero_()
+    return t
 
 
 def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: float = None, out=None, lse=None,
@@ -626,29 +681,42 @@ def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: flo
     heads, D], or (out, lse fp32 [T, heads]) with return_lse or an lse buffer."""
     import torch
     i32 = torch.int32
-    T, H, D = q.shape
+    dtype, at, shape = q.dtype, q.get_device(), q.shape
+    T, H, D = shape
     R = kv_lens.numel()
-    if cache.head_dim != D or H % cache.n_kv_heads:
-        raise ValueError(f"the cache holds {cache.n_kv_heads} heads of {cache.head_dim}; q has {H} of {D}")
+    Hk = cache.n_kv_heads
+    if cache.head_dim != D or H % Hk:
+        raise ValueError(f"the cache holds {Hk} heads of {cache.head_dim}; q has {H} of {D}")
     if block_table.dim() != 2 or block_table.shape[0] != R or (cu_q is not None and cu_q.numel() != R + 1):
         raise ValueError("kv_lens, block_table and cu_q must be of the same requests")
-    hq = _heads(q, "q", None, None)
+    hq = _heads(q, "q", dtype, at, shape)
+    data, nb, _ = _cache(cache, at)
     if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != (T, H, D):
-        raise ValueError(f"out must be {(T, H, D)}, not {tuple(out.shape)}")
-    if lse is None and return_lse:
+        out = q.new_empty(shape)
+        po = out.data_ptr()
+    elif out.shape != shape:
+        raise ValueError(f"out must be {tuple(shape)}, not {tuple(out.shape)}")
+    else:
+        po = _dev(out, "out", dtype, at)
+    pl = 0
+    if lse is not None:
+        if lse.shape != (T, H):
+            raise ValueError(f"lse must be {(T, H)}, not {tuple(lse.shape)}")
+        pl = _dev(lse, "lse", torch.float32, at)
+    elif return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    elif lse is not None and tuple(lse.shape) != (T, H):
-        raise ValueError(f"lse must be {(T, H)}, not {tuple(lse.shape)}")
+        pl = lse.data_ptr()
     if workspace is None:
-        workspace = alloc_attention_workspace(R, T, H, cache.n_kv_heads, D, q.device)
+        if stream is None:
+            workspace = alloc_attention_workspace(R, T, H, Hk, D, q.device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = alloc_attention_workspace(R, T, H, Hk, D, q.device)
     check(lib().sbm_attention_kv4(
-        C.byref(hq), _cache(cache, q), cache.n_blocks, cache.block_size, _dev(block_table, "block_table", i32, q),
-        block_table.shape[1], _dev(kv_lens, "kv_lens", i32, q), 0 if cu_q is None else _dev(cu_q, "cu_q", i32, q), R, T,
-        H, cache.n_kv_heads, D, D ** -0.5 if scale is None else scale, _dev(out, "out", q.dtype, q),
-        0 if lse is None else _dev(lse, "lse", torch.float32, q), _x_flag(q), _dev(workspace, "workspace", torch.uint8, q),
-        workspace.numel(), _error(error, q), _stream(stream)))
+        hq, data, nb, cache.block_size, _dev(block_table, "block_table", i32, at), block_table.shape[1],
+        _dev(kv_lens, "kv_lens", i32, at), 0 if cu_q is None else _dev(cu_q, "cu_q", i32, at), R, T, H, Hk, D,
+        D ** -0.5 if scale is None else scale, po, pl, _x_flag(q), _dev(workspace, "workspace", torch.uint8, at),
+        workspace.numel(), _error(error, at), _stream(stream)))
     return out if lse is None else (out, lse)
 
 # ------------------------------------------------------------------ synthetic stacks

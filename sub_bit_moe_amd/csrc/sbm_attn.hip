@@ -59,7 +59,8 @@ constexpr int tile_slots(int dim) { return dim == 256 ? 256 : 512; }
 constexpr int kFewRows = 64;
 // Counters of the workspace, before the partial results: three levels of joins for each kernel.
 constexpr int kLevels = 3, kFewCounters = 1024;
-constexpr int kCounters = kLevels * (kFewCounters + tile_slots(64));
+constexpr int kCounters = SBM_ATTENTION_ZEROED / 4;
+static_assert(kLevels * (kFewCounters + tile_slots(64)) <= kCounters);
 constexpr uint32_t kErrBlock = 1, kErrLength = 2, kErrCuQ = 4;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
