@@ -322,9 +322,10 @@ struct Rows {
   f32x4 o[D / 16];
   float m, l;
   int last;                    // the last position that the lane's row sees, -1: none
+  uint32_t nan;                // bit i: the outputs o[.][i] are NaN
 };
 
-// NaN for the rows that see a token whose values have one, where that token
+// Notes the rows that see a token whose values have a NaN, where that token
 // went into the products as if it had none (a masked step, some rows not seeing it).
 template <int D>
 __device__ __forceinline__ void nan_values(Rows<D>& s, const AttnArgs& a, const int32_t* table, int kh, int t0, int end,
@@ -338,9 +339,7 @@ __device__ __forceinline__ void nan_values(Rows<D>& s, const AttnArgs& a, const 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // rows 4g + i of an output tile are dimensions (4g + i) D / 16 and on
-      if (vs[(4 * g + i) * (D / 16) / 32] != kScaleNaN || t > s.last) continue;
-#pragma unroll
-      for (int e = 0; e < D / 16; ++e) s.o[e][i] = NAN;
+      if (vs[(4 * g + i) * (D / 16) / 32] == kScaleNaN && t <= s.last) s.nan |= 1u << i;
     }
   }
 }
@@ -434,6 +433,7 @@ __device__ __forceinline__ void init_rows(Rows<D>& s, const AttnArgs& a, int kh,
   s.last = i < rq.n ? min(rq.kv - rq.n + i, rq.kv - 1) : -1;
   s.m = kLowest;
   s.l = 0.f;
+  s.nan = 0;
 #pragma unroll
   for (int e = 0; e < D / 16; ++e) s.o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
   const uint16_t* q =
@@ -680,14 +680,15 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     float m = s_m[0][rl];
 #pragma unroll
     for (int w = 1; w < kAWaves; ++w) m = fmaxf(m, s_m[w][rl]);
-    const float by = __builtin_amdgcn_exp2f(s.m - m);
     if (rl < nr) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) {
+        const float by = s.nan >> j & 1u ? NAN : __builtin_amdgcn_exp2f(s.m - m);
 #pragma unroll
         for (int e = 0; e < D / 16; e += 4)
           *(float4*)&s_o[wave][rl][(D / 4) * g + (D / 16) * j + e] =
               make_float4(s.o[e][j] * by, s.o[e + 1][j] * by, s.o[e + 2][j] * by, s.o[e + 3][j] * by);
+      }
     }
     __syncthreads();
     const bool whole = s0 == 0 && s1 == (int)steps;
@@ -746,15 +747,14 @@ __device__ __forceinline__ f32x16 mfma_k(u32x4 k, const uint32_t* q, f32x16 c, u
                                                          (int)qs);
 }
 
-// Pieces of a query: 5 bits each below the largest of its 32 dimensions.  Three hold what bf16 has of all that are above
-// 1/64 of it, and the rest to 2^-14 of it; fp16 takes four.
-template <typename T>
-constexpr int kPieces = __is_same(T, __bf16) ? 3 : 4;
+// With three, of bf16 queries, the logarithm of the sum is off by 1.2e-6 of it (normally distributed rows), with
+// four by 8e-8; prompts took 2 % less time.
+constexpr int kPieces = 4;
 
 // 32 dimensions of a row as kPieces x 32 numbers of 6 bits; returns the pieces' scale bytes.  Each conversion
 // rounds what the ones before left to a multiple of 1/8 of its scale, up to 2.
 template <typename T>
-__device__ __forceinline__ uint32_t split_query(const AttnArgs& a, const uint16_t* q, uint32_t (&out)[kPieces<T>][6]) {
+__device__ __forceinline__ uint32_t split_query(const AttnArgs& a, const uint16_t* q, uint32_t (&out)[kPieces][6]) {
   typedef float f32x32 __attribute__((ext_vector_type(32)));
   typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
   f32x16 even, odd;
@@ -776,12 +776,12 @@ __device__ __forceinline__ uint32_t split_query(const AttnArgs& a, const uint16_
   }
   const uint32_t e = max(top >> 23, 16u);            // the last piece's scale is 2^-126 or more
 #pragma unroll
-  for (int p = 0; p < kPieces<T>; ++p) {
+  for (int p = 0; p < kPieces; ++p) {
     const float scale = exponent(e - 5 * p);
     const u32x6 c = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, scale);     // the two in turn
 #pragma unroll
     for (int i = 0; i < 6; ++i) out[p][i] = c[i];
-    if (p + 1 == kPieces<T>) break;
+    if (p + 1 == kPieces) break;
     const f32x32 got = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(c, scale);
 #pragma unroll
     for (int i = 0; i < 16; ++i) even[i] -= got[2 * i], odd[i] -= got[2 * i + 1];       // exact
@@ -804,9 +804,11 @@ struct Tile {
 // are of one block too (two with D = 64), so that its address is made by the scalar unit.
 template <int D>
 struct Fetch {
-  uint4 k;
+  u32x4 k;
   uint32_t ks, v[4], vs[D / 32];
   bool ok;
+  const uint8_t* rec;        // the block's record
+  uint32_t row;              // in it, the first of the unit's 16 tokens
 };
 
 // The blocks of a wave's unit: of its lanes' 16 tokens.
@@ -815,48 +817,54 @@ struct Blocks {
   int32_t b[D == 64 ? 2 : 1];
 };
 
-template <int D>
-__device__ __forceinline__ void fetch(Fetch<D>& f, const AttnArgs& a, const Blocks<D>& blocks, int kh, int t0, int unit) {
-  const int bs = 1 << a.shift;
-  // a block's K codes from the 16 tokens on; hidden tokens: read, and not used
-  auto record = [&](int32_t b, bool* ok) {
-    b = __builtin_amdgcn_readfirstlane(b);
-    *ok = (uint32_t)b < (uint32_t)a.n_blocks;
-    return a.cache + (uint64_t)((uint32_t)(*ok ? b : 0) * (uint32_t)a.kv_heads + (uint32_t)kh) * (uint32_t)kv_record_bytes(bs, D);
-  };
-  const int unit0 = __builtin_amdgcn_readfirstlane(unit);
-  const uint8_t* rec = record(blocks.b[0], &f.ok);
-  int row = (t0 + 16 * (unit0 / (D / 2))) & (bs - 1);                        // the unit's 16 tokens
-  if constexpr (D == 64) {
-    bool ok;
-    const uint8_t* other = record(blocks.b[1], &ok);
-    const int row1 = (t0 + 16 * (unit0 / 32 + 1)) & (bs - 1);
-    const bool second = unit & 32;
-    rec = second ? other : rec;
-    row = second ? row1 : row;
-    f.ok = second ? ok : f.ok;
-  }
-  const uint8_t* scales = rec + bs * D + row * (D / 32);
+// In kFetchParts parts: where the unit is and K, V, V's scales.  t: the unit's first 16 tokens (of the wave's two with D = 64).
+constexpr int kFetchParts = 3;
+template <int kPart, int D>
+__device__ __forceinline__ void fetch(Fetch<D>& f, const AttnArgs& a, const Blocks<D>& blocks, int kh, int t, int unit) {
+  const uint32_t bs = 1u << a.shift;
   // offsets of 32 bits to an address of the scalar unit (pinned, or the compiler keeps them as pairs)
-  uint32_t ko = unit % (D / 2);
-  const uint32_t u = unit >> 1, c = u % (D / 8);
-  uint32_t run = 8 * (unit & 1) + 4 * (u / (D / 8) & 1), vo = run * (D / 2) + 4 * c;
-  run *= D / 32;
-  pin(ko), pin(run), pin(vo);
-  f.k = *(const uint4*)(rec + row * (D / 2) + 16 * ko);
-  f.ks = scales[ko];
-  const uint8_t* vc = rec + bs * (D / 2) + row * (D / 2);
+  if constexpr (kPart == 0) {
+    auto record = [&](int32_t b, bool* ok) {            // hidden tokens: read, and not used
+      b = __builtin_amdgcn_readfirstlane(b);
+      *ok = (uint32_t)b < (uint32_t)a.n_blocks;
+      return a.cache + (uint64_t)((uint32_t)(*ok ? b : 0) * (uint32_t)a.kv_heads + (uint32_t)kh) * (uint32_t)kv_record_bytes(bs, D);
+    };
+    f.rec = record(blocks.b[0], &f.ok);
+    f.row = (uint32_t)t & (bs - 1u);
+    if constexpr (D == 64) {
+      bool ok;
+      const uint8_t* other = record(blocks.b[1], &ok);
+      const uint32_t row1 = (uint32_t)(t + 16) & (bs - 1u);
+      const bool second = unit & 32;
+      f.rec = second ? other : f.rec;
+      f.row = second ? row1 : f.row;
+      f.ok = second ? ok : f.ok;
+    }
+    uint32_t ko = unit % (D / 2);
+    pin(ko);
+    f.k = *(const u32x4*)(f.rec + f.row * (D / 2) + 16 * ko);
+    f.ks = (f.rec + (bs * D + f.row * (D / 32)))[ko];
+  } else if constexpr (kPart == 1) {
+    const uint32_t u = unit >> 1, c = u % (D / 8), run = 8 * (unit & 1) + 4 * (u / (D / 8) & 1);
+    uint32_t vo = run * (D / 2) + 4 * c;
+    pin(vo);
+    const uint8_t* vc = f.rec + (bs + f.row) * (D / 2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f.v[i] = *(const uint32_t*)(vc + vo + i * (D / 2));
-  const uint8_t* vs = scales + bs * (D / 32);
-  if constexpr (D == 64) {
-    const uint2 w = *(const uint2*)(vs + run);
-    f.vs[0] = w.x, f.vs[1] = w.y;
+    for (int i = 0; i < 4; ++i) f.v[i] = *(const uint32_t*)(vc + vo + i * (D / 2));
   } else {
+    const uint32_t u = unit >> 1;
+    uint32_t run = (8 * (unit & 1) + 4 * (u / (D / 8) & 1)) * (D / 32);
+    pin(run);
+    const uint8_t* vs = f.rec + (bs * D + (bs + f.row) * (D / 32));
+    if constexpr (D == 64) {
+      const uint2 w = *(const uint2*)(vs + run);
+      f.vs[0] = w.x, f.vs[1] = w.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < D / 128; ++i) {
-      const uint4 w = *(const uint4*)(vs + run + 16 * i);
-      f.vs[4 * i] = w.x, f.vs[4 * i + 1] = w.y, f.vs[4 * i + 2] = w.z, f.vs[4 * i + 3] = w.w;
+      for (int i = 0; i < D / 128; ++i) {
+        const uint4 w = *(const uint4*)(vs + run + 16 * i);
+        f.vs[4 * i] = w.x, f.vs[4 * i + 1] = w.y, f.vs[4 * i + 2] = w.z, f.vs[4 * i + 3] = w.w;
+      }
     }
   }
 }
@@ -888,7 +896,7 @@ template <int kStepNo, typename T, int D>
 __device__ __forceinline__ void put_tile(Tile<D>& tile, const Fetch<D>& f, const uint32_t (&sc)[4], int unit) {
   if constexpr (kStepNo == 0) {
     const int kt = unit / (D / 32), kx = unit % (D / 32);
-    *(uint4*)(tile.k + ((kt >> 5) * (D / 64) + (kx >> 1)) * 1024 + (((kt & 31) ^ (kx * (256 / D))) + 32 * (kx & 1)) * 16) = f.k;
+    *(u32x4*)(tile.k + ((kt >> 5) * (D / 64) + (kx >> 1)) * 1024 + (((kt & 31) ^ (kx * (256 / D))) + 32 * (kx & 1)) * 16) = f.k;
     tile.ks[unit] = (uint8_t)f.ks;
   } else {
     constexpr int kB = kStepNo - 1;                    // dimensions 2 kB and 2 kB + 1 of the thread's 8
@@ -908,10 +916,11 @@ __device__ __forceinline__ void put_tile(Tile<D>& tile, const Fetch<D>& f, const
 // A wave's 32 rows.
 template <typename T, int D>
 struct TileRows {
-  uint32_t q[D / 64][kPieces<T>][6], qs[D / 64];
+  uint32_t q[D / 64][kPieces][6], qs[D / 64];
   f32x16 o[D / 32];
   float m, l;
   int last;
+  uint32_t nan;                // bit db: the outputs o[db] are NaN
 };
 
 // As nan_values.  o[db][i] is dimension 32 db + 16 h + 4 (i % 4) + i / 4.
@@ -925,11 +934,8 @@ __device__ __forceinline__ void tile_nan_values(TileRows<T, D>& s, const AttnArg
     const uint8_t* vs = a.cache + ((int64_t)b * a.kv_heads + kh) * kv_record_bytes(bs, D) + bs * D + bs * (D / 32) +
                         (t & (bs - 1)) * (D / 32);
 #pragma unroll
-    for (int db = 0; db < D / 32; ++db) {
-      if (vs[db] != kScaleNaN || t > s.last) continue;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s.o[db][i] = NAN;
-    }
+    for (int db = 0; db < D / 32; ++db)
+      if (vs[db] == kScaleNaN && t <= s.last) s.nan |= 1u << db;
   }
 }
 
@@ -966,7 +972,7 @@ template <typename T, int D, typename Load, typename Prepare, typename Put>
 __device__ __forceinline__ void tile_products(TileRows<T, D>& s, const Tile<D>& tile, int t0, bool masked, uint32_t note,
                                               float scale2, int lane, Load load, Prepare prepare, Put put) {
   constexpr int kSubs = Tile<D>::kTokens / 32;
-  constexpr int kP = kPieces<T>, kS = D / 64 * kP, kG = D / 16, kHalf = kG / 2;      // products for 32 tokens: scores, values
+  constexpr int kP = kPieces, kS = D / 64 * kP, kG = D / 16, kHalf = kG / 2;      // products for 32 tokens: scores, values
   const int h = lane >> 5;
   const f32x16 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   KeyOperand<D> keys = tile_keys<D>(tile, 0, lane);
@@ -996,7 +1002,7 @@ __device__ __forceinline__ void tile_products(TileRows<T, D>& s, const Tile<D>& 
   __builtin_amdgcn_sched_barrier(0);
   each([&](auto gi) {
     product(gi, z);
-    if constexpr (decltype(gi)::value == 0) load();
+    if constexpr (decltype(gi)::value < kFetchParts * Tile<D>::kUnits) load(gi);
     __builtin_amdgcn_sched_barrier(0);
   }, std::make_integer_sequence<int, kS>{});
   if (masked) mask(z, 0);
@@ -1167,6 +1173,7 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
   s.last = i < rq.n ? rq.kv - rq.n + i : -1;
   s.m = kLowest;
   s.l = 0.f;
+  s.nan = 0;
 #pragma unroll
   for (int db = 0; db < D / 32; ++db)
 #pragma unroll
@@ -1177,32 +1184,36 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
     for (int kb = 0; kb < D / 64; ++kb) s.qs[kb] = split_query<T>(a, q + 64 * kb + 32 * h, s.q[kb]);
   }
   constexpr int kUnits = Tile<D>::kUnits;
+  constexpr auto kUnitList = std::make_integer_sequence<int, kUnits>{};
+  const int unit_t = 16 * (64 * wave / (D / 2));        // the first of a wave's units' tokens
+  constexpr int kUnitTokens = 32 * kTileThreads / D;
   auto blocks_at = [&](int j, Blocks<D> (&b)[kUnits]) {
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u)
+    each([&](auto u) {
 #pragma unroll
       for (int x = 0; x < (D == 64 ? 2 : 1); ++x) {
-        const int t = j * kTokens + 16 * ((64 * wave + u * kTileThreads) / (D / 2) + x);
+        const int t = j * kTokens + unit_t + u * kUnitTokens + 16 * x;
         // always read: a wait at the end of a branch would be for the tile's loads too
         const int32_t held = table[min(t, end - 1) >> a.shift];
         b[u].b[x] = t < end ? held : -1;
       }
+    }, kUnitList);
   };
   Fetch<D> f[kUnits];
-  auto load = [&](int j, const Blocks<D> (&b)[kUnits]) {
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) fetch<D>(f[u], a, b[u], kh, j * kTokens, tid + u * kTileThreads);
+  Blocks<D> next[kUnits];
+  auto load = [&](auto part, int j) {                    // of tile j, whose blocks are `next`; the last reads those of tile j + 1
+    constexpr int u = decltype(part)::value / kFetchParts, kPart = decltype(part)::value % kFetchParts;
+    fetch<kPart, D>(f[u], a, next[u], kh, j * kTokens + unit_t + u * kUnitTokens, tid + u * kTileThreads);
+    if constexpr (decltype(part)::value + 1 == kFetchParts * kUnits) blocks_at(j + 1, next);
   };
   uint32_t sc[kUnits][4];
   auto prepare = [&](int j) {
     const int t0 = j * kTokens;
     uint32_t note = 0;
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
+    each([&](auto u) {
       const int unit = tid + u * kTileThreads;
       note |= prepare_values<D>(f[u], sc[u], t0, end, t0 + kTokens - 1 > first, unit);
       if (!f[u].ok && t0 + 16 * (unit / (D / 2)) < end && a.error) atomicOr(a.error, kErrBlock);
-    }
+    }, kUnitList);
     if (note) atomicOr(&s_note[j & 3], note);
   };
   auto put = [&](auto step, int j) {
@@ -1213,10 +1224,8 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
     each([&](auto step) { put(step, j); }, std::make_integer_sequence<int, kPutSteps * kUnits>{});
   };
   if (j0 < j1) {
-    Blocks<D> next[kUnits];
     blocks_at(j0, next);
-    load(j0, next);
-    blocks_at(j0 + 1, next);
+    each([&](auto part) { load(part, j0); }, std::make_integer_sequence<int, kFetchParts * kUnits>{});
     prepare(j0);
     put_all(j0);
     __syncthreads();
@@ -1228,16 +1237,17 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
       // the next tile is read and converted while this one is worked on; past the last, the last again
       const int jn = min(j + 1, j1 - 1);
       tile_products<T, D>(s, s_tile[j & 1], t0, masked, note, a.scale2, lane,
-                          [&] {
-                            load(jn, next);
-                            blocks_at(j + 2, next);
-                          },
-                          [&] { prepare(jn); }, [&](auto step) { put(step, j + 1); });
+                          [&](auto part) { load(part, jn); }, [&] { prepare(jn); }, [&](auto step) { put(step, j + 1); });
       if (note & kNoteNaN) tile_nan_values<T, D>(s, a, table, kh, t0, end);
       __syncthreads();
     }
   }
   s.l += __shfl_xor(s.l, 32, 64);
+  if (__any(s.nan)) {
+#pragma unroll
+    for (int db = 0; db < D / 32; ++db)
+      if (s.nan >> db & 1u) s.o[db] *= NAN;
+  }
   const bool valid = row - row0 < nr;
   const int64_t at = (int64_t)(rq.q0 + i) * a.heads + kh * a.group + row % a.group;
   if (parts == 1) {
