@@ -383,7 +383,7 @@ __device__ __forceinline__ void step(Rows<D>& s, const Raw<D>& r, const AttnArgs
   }
   // P^T = exp2(scale2 * S^T - m)
   float top = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7]))) * a.scale2;
-  if (__any(top > s.m + (kBias + kSlack))) {
+  if (__builtin_expect(__any(top > s.m + (kBias + kSlack)), 0)) {
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const float to = fmaxf(s.m, top - kBias), by = __builtin_amdgcn_exp2f(s.m - to);
@@ -880,7 +880,7 @@ __device__ __forceinline__ uint32_t prepare_values(const Fetch<D>& f, uint32_t (
   uint32_t note = 0;
   value_scales<D>(f.vs, c >> 2, sc);
   if (!f.ok) note = 1u << tb;
-  if (border || !f.ok) {
+  if (__builtin_expect(border || !f.ok, 0)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool there = f.ok && t0 + 16 * tb + 8 * half + 4 * h + i < end;
@@ -989,7 +989,7 @@ __device__ __forceinline__ void tile_products(TileRows<T, D>& s, const Tile<D>& 
   };
   auto raise = [&](float top) {
     top *= scale2;
-    if (__any(top > s.m + (kBias + kSlack))) {
+    if (__builtin_expect(__any(top > s.m + (kBias + kSlack)), 0)) {
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float to = fmaxf(s.m, top - kBias), by = __builtin_amdgcn_exp2f(s.m - to);
       s.m = to;
@@ -1005,7 +1005,13 @@ __device__ __forceinline__ void tile_products(TileRows<T, D>& s, const Tile<D>& 
     if constexpr (decltype(gi)::value < kFetchParts * Tile<D>::kUnits) load(gi);
     __builtin_amdgcn_sched_barrier(0);
   }, std::make_integer_sequence<int, kS>{});
-  if (masked) mask(z, 0);
+  if constexpr (D == 256) {
+    // a wave a SIMD: the outputs are in the accumulation registers, where the products take them.  Said here, or they are
+    // copied out before each tile for the multiplication in `raise` (piece of 1024 tokens behind 19000: 463, not 492 us)
+#pragma unroll
+    for (int db = 0; db < D / 32; ++db) asm volatile("" : "+a"(s.o[db]));
+  }
+  if (__builtin_expect(masked, 0)) mask(z, 0);
   {
     float top = fmaxf(z[0], z[1]);
 #pragma unroll
@@ -1040,7 +1046,7 @@ __device__ __forceinline__ void tile_products(TileRows<T, D>& s, const Tile<D>& 
       __builtin_amdgcn_sched_barrier(0);
     }, std::make_integer_sequence<int, kS>{});
     s.l += sum[0] + sum[1];
-    if (more && masked) mask(next, sub + 1);
+    if (more && __builtin_expect(masked, 0)) mask(next, sub + 1);
     if (!more) prepare();
     float top = -INFINITY;
     each([&](auto gi) {
@@ -1214,7 +1220,7 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
       note |= prepare_values<D>(f[u], sc[u], t0, end, t0 + kTokens - 1 > first, unit);
       if (!f[u].ok && t0 + 16 * (unit / (D / 2)) < end && a.error) atomicOr(a.error, kErrBlock);
     }, kUnitList);
-    if (note) atomicOr(&s_note[j & 3], note);
+    if (__builtin_expect(note != 0, 0)) atomicOr(&s_note[j & 3], note);
   };
   auto put = [&](auto step, int j) {
     constexpr int u = decltype(step)::value / kPutSteps;
@@ -1238,7 +1244,7 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
       const int jn = min(j + 1, j1 - 1);
       tile_products<T, D>(s, s_tile[j & 1], t0, masked, note, a.scale2, lane,
                           [&](auto part) { load(part, jn); }, [&] { prepare(jn); }, [&](auto step) { put(step, j + 1); });
-      if (note & kNoteNaN) tile_nan_values<T, D>(s, a, table, kh, t0, end);
+      if (__builtin_expect(note & kNoteNaN, 0)) tile_nan_values<T, D>(s, a, table, kh, t0, end);
       __syncthreads();
     }
   }
