@@ -56,7 +56,7 @@ constexpr int kTileThreads = 256;
 constexpr int kTileRows = kTileThreads / 2;
 constexpr int tile_slots(int dim) { return dim == 256 ? 256 : 512; }
 // Rows (tokens x heads of one key head) of a request up to which the few-row kernel takes it.
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 128;
 // Counters of the workspace, before the partial results: three levels of joins for each kernel.
 constexpr int kLevels = 3, kFewCounters = 1024;
 constexpr int kCounters = SBM_ATTENTION_ZEROED / 4;
@@ -455,16 +455,36 @@ __device__ __forceinline__ void store4(const AttnArgs& a, int kh, const Request&
   if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-// A partial result: O [kRows][D], then (m, l) [kRows].
+// A partial result: kRows x D outputs, then (m, l) [kRows].
 template <int D, int kRows>
 constexpr int kPart = kRows * (D + 2);
+
+// The outputs go four dimensions at a time, two pairs: element e is of row row(e), from dimension dim(e) on, its first
+// pair at pair(e) and its second kNext floats behind.  What is written through goes to memory as it is issued, so a
+// store of a wave covers whole lines: lanes' pairs are neighbours.
+template <int D>
+struct FewLayout {                                   // row by row
+  static constexpr int kNext = 2;
+  __device__ static int count(int nr) { return nr * (D / 4); }
+  __device__ static int row(int e) { return e / (D / 4); }
+  __device__ static int dim(int e) { return e % (D / 4) * 4; }
+  __device__ static int pair(int e) { return 4 * e; }
+};
+template <int D>
+struct TileLayout {                                  // as the tile kernel's waves hold them: [wave][D / 32][8 pairs][64 lanes]
+  static constexpr int kNext = 128;
+  __device__ static int count(int nr) { return (nr + 31) / 32 * 32 * (D / 4); }
+  __device__ static int row(int e) { return (e >> 8) / (D / 32) * 32 + (e & 31); }
+  __device__ static int dim(int e) { return (e >> 8) % (D / 32) * 32 + (e >> 5 & 1) * 16 + (e >> 6 & 3) * 4; }
+  __device__ static int pair(int e) { return ((e >> 6) * 2 * 64 + (e & 63)) * 2; }
+};
 
 // Partial results of the same rows, joined kRadix at a time by the workgroup that is the last of them to end, the joins
 // likewise, until one is left: no workgroup waits, and as the members go in order the result
 // does not depend on who ends last.  p: this workgroup's part, already written, of np > 1; at(p): where part p is, a join's
 // result being where its first part was; counters: zero before and after.  One at a time would read np parts with one
 // workgroup (170 parts of 8 x 256: 300 us).
-template <typename T, int D, int kRows, int kRadix, int kThreads, typename At>
+template <typename T, int D, int kRows, int kRadix, int kThreads, typename Layout, typename At>
 __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, uint32_t* counters, int level_stride, float* s_w,
                                   uint32_t* s_flag, int kh, const Request& rq, int row0, int nr) {
   float* s_l = s_w + kRadix * kRows;
@@ -503,38 +523,43 @@ __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, ui
       }
       __syncthreads();
       constexpr int kB = 4;                            // four elements' loads in flight
-      for (int e0 = tid; e0 < nr * (D / 4); e0 += kB * kThreads) {
+      const int count = Layout::count(nr);
+      for (int e0 = tid; e0 < count; e0 += kB * kThreads) {
         float4 o[kB];
 #pragma unroll
         for (int b = 0; b < kB; ++b) o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k0 = 0; k0 < members; k0 += 4) {
-          float4 x[4][kB];
+          float2 x[4][kB], y[4][kB];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float* v = at((first + min(k0 + k, members - 1)) * stride);
 #pragma unroll
-            for (int b = 0; b < kB; ++b) x[k][b] = *(const float4*)(v + 4 * min(e0 + b * kThreads, nr * (D / 4) - 1));
+            for (int b = 0; b < kB; ++b) {
+              const int p = Layout::pair(min(e0 + b * kThreads, count - 1));
+              x[k][b] = *(const float2*)(v + p);
+              y[k][b] = *(const float2*)(v + p + Layout::kNext);
+            }
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
 #pragma unroll
             for (int b = 0; b < kB; ++b) {
-              const int row = min(e0 + b * kThreads, nr * (D / 4) - 1) / (D / 4);
+              const int row = min(Layout::row(min(e0 + b * kThreads, count - 1)), nr - 1);
               const float w = k0 + k < members ? s_w[(k0 + k) * kRows + row] : 0.f;
-              o[b].x += w * x[k][b].x, o[b].y += w * x[k][b].y, o[b].z += w * x[k][b].z, o[b].w += w * x[k][b].w;
+              o[b].x += w * x[k][b].x, o[b].y += w * x[k][b].y, o[b].z += w * y[k][b].x, o[b].w += w * y[k][b].y;
             }
           }
         }
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
-          const int e = e0 + b * kThreads, row = e / (D / 4);
-          if (e >= nr * (D / 4)) break;
+          const int e = e0 + b * kThreads, row = Layout::row(e);
+          if (e >= count || row >= nr) continue;
           if (last_level) {
-            store4<T, D>(a, kh, rq, row0 + row, e % (D / 4) * 4, o[b], s_l[kRows + row], s_l[row]);
+            store4<T, D>(a, kh, rq, row0 + row, Layout::dim(e), o[b], s_l[kRows + row], s_l[row]);
           } else {
-            float* v = at(first * stride) + 4 * e;
+            float* v = at(first * stride) + Layout::pair(e);
             put2(v, o[b].x, o[b].y);
-            put2(v + 2, o[b].z, o[b].w);
+            put2(v + Layout::kNext, o[b].z, o[b].w);
           }
         }
       }
@@ -694,30 +719,38 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     const bool whole = s0 == 0 && s1 == (int)steps;
     const uint64_t b0 = quotient(item_at, per), b1 = quotient(item_at + steps - 1, per);       // the workgroups that share the rows
     float* part = a.parts + (2 * (uint64_t)blockIdx.x + (blockIdx.x == b0 ? 1 : 0)) * kPart<D, 16>;
-    for (int e = tid; e < nr * (D / 4); e += kAThreads) {
-      const int row = e / (D / 4), d = e % (D / 4) * 4;
-      float top = s_m[0][row];
+    auto joined = [&](int row, int d, float* v, int n, float* top, float* l) {       // n dimensions from d on, their m and l
+      float t = s_m[0][row];
 #pragma unroll
-      for (int w = 1; w < kAWaves; ++w) top = fmaxf(top, s_m[w][row]);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float l = 0.f;
+      for (int w = 1; w < kAWaves; ++w) t = fmaxf(t, s_m[w][row]);
+      float sum = 0.f;
+      for (int i = 0; i < n; ++i) v[i] = 0.f;
 #pragma unroll
       for (int w = 0; w < kAWaves; ++w) {
-        const float4 v = *(const float4*)&s_o[w][row][d];
-        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-        l += s_l[w][row] * __builtin_amdgcn_exp2f(s_m[w][row] - top);
+        for (int i = 0; i < n; ++i) v[i] += s_o[w][row][d + i];
+        sum += s_l[w][row] * __builtin_amdgcn_exp2f(s_m[w][row] - t);
       }
-      if (whole) {
-        store4<T, D>(a, kh, rq, row0 + row, d, o, top, l);
-      } else {
-        put2(part + row * D + d, o.x, o.y);
-        put2(part + row * D + d + 2, o.z, o.w);
+      *top = t, *l = sum;
+    };
+    if (whole) {
+      for (int e = tid; e < nr * (D / 4); e += kAThreads) {
+        const int row = e / (D / 4), d = e % (D / 4) * 4;
+        float v[4], top, l;
+        joined(row, d, v, 4, &top, &l);
+        store4<T, D>(a, kh, rq, row0 + row, d, make_float4(v[0], v[1], v[2], v[3]), top, l);
+      }
+    } else {
+      for (int e = tid; e < nr * (D / 2); e += kAThreads) {
+        const int row = e / (D / 2), d = e % (D / 2) * 2;
+        float v[2], top, l;
+        joined(row, d, v, 2, &top, &l);
+        put2(part + 2 * e, v[0], v[1]);
         if (d == 0) put2(part + 16 * D + 2 * row, top, l);
       }
     }
     if (whole) continue;
     float* p0 = a.parts + (2 * b0 + 1) * kPart<D, 16>;
-    join<T, D, 16, 16, kAThreads>(a, [&](int p) { return p == 0 ? p0 : p0 + (2 * (int64_t)p - 1) * kPart<D, 16>; },
+    join<T, D, 16, 16, kAThreads, FewLayout<D>>(a, [&](int p) { return p == 0 ? p0 : p0 + (2 * (int64_t)p - 1) * kPart<D, 16>; },
                        (int)(blockIdx.x - b0), (int)(b1 - b0) + 1, a.counters + b0, kFewCounters, &s_o[0][0][0], &s_last, kh,
                        rq, row0, nr);
   }
@@ -1277,19 +1310,19 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
   const uint32_t item = unit / (uint32_t)a.kv_heads / parts * (uint32_t)a.kv_heads + (uint32_t)kh;
   const uint32_t slot0 = slots0 + item * parts;
   float* p0 = a.parts + (int64_t)slot0 * kPart<D, kTileRows>;
-  if (valid) {
-    float* mine = p0 + (int64_t)part * kPart<D, kTileRows>;
-    float* o = mine + (row - row0) * D + 16 * h;
+  float* mine = p0 + (int64_t)part * kPart<D, kTileRows>;
+  if (32 * wave < nr) {                                // rows that are not there are written with the others, and not read
+    float* o = mine + wave * 32 * D + 2 * lane;
 #pragma unroll
     for (int db = 0; db < D / 32; ++db)
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         const int b = x >> 1, lo = x & 1 ? 2 : 0;
-        put2(o + 32 * db + 2 * x, s.o[db][4 * lo + b], s.o[db][4 * lo + 4 + b]);
+        put2(o + (db * 8 + x) * 128, s.o[db][4 * lo + b], s.o[db][4 * lo + 4 + b]);
       }
     if (h == 0) put2(mine + kTileRows * D + 2 * (row - row0), s.m, s.l);
   }
-  join<T, D, kTileRows, 8, kTileThreads>(a, [&](int p) { return p0 + (int64_t)p * kPart<D, kTileRows>; }, part, (int)parts,
+  join<T, D, kTileRows, 8, kTileThreads, TileLayout<D>>(a, [&](int p) { return p0 + (int64_t)p * kPart<D, kTileRows>; }, part, (int)parts,
                            a.counters + kLevels * kFewCounters + slot0, tile_slots(64), (float*)&s_tile[0], &s_unit[0], kh, rq,
                            row0, nr);
 }
