@@ -1121,12 +1121,13 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, const Request& q) {
   return s;
 }
 
-// With fewer rows than the chip takes the tokens are split, kMinTiles to a part at least.
-constexpr uint32_t kMinTiles = 8;
+// With fewer rows than the chip takes the tokens are split, so many tiles to a part at least (tiles of wide heads take
+// longer; with half of this a join costs more than it saves).
+constexpr uint32_t min_tiles(int dim) { return dim == 256 ? 4 : 8; }
 template <int D>
 __device__ __forceinline__ uint32_t parts_of(const Share& s, uint64_t total) {
   const uint64_t parts = quotient((uint64_t)s.steps * tile_slots(D), max(total, (uint64_t)1));
-  return (uint32_t)max(min(parts, (uint64_t)(s.steps / kMinTiles)), (uint64_t)1);
+  return (uint32_t)max(min(parts, (uint64_t)(s.steps / min_tiles(D))), (uint64_t)1);
 }
 
 template <typename T, int D>
