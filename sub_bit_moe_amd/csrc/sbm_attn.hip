@@ -1246,15 +1246,15 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
     if constexpr (decltype(part)::value + 1 == kFetchParts * kUnits) blocks_at(j + 1, next);
   };
   uint32_t sc[kUnits][4];
-  auto prepare = [&](int j) {
+  auto prepare = [&](int j, bool real) {               // real: past the last tile what was read is not looked at
     const int t0 = j * kTokens;
     uint32_t note = 0;
     each([&](auto u) {
       const int unit = tid + u * kTileThreads;
       note |= prepare_values<D>(f[u], sc[u], t0, end, t0 + kTokens - 1 > first, unit);
-      if (!f[u].ok && t0 + 16 * (unit / (D / 2)) < end && a.error) atomicOr(a.error, kErrBlock);
+      if (real && !f[u].ok && t0 + 16 * (unit / (D / 2)) < end && a.error) atomicOr(a.error, kErrBlock);
     }, kUnitList);
-    if (__builtin_expect(note != 0, 0)) atomicOr(&s_note[j & 3], note);
+    if (__builtin_expect(real && note != 0, 0)) atomicOr(&s_note[j & 3], note);
   };
   auto put = [&](auto step, int j) {
     constexpr int u = decltype(step)::value / kPutSteps;
@@ -1266,7 +1266,7 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
   if (j0 < j1) {
     blocks_at(j0, next);
     each([&](auto part) { load(part, j0); }, std::make_integer_sequence<int, kFetchParts * kUnits>{});
-    prepare(j0);
+    prepare(j0, true);
     put_all(j0);
     __syncthreads();
     for (int j = j0; j < j1; ++j) {
@@ -1277,7 +1277,7 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
       // the next tile is read and converted while this one is worked on; past the last, the last again
       const int jn = min(j + 1, j1 - 1);
       tile_products<T, D>(s, s_tile[j & 1], t0, masked, note, a.scale2, lane,
-                          [&](auto part) { load(part, jn); }, [&] { prepare(jn); }, [&](auto step) { put(step, j + 1); });
+                          [&](auto part) { load(part, jn); }, [&] { prepare(jn, j + 1 < j1); }, [&](auto step) { put(step, j + 1); });
       if (__builtin_expect(note & kNoteNaN, 0)) tile_nan_values<T, D>(s, a, table, kh, t0, end);
       __syncthreads();
     }
