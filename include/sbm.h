@@ -500,10 +500,10 @@ size_t sbm_attention_kv4_workspace_bytes(int32_t n_requests, int32_t n_tokens, i
  *             that falls, or passes n_tokens, sets bit 2 (that request's rows
  *             may be left unwritten)
  *   workspace: device, 16-byte aligned, of sbm_attention_kv4_workspace_bytes(...)
- *             or more, ZEROED by the caller before its first use; every call
- *             leaves it ready for the next (calls that share one must not
- *             overlap).  n_requests <= 4096
- * fp16: cached values are read as fp16 (magnitudes above 65504 become
+ *             or more, its first SBM_ATTENTION_ZEROED bytes ZEROED by the caller
+ *             before its first use; every call leaves it ready for the next (calls
+ *             that share one must not overlap).  n_requests <= 4096
+ * fp16: cached values may be read as fp16 (magnitudes above 65504 become
  * infinite; a cache written from fp16 holds none). */
 int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks, int32_t block_size,
                       const int32_t* block_table, int32_t table_width, const int32_t* kv_lens, const int32_t* cu_q,
