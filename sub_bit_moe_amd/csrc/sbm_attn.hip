@@ -445,6 +445,8 @@ __device__ __forceinline__ void init_rows(Rows<D>& s, const AttnArgs& a, int kh,
 // How many times 32 tokens a wave has under way, and waves on a SIMD, by the registers that takes.
 constexpr int few_ring(int dim) { return dim == 256 ? 1 : 2; }
 constexpr int few_waves(int dim) { return dim == 64 ? 3 : 2; }
+// Workgroups of the few-row kernel at most: as many as the chip holds at once.
+constexpr int few_wgs(int dim) { return 256 * few_waves(dim); }
 // A row's outputs are stored, four neighbouring dimensions at a time.
 template <typename T, int D>
 __device__ __forceinline__ void store4(const AttnArgs& a, int kh, const Request& rq, int row, int d, float4 o, float m,
@@ -578,7 +580,7 @@ __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, ui
 // Bound by HBM with long caches (the codes are read once, K and V of 32 tokens
 // ahead), by latency with short ones.
 template <typename T, int D>
-__global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnArgs a) {
+__device__ __forceinline__ void few_rows(const AttnArgs& a, const uint32_t block, const uint32_t grid) {
   constexpr int kPad = D + 4;
   __shared__ __align__(16) float s_o[kAWaves][16][kPad];
   __shared__ float s_m[kAWaves][16], s_l[kAWaves][16];
@@ -589,7 +591,7 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
   // tokens of no request
   if (a.cu_q) {
     const int c0 = min(max(a.cu_q[0], 0), a.n_tokens), c1 = min(max(a.cu_q[R], 0), a.n_tokens);
-    for (int t = blockIdx.x; t < a.n_tokens; t += gridDim.x) {
+    for (int t = (int)block; t < a.n_tokens; t += (int)grid) {
       if (t >= c0 && t < c1) continue;
       for (int d = tid; d < a.heads * D; d += kAThreads) a.out[(int64_t)t * a.heads * D + d] = 0;
       if (a.lse)
@@ -601,7 +603,7 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     if (r >= R) return 0;
     uint32_t bad = 0;
     const Request q = request(a, r, &bad);
-    if (bad && blockIdx.x == 0 && a.error) atomicOr(a.error, bad);
+    if (bad && block == 0 && a.error) atomicOr(a.error, bad);
     if ((int64_t)q.n * a.group > kFewRows) return 0;
     const uint32_t tiles = ((uint32_t)q.n * (uint32_t)a.group + 15u) / 16u;
     return (uint64_t)tiles * (uint32_t)a.kv_heads * max((uint32_t)(q.kv + kStep - 1) / kStep, 1u);
@@ -609,8 +611,8 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
   uint64_t total = 0, pos, stop, per, r_at;            // r_at: the request's first step
   int r;
   auto share = [&] {
-    per = max(quotient(total + gridDim.x - 1, gridDim.x), (uint64_t)kMinSteps);
-    pos = per * blockIdx.x;
+    per = max(quotient(total + grid - 1, grid), (uint64_t)kMinSteps);
+    pos = per * block;
     stop = min(pos + per, total);
   };
   if (R <= 64) {                                       // every wave for itself
@@ -718,7 +720,7 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     __syncthreads();
     const bool whole = s0 == 0 && s1 == (int)steps;
     const uint64_t b0 = quotient(item_at, per), b1 = quotient(item_at + steps - 1, per);       // the workgroups that share the rows
-    float* part = a.parts + (2 * (uint64_t)blockIdx.x + (blockIdx.x == b0 ? 1 : 0)) * kPart<D, 16>;
+    float* part = a.parts + (2 * (uint64_t)block + (block == b0 ? 1 : 0)) * kPart<D, 16>;
     auto joined = [&](int row, int d, float* v, int n, float* top, float* l) {       // n dimensions from d on, their m and l
       float t = s_m[0][row];
 #pragma unroll
@@ -751,9 +753,14 @@ __global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnA
     if (whole) continue;
     float* p0 = a.parts + (2 * b0 + 1) * kPart<D, 16>;
     join<T, D, 16, 16, kAThreads, FewLayout<D>>(a, [&](int p) { return p == 0 ? p0 : p0 + (2 * (int64_t)p - 1) * kPart<D, 16>; },
-                       (int)(blockIdx.x - b0), (int)(b1 - b0) + 1, a.counters + b0, kFewCounters, &s_o[0][0][0], &s_last, kh,
+                       (int)(block - b0), (int)(b1 - b0) + 1, a.counters + b0, kFewCounters, &s_o[0][0][0], &s_last, kh,
                        rq, row0, nr);
   }
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(kAThreads, few_waves(D)) void attn_few_kernel(AttnArgs a) {
+  few_rows<T, D>(a, blockIdx.x, gridDim.x);
 }
 
 // ------------------------------------------------------------------ prompts
@@ -1131,7 +1138,7 @@ __device__ __forceinline__ uint32_t parts_of(const Share& s, uint64_t total) {
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kernel(AttnArgs a) {
+__device__ __forceinline__ void tile_rows(const AttnArgs& a, const uint32_t block) {
   constexpr int kTokens = Tile<D>::kTokens;
   __shared__ __align__(16) Tile<D> s_tile[2];
   __shared__ uint64_t s_wave[kTileThreads / 64];
@@ -1148,17 +1155,17 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
   uint32_t unit, slots0, parts;
   if (R <= 64) {                                       // every wave for itself
     Share s = share(lane);
-    if (bad && blockIdx.x == 0 && wave == 0 && a.error) atomicOr(a.error, bad);
+    if (bad && block == 0 && wave == 0 && a.error) atomicOr(a.error, bad);
     uint64_t total = of_lane(wave_scan_add((uint64_t)s.tiles * s.steps * (uint32_t)a.kv_heads), 63);
     // requests that overlap may be more than the grid has workgroups for: then no rows are shared by several
     if (__any(bad & kErrCuQ)) total = 1ull << 60;
     s.parts = parts_of<D>(s, total);
     const uint64_t mine = (uint64_t)s.tiles * (uint32_t)a.kv_heads * s.parts, upto = wave_scan_add(mine);
     const uint64_t shared = s.parts > 1 ? mine : 0, slots = wave_scan_add(shared);
-    const uint64_t here = __ballot(blockIdx.x < upto && blockIdx.x >= upto - mine);
+    const uint64_t here = __ballot(block < upto && block >= upto - mine);
     if (!here) return;
     r = (int)__builtin_ctzll(here);
-    unit = (uint32_t)(blockIdx.x - of_lane(upto - mine, r));
+    unit = (uint32_t)(block - of_lane(upto - mine, r));
     slots0 = (uint32_t)of_lane(slots - shared, r);
     parts = (uint32_t)__builtin_amdgcn_readlane((int)s.parts, r);
     __syncthreads();
@@ -1169,7 +1176,7 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
       scan_add<kTileThreads / 64>((uint64_t)s.tiles * s.steps * (uint32_t)a.kv_heads, s_wave, &sum);
       total += sum;
     }
-    if (bad && blockIdx.x == 0 && a.error) atomicOr(a.error, bad);
+    if (bad && block == 0 && a.error) atomicOr(a.error, bad);
     if (__syncthreads_or((int)(bad & kErrCuQ))) total = 1ull << 60;
     if (tid == 0) s_unit[0] = 0xFFFFFFFFu;
     uint64_t units = 0, split = 0;
@@ -1181,9 +1188,9 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
       units += sum;
       const uint64_t slots = split + scan_add<kTileThreads / 64>(shared, s_wave, &sum);
       split += sum;
-      if (blockIdx.x < upto && blockIdx.x >= upto - mine) {
+      if (block < upto && block >= upto - mine) {
         s_unit[0] = (uint32_t)(base + tid);
-        s_unit[1] = (uint32_t)(blockIdx.x - (upto - mine));
+        s_unit[1] = (uint32_t)(block - (upto - mine));
         s_unit[2] = (uint32_t)(slots - shared);
         s_unit[3] = s.parts;
       }
@@ -1208,8 +1215,6 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
   TileRows<T, D> s;
   const int row = row0 + 32 * wave + (lane & 31), i = row / a.group, h = lane >> 5;
   const int wave_first = __builtin_amdgcn_readfirstlane(max(rq.kv - rq.n + (row0 + 32 * wave) / a.group, -1));
-  const int wave_last =
-      row0 + 32 * wave < rq.n * a.group ? rq.kv - rq.n + min((row0 + 32 * wave + 31) / a.group, rq.n - 1) : -1;
   s.last = i < rq.n ? rq.kv - rq.n + i : -1;
   s.m = kLowest;
   s.l = 0.f;
@@ -1310,7 +1315,7 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
   }
   const uint32_t item = unit / (uint32_t)a.kv_heads / parts * (uint32_t)a.kv_heads + (uint32_t)kh;
   const uint32_t slot0 = slots0 + item * parts;
-  float* p0 = a.parts + (int64_t)slot0 * kPart<D, kTileRows>;
+  float* p0 = a.parts + kPart<D, 16> * 2 * few_wgs(D) + (int64_t)slot0 * kPart<D, kTileRows>;
   float* mine = p0 + (int64_t)part * kPart<D, kTileRows>;
   if (32 * wave < nr) {                                // rows that are not there are written with the others, and not read
     float* o = mine + wave * 32 * D + 2 * lane;
@@ -1328,10 +1333,39 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
                            row0, nr);
 }
 
+template <typename T, int D>
+__global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kernel(AttnArgs a) {
+  tile_rows<T, D>(a, blockIdx.x);
+}
+
+// A step that may hold both: one launch, so that the few-row part, which waits for memory, and the prompts, which do not,
+// run at once.  A workgroup a CU of each comes first, then the rest.  Heads of 128, 24 requests with four prompts of 511
+// tokens: 140 us instead of 150 with two launches; two prompts of 1077 tokens and 6 heads beside five requests: 40, not 50.
+// Heads of 256 take a whole CU's registers for a prompt's workgroup and are launched one after the other.
+constexpr uint32_t kCus = 256;
+template <typename T, int D>
+__global__ __launch_bounds__(kTileThreads, 2) void attn_step_kernel(AttnArgs a, uint32_t few, uint32_t tiles) {
+  static_assert(kTileThreads == kAThreads);
+  const uint32_t b = blockIdx.x, f0 = min(few, kCus), t0 = min(tiles, kCus);
+  // each part reads the arguments anew: shared, they would be held in registers through both
+  typedef const AttnArgs __attribute__((address_space(4))) * Kernarg;
+  Kernarg own = (Kernarg)__builtin_amdgcn_kernarg_segment_ptr();
+  if (b < f0 || (b >= f0 + t0 && b < t0 + few)) {
+    asm volatile("" : "+s"(own));
+    const AttnArgs l = *(const AttnArgs*)own;
+    few_rows<T, D>(l, b < f0 ? b : b - t0, few);
+  } else {
+    asm volatile("" : "+s"(own));
+    const AttnArgs l = *(const AttnArgs*)own;
+    tile_rows<T, D>(l, b < f0 + t0 ? b - f0 : b - few);
+  }
+}
+
 // ------------------------------------------------------------------ launches
 
-// Workgroups of the few-row kernel at most: as many as the chip holds at once.
-constexpr int few_wgs(int32_t head_dim) { return 256 * few_waves(head_dim); }
+
+// Floats of the few-row kernel's partial results; the tile kernel's lie behind them.
+constexpr size_t few_parts(int32_t head_dim) { return 16 * ((size_t)head_dim + 2) * 2 * few_wgs(head_dim); }
 
 // The tile kernel's workgroups at most: 128 rows each, the last of a request fewer, and those that split the tokens.
 int64_t tile_wgs(int64_t n_requests, int64_t rows, int64_t kv_heads, int32_t dim) {
@@ -1341,17 +1375,23 @@ int64_t tile_wgs(int64_t n_requests, int64_t rows, int64_t kv_heads, int32_t dim
 template <typename T, int D>
 void launch_attn(const AttnArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.n_tokens * a.group;
-  if (a.cu_q || a.group <= kFewRows) {
-    // no more workgroups than the longest requests that the table allows would need
-    const int64_t steps = std::max<int64_t>((((int64_t)a.width << a.shift) + kStep - 1) / kStep, 1);
-    const int64_t tiles = (rows + 15) / 16 + a.n_requests;
-    const int64_t most = std::min<int64_t>(tiles * a.kv_heads, 1 << 20) * steps;
-    const int64_t grid = std::min<int64_t>((most + kMinSteps - 1) / kMinSteps, few_wgs(D));
-    hipLaunchKernelGGL((attn_few_kernel<T, D>), dim3((unsigned)grid), dim3(kAThreads), 0, s, a);
+  // no more workgroups than the longest requests that the table allows would need
+  const int64_t steps = std::max<int64_t>((((int64_t)a.width << a.shift) + kStep - 1) / kStep, 1);
+  const int64_t most = std::min<int64_t>(((rows + 15) / 16 + a.n_requests) * a.kv_heads, 1 << 20) * steps;
+  const unsigned few = (unsigned)std::min<int64_t>((most + kMinSteps - 1) / kMinSteps, few_wgs(D));
+  const unsigned tiles = (unsigned)tile_wgs(a.n_requests, rows, a.kv_heads, D);
+  const bool some_few = a.cu_q || a.group <= kFewRows, some_tiles = a.cu_q ? rows > kFewRows : a.group > kFewRows;
+  if constexpr (D != 256) {
+    // with heads of 64 up to what the chip holds at once: 500 tiles of rows take 41 us, two launches 43; 1000 take 120
+    // and 114, 2000 take 223 and 201 (with heads of 128, 1000 tiles: 318 and 322)
+    const bool one = D != 64 || rows / kTileRows * a.kv_heads <= 2 * (int64_t)kCus;
+    if (some_few && some_tiles && one) {
+      hipLaunchKernelGGL((attn_step_kernel<T, D>), dim3(few + tiles), dim3(kTileThreads), 0, s, a, few, tiles);
+      return;
+    }
   }
-  if (a.cu_q ? rows > kFewRows : a.group > kFewRows)
-    hipLaunchKernelGGL((attn_tile_kernel<T, D>), dim3((unsigned)tile_wgs(a.n_requests, rows, a.kv_heads, D)),
-                       dim3(kTileThreads), 0, s, a);
+  if (some_few) hipLaunchKernelGGL((attn_few_kernel<T, D>), dim3(few), dim3(kAThreads), 0, s, a);
+  if (some_tiles) hipLaunchKernelGGL((attn_tile_kernel<T, D>), dim3(tiles), dim3(kTileThreads), 0, s, a);
 }
 
 template <typename T>
@@ -1373,9 +1413,8 @@ size_t sbm_attention_kv4_workspace_bytes(int32_t n_requests, int32_t n_tokens, i
   if (n_requests < 0 || n_tokens < 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads ||
       !kv_shape_ok(16, head_dim))
     return 0;
-  // the two kernels run one after the other
-  const size_t row = (size_t)head_dim + 2, few = 16 * row * 2 * few_wgs(head_dim), tile = (size_t)kTileRows * row * tile_slots(head_dim);
-  return sizeof(uint32_t) * kCounters + sizeof(float) * std::max(few, tile);
+  const size_t tile = (size_t)kTileRows * ((size_t)head_dim + 2) * tile_slots(head_dim);
+  return sizeof(uint32_t) * kCounters + sizeof(float) * (few_parts(head_dim) + tile);
 }
 
 int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks, int32_t block_size,
