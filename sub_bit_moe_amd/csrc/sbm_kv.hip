@@ -52,7 +52,8 @@ __device__ __forceinline__ int last_at_most(const uint32_t* p, int n, uint32_t v
 // Every workgroup scans all the lengths (at most 4096, so one to sixteen
 // rounds) into its LDS and then fills its share of the tokens and new blocks by
 // binary search: one launch, no workgroup waits for another.  Bound by latency:
-// lengths, scan, search, free list, store.
+// lengths, scan, search, free list, store (64 requests 4 us, 512 requests with
+// 60512 new tokens 6 us).
 __global__ __launch_bounds__(kPThreads) void plan_kernel(PlanArgs a) {
   __shared__ uint32_t s_tok[kMaxRequests + 1], s_need[kMaxRequests + 1];
   __shared__ uint32_t s_wave[2][kPThreads / 64], s_bad;
@@ -250,56 +251,64 @@ struct QkLane {
   bool turn, split, low;     // rotated; with partners eight apart or more; those are the higher ones
 };
 
-// Eight weights, and their partners'.
-struct QkWeights {
-  uint16_t w[8], other[8];
+// A lane's eight elements after the norm, x, and their partners z become x * own + z * with: weight and rotation in one
+// factor each, the same for all the heads.  An element that is not rotated is its own partner, times 0.
+template <typename C>
+struct QkTurn {
+  C own[8], with[8];
 };
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_weights(QkWeights& q, const uint16_t* w, const QkLane& l) {
+template <typename T, typename C, bool kVec>
+__device__ __forceinline__ void load_turn(QkTurn<C>& r, const uint16_t* weight, const QkLane& l) {
   constexpr uint16_t kOne = __is_same(T, __bf16) ? 0x3F80 : 0x3C00;
-  if (w) {
-    load8<kVec>(w + l.d0, q.w);
-    load8<kVec>(w + l.p0, q.other);
+  uint16_t w[8], z[8];
+  if (weight) {
+    load8<kVec>(weight + l.d0, w);
+    load8<kVec>(weight + l.p0, z);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q.w[j] = q.other[j] = kOne;
+    for (int j = 0; j < 8; ++j) w[j] = z[j] = kOne;
   }
-}
-
-// Norm and rotation of a lane's eight elements of one head; C: the type it is computed in.
-template <typename T, typename C, int D, bool kVec>
-__device__ __forceinline__ void norm_rope8(const uint16_t* raw, const uint16_t* other, const QkWeights& w, const QkLane& l,
-                                           const QkArgs& a, uint16_t* out) {
-  C ss = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const C x = (C)to_f32<T>(raw[j]);
-    ss += x * x;
-  }
-  ss = group_sum<D / 8>(ss);
-  const C inv = inverse_root(ss * ((C)1 / (C)D) + (C)a.eps);
-  C y[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = (C)to_f32<T>(raw[j]) * inv * (C)to_f32<T>(w.w[j]);
+  for (int j = 0; j < 8; ++j) r.own[j] = (C)to_f32<T>(w[j]), r.with[j] = (C)0;
   if (l.split) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const C z = (C)to_f32<T>(other[j]) * inv * (C)to_f32<T>(w.other[j]);
-      const C c = (C)l.cos[j], s = (C)l.sin[j];
-      y[j] = l.low ? y[j] * c - z * s : y[j] * c + z * s;
+      r.own[j] *= (C)l.cos[j];
+      r.with[j] = (C)to_f32<T>(z[j]) * (C)(l.low ? -l.sin[j] : l.sin[j]);
     }
   } else if (l.turn) {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const C c = (C)l.cos[j >> 1], s = (C)l.sin[j >> 1];
-      const C u = y[j], v = y[j + 1];
-      y[j] = u * c - v * s;
-      y[j + 1] = v * c + u * s;
+    for (int j = 0; j < 8; ++j) {
+      r.own[j] *= (C)l.cos[j >> 1];
+      r.with[j] = (C)to_f32<T>(w[j ^ 1]) * (C)(j & 1 ? l.sin[j >> 1] : -l.sin[j >> 1]);
     }
   }
+}
+
+__device__ __forceinline__ float fused(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
+__device__ __forceinline__ double fused(double a, double b, double c) { return __builtin_fma(a, b, c); }
+
+// Norm and rotation of a lane's eight elements of one head; C: the type it is computed in.
+template <typename T, typename C, int D>
+__device__ __forceinline__ void norm_rope8(const uint16_t* raw, uint16_t* other, const QkTurn<C>& r, const QkLane& l,
+                                           const QkArgs& a, uint16_t* out) {
+  C x[8], ss = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) out[j] = round_once<T>(y[j]);
+  for (int j = 0; j < 8; ++j) {
+    x[j] = (C)to_f32<T>(raw[j]);
+    ss = fused(x[j], x[j], ss);
+  }
+  ss = group_sum<D / 8>(ss);
+  const C inv = inverse_root(ss * ((C)1 / (C)D) + (C)a.eps);
+  if (l.turn && !l.split) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) other[j] = raw[j ^ 1];
+  }
+  // the norm first: its results are sqrt(D) at most, whatever the elements and the weights are
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    out[j] = round_once<T>(fused((C)to_f32<T>(other[j]) * inv, r.with[j], (x[j] * inv) * r.own[j]));
 }
 
 // Eight of a block's 32 values (four neighbouring lanes hold them) to codes and the block's scale.
@@ -323,20 +332,24 @@ __device__ __forceinline__ uint32_t quantise8(const uint16_t* x, uint32_t* scale
   const int32_t e = (int32_t)(top >> 23) - 2 + ((top & 0x7FFFFFu) > 0x600000u);
   const uint32_t s = (uint32_t)min(max(e, 1), (int32_t)most);
   *scale = s;
+  // the conversion rounds to nearest, ties to even, and takes 7 down to 6; the division is by the multiplication, which keeps
+  // what is below the normal numbers
   const float by = __uint_as_float((254u - s) << 23);
   uint32_t codes = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float m = fabsf(f[j]) * by;
-    const uint32_t c = (m > 0.25f) + (m >= 0.75f) + (m > 1.25f) + (m >= 1.75f) + (m > 2.5f) + (m >= 3.5f) + (m > 5.f);
-    codes |= (c | (__float_as_uint(f[j]) >> 31 << 3)) << (4 * j);
-  }
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[0] * by, f[1] * by, 1.f, 0);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[2] * by, f[3] * by, 1.f, 1);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[4] * by, f[5] * by, 1.f, 2);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[6] * by, f[7] * by, 1.f, 3);
   return codes;
 }
 
 // D / 8 lanes hold a head (16-byte accesses) and take every so-manieth head of one token, so that its cosines and sines
-// and the weights are read once for all of them.  Bound by HBM for prompts, by latency for a few tokens (whose heads are
-// shared out over gridDim.y).
+// and the weights are read, and multiplied with each other, once for all of them.  A wave has a token to itself: with the
+// groups of a workgroup on one token a group has too few heads for that (2000 tokens of 32 + 8 + 8 heads of 128: 14.8, not
+// 11.9 us).  A few tokens' heads are shared out over gridDim.y.  The instructions count: with the products of weight and
+// rotation made for each head, and codes by comparing, 8191 tokens of 40 + 8 + 8 heads of 128 took 59 us, 98 % of them
+// issuing vector instructions; now 45.  Bound by HBM for prompts (4096 tokens of 32 + 8 heads, 86 MB: 17.2 us, 5.0 TB/s),
+// by latency for a few tokens (64 tokens: 4 us).
 template <typename T, int D, bool kVec>
 __global__ __launch_bounds__(kQThreads, 4) void qk_kernel(QkArgs a) {
   constexpr int L = D / 8, kGroups = kQThreads / L;
@@ -391,8 +404,8 @@ __global__ __launch_bounds__(kQThreads, 4) void qk_kernel(QkArgs a) {
   }
   uint16_t y[8];
   if (h < heads) {
-    QkWeights w;
-    load_weights<T, kVec>(w, a.qw, l);
+    QkTurn<float> r;
+    load_turn<T, float, kVec>(r, a.qw, l);
     // kAhead heads are read together
     constexpr int kAhead = 2;
     for (; h < heads; h += kAhead * step) {
@@ -406,7 +419,7 @@ __global__ __launch_bounds__(kQThreads, 4) void qk_kernel(QkArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        norm_rope8<T, float, D, kVec>(raw[i], other[i], w, l, a, y);
+        norm_rope8<T, float, D>(raw[i], other[i], r, l, a, y);
         if (h + i * step < heads) store8<kVec>(a.q_out + t * a.qo_ts + (h + i * step) * a.qo_hs + l.d0, y);
       }
     }
@@ -414,8 +427,8 @@ __global__ __launch_bounds__(kQThreads, 4) void qk_kernel(QkArgs a) {
     h -= ((h - heads) / step) * step;
   }
   if (h >= all) return;
-  QkWeights w;
-  load_weights<T, kVec>(w, a.kw, l);
+  QkTurn<double> r;
+  load_turn<T, double, kVec>(r, a.kw, l);
   const int64_t bs = 1ll << a.shift, row = slot & (bs - 1);
   for (; h < all; h += step) {
     const bool is_v = h >= heads + kv_heads;
@@ -427,7 +440,7 @@ __global__ __launch_bounds__(kQThreads, 4) void qk_kernel(QkArgs a) {
       uint16_t raw[8], other[8];
       load8<kVec>(a.k + t * a.k_ts + kh * a.k_hs + l.d0, raw);
       load8<kVec>(a.k + t * a.k_ts + kh * a.k_hs + l.p0, other);
-      norm_rope8<T, double, D, kVec>(raw, other, w, l, a, y);
+      norm_rope8<T, double, D>(raw, other, r, l, a, y);
       if (a.k_out) store8<kVec>(a.k_out + t * a.ko_ts + kh * a.ko_hs + l.d0, y);
       if (slot < 0) continue;
     }
@@ -441,6 +454,8 @@ __global__ __launch_bounds__(kQThreads, 4) void qk_kernel(QkArgs a) {
 
 // ------------------------------------------------------------------ the cache's reader
 
+// A lane has eight values of a head: 4 bytes of codes read, 16 of values written.  Bound by HBM for prompts (8191 tokens of
+// 8 + 8 heads of 128: 10.5 us, 4.0 TB/s), by latency for a few tokens (64: 2.9 us).
 template <typename T, int D>
 __global__ __launch_bounds__(kQThreads) void load_kernel(const uint8_t* cache, int32_t n_blocks, int32_t kv_heads,
                                                          int32_t shift, const int32_t* slots, uint32_t n_tokens,
@@ -484,9 +499,9 @@ template <typename T, int D>
 void launch_qk(QkArgs a, bool vec, hipStream_t s) {
   constexpr int kGroups = kQThreads / (D / 8);
   const int64_t all = a.heads + a.kv_heads + (a.cache ? a.kv_heads : 0);
-  // as many groups of lanes for a token as it has heads, a workgroup's at most
+  // as many groups of lanes for a token as it has heads, a wave's at most
   a.per_token = 0;
-  while ((1 << a.per_token) < kGroups && (1 << a.per_token) < all) ++a.per_token;
+  while ((1 << a.per_token) < 64 / (D / 8) && (1 << a.per_token) < all) ++a.per_token;
   const int64_t tokens = kGroups >> a.per_token, x = (a.n_tokens + tokens - 1) / tokens;
   const int64_t rounds = (all + (1 << a.per_token) - 1) >> a.per_token;
   const int64_t y = std::min<int64_t>(std::min<int64_t>(rounds, std::max<int64_t>(kQFull / x, 1)), 65535);
