@@ -50,12 +50,18 @@ constexpr float kLn2 = 0.693147180559945309f;
 // The few-row kernel's share of a request's tokens: kStep for a workgroup at a
 // time, 32 for each of its waves.
 constexpr int kStep = 32 * kAWaves;
-constexpr int kMinSteps = 2;              // a workgroup's least work, in steps
-// The tile kernel: rows of a workgroup, and workgroups among which a few long rows are split.
+// A workgroup's least work, in steps.  With heads of 64 a step takes no longer than its place in a join (one request of 1000
+// tokens, 16 heads: 9.5 us, by single steps 10.7), with wider ones it does (pieces of 15 tokens behind up to 722, 16 heads of
+// 256 over 2: 17 us, by pairs 21; short prompts beside single tokens, heads of 128: 14.5 and 17).
+constexpr int min_steps(int dim) { return dim == 64 ? 2 : 1; }
+// The tile kernel: rows of a workgroup, and workgroups among which a few long rows are split, as many as the chip holds
+// at once (1024 tokens behind 19000 others, heads of 128: 210 us, half as many 255).
 constexpr int kTileThreads = 256;
 constexpr int kTileRows = kTileThreads / 2;
 constexpr int tile_slots(int dim) { return dim == 256 ? 256 : 512; }
-// Rows (tokens x heads of one key head) of a request up to which the few-row kernel takes it.
+// Rows (tokens x heads of one key head) of a request up to which the few-row kernel takes it: a tile of 128 rows costs the
+// tile kernel as much with fewer (4 prompts of 89 rows behind up to 3700 tokens, heads of 128: 26 us, as tiles 40; pieces
+// of 15 tokens, 120 rows, heads of 256: 28 and 63).
 constexpr int kFewRows = 128;
 // Counters of the workspace, before the partial results: three levels of joins for each kernel.
 constexpr int kLevels = 3, kFewCounters = 1024;
@@ -442,7 +448,9 @@ __device__ __forceinline__ void init_rows(Rows<D>& s, const AttnArgs& a, int kh,
   for (int kk = 0; kk < D / 32; ++kk) s.q[kk] = load_query<T>(a, q + (D / 4) * g + 8 * kk);
 }
 
-// How many times 32 tokens a wave has under way, and waves on a SIMD, by the registers that takes.
+// How many times 32 tokens a wave has under way, and waves on a SIMD, by the registers that takes (222 of 256 with heads of
+// 256).  Two under way against one: 64 requests of up to 16000 tokens, heads of 128, 121 us and 127; three waves against
+// two: 40 requests of up to 12000 tokens, heads of 64, 50 us and 54.
 constexpr int few_ring(int dim) { return dim == 256 ? 1 : 2; }
 constexpr int few_waves(int dim) { return dim == 64 ? 3 : 2; }
 // Workgroups of the few-row kernel at most: as many as the chip holds at once.
@@ -578,7 +586,9 @@ __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, ui
 // whatever the lengths, its waves 32 tokens each; a run's first and last 16 rows may be
 // shared with neighbours, whose partial results the last one of them to end joins.
 // Bound by HBM with long caches (the codes are read once, K and V of 32 tokens
-// ahead), by latency with short ones.
+// ahead): 64 requests of up to 16000 tokens, 8 key heads of 128 (573 MB) 121 us, 4.7
+// TB/s; two of 250000 (488 MB) 103 us, 4.7 TB/s.  By latency with short ones: one
+// request of 1000 tokens 9.5 us.
 template <typename T, int D>
 __device__ __forceinline__ void few_rows(const AttnArgs& a, const uint32_t block, const uint32_t grid) {
   constexpr int kPad = D + 4;
@@ -611,7 +621,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const uint32_t block
   uint64_t total = 0, pos, stop, per, r_at;            // r_at: the request's first step
   int r;
   auto share = [&] {
-    per = max(quotient(total + grid - 1, grid), (uint64_t)kMinSteps);
+    per = max(quotient(total + grid - 1, grid), (uint64_t)min_steps(D));
     pos = per * block;
     stop = min(pos + per, total);
   };
@@ -1129,7 +1139,8 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, const Request& q) {
 }
 
 // With fewer rows than the chip takes the tokens are split, so many tiles to a part at least (tiles of wide heads take
-// longer; with half of this a join costs more than it saves).
+// longer: 7 requests with four prompts of 194 tokens, heads of 256: 84 us, with parts of eight 92; two prompts of 854
+// tokens, heads of 128: 38 us, with parts of four 48).
 constexpr uint32_t min_tiles(int dim) { return dim == 256 ? 4 : 8; }
 template <int D>
 __device__ __forceinline__ uint32_t parts_of(const Share& s, uint64_t total) {
@@ -1137,6 +1148,12 @@ __device__ __forceinline__ uint32_t parts_of(const Share& s, uint64_t total) {
   return (uint32_t)max(min(parts, (uint64_t)(s.steps / min_tiles(D))), (uint64_t)1);
 }
 
+// A workgroup takes 128 rows of a key head and a run of tiles of tokens: it reads a tile's codes once for all of them, converts
+// V into one half of its LDS while the products read the other.  Four 6-bit pieces of a query cost the matrix pipes what one
+// 16-bit product does, and save K's conversion, the vector instructions being the next limit.  Two prompts of 4000 tokens
+// (32 heads of 128 over 8, 2.6e11 operations): 280 to 299 us by the card, 880 to 935 TFLOP/s, with the matrix pipes busy 43 % of the cycles and the
+// vector pipes 58 %; the clock falls with random data: as two launches zeros took 296 us, normally distributed values 350.  1024 tokens behind 19000 (16 heads of 256 over 4, 3.3e11): 427 us, 768 TFLOP/s, one wave a SIMD, whose
+// products wait for its exponentials.
 template <typename T, int D>
 __device__ __forceinline__ void tile_rows(const AttnArgs& a, const uint32_t block) {
   constexpr int kTokens = Tile<D>::kTokens;
@@ -1378,7 +1395,7 @@ void launch_attn(const AttnArgs& a, hipStream_t s) {
   // no more workgroups than the longest requests that the table allows would need
   const int64_t steps = std::max<int64_t>((((int64_t)a.width << a.shift) + kStep - 1) / kStep, 1);
   const int64_t most = std::min<int64_t>(((rows + 15) / 16 + a.n_requests) * a.kv_heads, 1 << 20) * steps;
-  const unsigned few = (unsigned)std::min<int64_t>((most + kMinSteps - 1) / kMinSteps, few_wgs(D));
+  const unsigned few = (unsigned)std::min<int64_t>((most + min_steps(D) - 1) / min_steps(D), few_wgs(D));
   const unsigned tiles = (unsigned)tile_wgs(a.n_requests, rows, a.kv_heads, D);
   const bool some_few = a.cu_q || a.group <= kFewRows, some_tiles = a.cu_q ? rows > kFewRows : a.group > kFewRows;
   if constexpr (D != 256) {
