@@ -1151,9 +1151,10 @@ __device__ __forceinline__ uint32_t parts_of(const Share& s, uint64_t total) {
 // A workgroup takes 128 rows of a key head and a run of tiles of tokens: it reads a tile's codes once for all of them, converts
 // V into one half of its LDS while the products read the other.  Four 6-bit pieces of a query cost the matrix pipes what one
 // 16-bit product does, and save K's conversion, the vector instructions being the next limit.  Two prompts of 4000 tokens
-// (32 heads of 128 over 8, 2.6e11 operations): 280 to 299 us by the card, 880 to 935 TFLOP/s, with the matrix pipes busy 43 % of the cycles and the
-// vector pipes 58 %; the clock falls with random data: as two launches zeros took 296 us, normally distributed values 350.  1024 tokens behind 19000 (16 heads of 256 over 4, 3.3e11): 427 us, 768 TFLOP/s, one wave a SIMD, whose
-// products wait for its exponentials.
+// (32 heads of 128 over 8, 2.6e11 operations): 280 to 299 us by the card, 880 to 935 TFLOP/s, with the matrix pipes busy 43 %
+// of the cycles and vector instructions issued in 58 %; the clock falls with random data (as two launches zeros took 296 us,
+// normally distributed values 350).  1024 tokens behind 19000 (16 heads of 256 over 4, 3.3e11): 427 us, 766 TFLOP/s, one wave
+// a SIMD, whose products wait for its exponentials (matrix pipes busy 33 %).
 template <typename T, int D>
 __device__ __forceinline__ void tile_rows(const AttnArgs& a, const uint32_t block) {
   constexpr int kTokens = Tile<D>::kTokens;

@@ -348,7 +348,8 @@ __device__ __forceinline__ uint32_t quantise8(const uint16_t* x, uint32_t* scale
 // groups of a workgroup on one token a group has too few heads for that (2000 tokens of 32 + 8 + 8 heads of 128: 14.8, not
 // 11.9 us).  A few tokens' heads are shared out over gridDim.y.  The instructions count: with the products of weight and
 // rotation made for each head, and codes by comparing, 8191 tokens of 40 + 8 + 8 heads of 128 took 59 us, 98 % of them
-// issuing vector instructions; now 45.  Bound by HBM for prompts (4096 tokens of 32 + 8 heads, 86 MB: 17.2 us, 5.0 TB/s),
+// issuing vector instructions; now 42 us (5.0 TB/s) and 79 %.  Bound by HBM for prompts (4096 tokens of 32 + 8 heads, 86 MB:
+// 17.2 us, 5.0 TB/s),
 // by latency for a few tokens (64 tokens: 4 us).
 template <typename T, int D, bool kVec>
 __global__ __launch_bounds__(kQThreads, 4) void qk_kernel(QkArgs a) {
