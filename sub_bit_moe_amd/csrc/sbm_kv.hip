@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kPThreads) void plan_kernel(PlanArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, R = a.n_requests;
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  uint32_t tok0 = 0, need0 = 0;                  // sums before this round
+  uint32_t tok0 = 0, need0 = 0;                  // sums before these lengths
   for (int base = 0; base < R; base += kPThreads) {
     const int r = base + tid;
     uint32_t tok = 0, need = 0;
