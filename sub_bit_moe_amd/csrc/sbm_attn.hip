@@ -41,10 +41,13 @@ namespace {
 constexpr int kAThreads = 256;
 constexpr int kAWaves = kAThreads / 64;
 // P is held as exp2(z - m) with m = (the row's maximum when m was last raised)
-// - kBias, and m is raised when a score passes that maximum by kSlack: P stays
-// below 2^15, which fp16 holds, and a score has to be 32 below the maximum (in
-// powers of two) before fp16 drops it.
-constexpr float kBias = 8.f, kSlack = 7.f;
+// - bias, and m is raised when a score passes that maximum by kSlack.  fp16: P stays
+// below 2^15, which the type holds, and a score has to be 32 below the maximum (in
+// powers of two) before it is dropped.  bf16: P is at most 1, so that a sum of P v is
+// no larger than that of |v|, which may be near the largest that 32 bits hold.
+constexpr float kSlack = 7.f;
+template <typename T>
+constexpr float kBias = __is_same(T, __bf16) ? -kSlack : 8.f;
 constexpr float kLowest = -3.0e38f;       // m before the first score
 constexpr float kLn2 = 0.693147180559945309f;
 // The few-row kernel's share of a request's tokens: kStep for a workgroup at a
@@ -389,10 +392,10 @@ __device__ __forceinline__ void step(Rows<D>& s, const Raw<D>& r, const AttnArgs
   }
   // P^T = exp2(scale2 * S^T - m)
   float top = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7]))) * a.scale2;
-  if (__builtin_expect(__any(top > s.m + (kBias + kSlack)), 0)) {
+  if (__builtin_expect(__any(top > s.m + (kBias<T> + kSlack)), 0)) {
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const float to = fmaxf(s.m, top - kBias), by = __builtin_amdgcn_exp2f(s.m - to);
+    const float to = fmaxf(s.m, top - kBias<T>), by = __builtin_amdgcn_exp2f(s.m - to);
     s.m = to;
     s.l *= by;
 #pragma unroll
@@ -1039,9 +1042,9 @@ __device__ __forceinline__ void tile_products(TileRows<T, D>& s, const Tile<D>& 
   };
   auto raise = [&](float top) {
     top *= scale2;
-    if (__builtin_expect(__any(top > s.m + (kBias + kSlack)), 0)) {
+    if (__builtin_expect(__any(top > s.m + (kBias<T> + kSlack)), 0)) {
       top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float to = fmaxf(s.m, top - kBias), by = __builtin_amdgcn_exp2f(s.m - to);
+      const float to = fmaxf(s.m, top - kBias<T>), by = __builtin_amdgcn_exp2f(s.m - to);
       s.m = to;
       s.l *= by;
 #pragma unroll
