@@ -504,7 +504,8 @@ size_t sbm_attention_kv4_workspace_bytes(int32_t n_requests, int32_t n_tokens, i
  *             before its first use; every call leaves it ready for the next (calls
  *             that share one must not overlap).  n_requests <= 4096
  * fp16: cached values may be read as fp16 (magnitudes above 65504 become
- * infinite; a cache written from fp16 holds none). */
+ * infinite to the rows that see them, and to no others; a cache written from
+ * fp16 holds none). */
 int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks, int32_t block_size,
                       const int32_t* block_table, int32_t table_width, const int32_t* kv_lens, const int32_t* cu_q,
                       int32_t n_requests, int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,

@@ -114,6 +114,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 __device__ __forceinline__ float exponent(uint32_t s) { return __uint_as_float(s << 23); }
 
+// A block of values is odd where the type does not hold all that its scale and codes may give: the scale is NaN's, or one
+// past those that the cache's writer uses for the type, under which large codes become infinite.  0 times such a value is
+// NaN, so where some row does not see a token with odd blocks these go into the product as zeros (or nearly, 2^-127
+// of their codes with bf16), and what they are to the rows that see them is added by itself (add_odd, tile_add_odd).
+template <typename T>
+__device__ __forceinline__ bool is_odd(uint32_t scale) {
+  return scale > (__is_same(T, __bf16) ? 252u : 140u);
+}
+
+template <typename T>
+__device__ __forceinline__ float low_f32(uint32_t w) {
+  return (float)__builtin_bit_cast(T, (uint16_t)w);
+}
+
 // Eight of a query's dimensions, with the scale's sign.
 template <typename T>
 __device__ __forceinline__ u32x4 load_query(const AttnArgs& a, const uint16_t* q) {
@@ -331,24 +345,39 @@ struct Rows {
   f32x4 o[D / 16];
   float m, l;
   int last;                    // the last position that the lane's row sees, -1: none
-  uint32_t nan;                // bit i: the outputs o[.][i] are NaN
 };
 
-// Notes the rows that see a token whose values have a NaN, where that token
-// went into the products as if it had none (a masked step, some rows not seeing it).
-template <int D>
-__device__ __forceinline__ void nan_values(Rows<D>& s, const AttnArgs& a, const int32_t* table, int kh, int t0, int end,
+// Adds what the odd blocks of 32 tokens are to the rows that see them, where they went into the products as
+// nothing (a masked step).  p: the step's probabilities as the product took them.
+template <typename T, int D>
+__device__ __forceinline__ void add_odd(Rows<D>& s, u32x4 p, const AttnArgs& a, const int32_t* table, int kh, int t0, int end,
                                         int lane) {
-  const int bs = 1 << a.shift, g = lane >> 4;
-  for (int t = t0; t < min(t0 + 32, end); ++t) {
+  constexpr int E = D / 16;
+  const int bs = 1 << a.shift, g = lane >> 4, n = min(end - t0, 32);
+  for (int i = 0; i < n; ++i) {
+    const int t = t0 + i;
     const int32_t b = table[t >> a.shift];
     if ((uint32_t)b >= (uint32_t)a.n_blocks) continue;
-    const uint8_t* vs = a.cache + ((int64_t)b * a.kv_heads + kh) * kv_record_bytes(bs, D) + bs * D + bs * (D / 32) +
-                        (t & (bs - 1)) * (D / 32);
+    // token i's probabilities: element 4 (i / 16) + i % 4 of the lanes with g = i / 4 % 4
+    const int pair = 2 * (i >> 4) + (i >> 1 & 1);
+    uint32_t w = pair & 2 ? (pair & 1 ? p[3] : p[2]) : (pair & 1 ? p[1] : p[0]);
+    w = (uint32_t)__shfl((int)w, (i >> 2 & 3) * 16 + (lane & 15), 64);
+    const float by = low_f32<T>(i & 1 ? w >> 16 : w);
+    if (t > s.last) continue;
+    const uint8_t* rec = a.cache + ((int64_t)b * a.kv_heads + kh) * kv_record_bytes(bs, D);
+    const uint8_t *vc = rec + (bs + (t & (bs - 1))) * (D / 2), *vs = rec + bs * D + (bs + (t & (bs - 1))) * (D / 32);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // rows 4g + i of an output tile are dimensions (4g + i) D / 16 and on
-      if (vs[(4 * g + i) * (D / 16) / 32] == kScaleNaN && t <= s.last) s.nan |= 1u << i;
+    for (int j = 0; j < 4; ++j) {
+      // o[.][j] are dimensions (4g + j) E and on
+      const int d = (4 * g + j) * E;
+      const uint32_t scale = vs[d / 32];
+      if (!is_odd<T>(scale)) continue;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const uint32_t v = cvt_fp4<T, 0>(vc[(d + e) / 2], exponent(scale));
+        s.o[e][j] += by * low_f32<T>(v);
+        s.o[e + 1][j] += by * low_f32<T>(v >> 16);
+      }
     }
   }
 }
@@ -376,7 +405,7 @@ __device__ __forceinline__ void step(Rows<D>& s, const Raw<D>& r, const AttnArgs
   uint32_t vs[8];
   value_scales<D>(r.vs[0], m * (D / 16) / 32, vs);
   value_scales<D>(r.vs[1], m * (D / 16) / 32, vs + 4);
-  bool odd_v = false;            // a NaN among the values of tokens that not every row sees
+  bool odd_v = false;            // odd blocks among the values of tokens that not every row sees
   float z[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) z[j] = sc[j >> 2][j & 3];
@@ -384,9 +413,9 @@ __device__ __forceinline__ void step(Rows<D>& s, const Raw<D>& r, const AttnArgs
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
-      const bool there = r.ok[j >> 2] && t < end, nan = (vs[j] & 0x7F800000u) == 0x7F800000u;
-      odd_v = odd_v || (there && nan);
-      if (!there || nan) vs[j] = 0x3F800000u;      // 0 * NaN is NaN: what is not seen has to be finite
+      const bool there = r.ok[j >> 2] && t < end, odd = is_odd<T>(vs[j] >> 23 & 255u);
+      odd_v = odd_v || (there && odd);
+      if (!there || odd) vs[j] = 0;                // 0 * NaN is NaN: what is not seen has to be finite
       if (t > s.last || !r.ok[j >> 2]) z[j] = -INFINITY;
     }
   }
@@ -433,7 +462,7 @@ __device__ __forceinline__ void step(Rows<D>& s, const Raw<D>& r, const AttnArgs
     pair(std::integral_constant<int, 6>{});
     pair(std::integral_constant<int, 7>{});
   }
-  if (masked && __any(odd_v)) nan_values<D>(s, a, table, kh, t0, end, lane);
+  if (masked && __builtin_expect(__any(odd_v), 0)) add_odd<T, D>(s, p, a, table, kh, t0, end, lane);
 }
 
 template <typename T, int D>
@@ -442,7 +471,6 @@ __device__ __forceinline__ void init_rows(Rows<D>& s, const AttnArgs& a, int kh,
   s.last = i < rq.n ? min(rq.kv - rq.n + i, rq.kv - 1) : -1;
   s.m = kLowest;
   s.l = 0.f;
-  s.nan = 0;
 #pragma unroll
   for (int e = 0; e < D / 16; ++e) s.o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
   const uint16_t* q =
@@ -723,7 +751,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const uint32_t block
     if (rl < nr) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float by = s.nan >> j & 1u ? NAN : __builtin_amdgcn_exp2f(s.m - m);
+        const float by = __builtin_amdgcn_exp2f(s.m - m);
 #pragma unroll
         for (int e = 0; e < D / 16; e += 4)
           *(float4*)&s_o[wave][rl][(D / 4) * g + (D / 16) * j + e] =
@@ -924,10 +952,10 @@ __device__ __forceinline__ void fetch(Fetch<D>& f, const AttnArgs& a, const Bloc
 
 // The fetched part into LDS, V converted, in kPutSteps steps after the first.
 // border: some row of the workgroup does not see all of the tile.  Returns what
-// the waves have to know: a bit for each 16 tokens without a block, kNoteNaN: a NaN among V that went in as 1.
-constexpr uint32_t kNoteNaN = 1u << 31;
+// the waves have to know: a bit for each 16 tokens without a block, kNoteOdd: odd blocks among V that went in as nothing.
+constexpr uint32_t kNoteOdd = 1u << 31;
 constexpr int kPutSteps = 5;
-template <int D>
+template <typename T, int D>
 __device__ __forceinline__ uint32_t prepare_values(const Fetch<D>& f, uint32_t (&sc)[4], int t0, int end, bool border, int unit) {
   const int u = unit >> 1, c = u % (D / 8), h = u / (D / 8) & 1, tb = unit / (D / 2), half = unit & 1;
   uint32_t note = 0;
@@ -937,9 +965,9 @@ __device__ __forceinline__ uint32_t prepare_values(const Fetch<D>& f, uint32_t (
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool there = f.ok && t0 + 16 * tb + 8 * half + 4 * h + i < end;
-      const bool nan = (sc[i] & 0x7F800000u) == 0x7F800000u;
-      if (there && nan) note |= kNoteNaN;
-      if (!there || nan) sc[i] = 0x3F800000u;         // 0 * NaN is NaN: what is not seen has to be finite
+      const bool odd = is_odd<T>(sc[i] >> 23 & 255u);
+      if (there && odd) note |= kNoteOdd;
+      if (!there || odd) sc[i] = 0;                   // 0 * NaN is NaN: what is not seen has to be finite
     }
   }
   return note;
@@ -973,22 +1001,56 @@ struct TileRows {
   f32x16 o[D / 32];
   float m, l;
   int last;
-  uint32_t nan;                // bit db: the outputs o[db] are NaN
 };
 
-// As nan_values.  o[db][i] is dimension 32 db + 16 h + 4 (i % 4) + i / 4.
+// As add_odd, after a tile's products.  Their probabilities are gone, so those of the tokens with odd blocks are computed anew
+// (behind each 32 tokens, with them still there, the branch alone cost 2 % with heads of 256).  o[db][i] is dimension
+// 32 db + 16 h + 4 (i % 4) + i / 4.
 template <typename T, int D>
-__device__ __forceinline__ void tile_nan_values(TileRows<T, D>& s, const AttnArgs& a, const int32_t* table, int kh, int t0,
-                                             int end) {
+__device__ __forceinline__ void tile_add_odd(TileRows<T, D>& s, const AttnArgs& a, const int32_t* table, int kh, int t0, int end,
+                                             const uint16_t* query, int h) {
   const int bs = 1 << a.shift;
   for (int t = t0; t < min(t0 + Tile<D>::kTokens, end); ++t) {
     const int32_t b = table[t >> a.shift];
     if ((uint32_t)b >= (uint32_t)a.n_blocks) continue;
-    const uint8_t* vs = a.cache + ((int64_t)b * a.kv_heads + kh) * kv_record_bytes(bs, D) + bs * D + bs * (D / 32) +
-                        (t & (bs - 1)) * (D / 32);
+    const int row = t & (bs - 1);
+    const uint8_t* rec = a.cache + ((int64_t)b * a.kv_heads + kh) * kv_record_bytes(bs, D);
+    const uint8_t *kc = rec + row * (D / 2), *vc = kc + bs * (D / 2), *ks = rec + bs * D + row * (D / 32), *vs = ks + bs * (D / 32);
+    bool any = false;
+    for (int db = 0; db < D / 32; ++db) any = any || is_odd<T>(vs[db]);
+    if (!any) continue;
+    float z = 0.f;                                     // half of the dimensions in each half of the wave
+#pragma unroll 1
+    for (int d = 16 * h; d < D; d += 32) {
+      float sum = 0.f;
+#pragma unroll 1
+      for (int x = 0; x < 16; x += 8) {
+        const u32x4 q = load_query<T>(a, query + d + x);
 #pragma unroll
-    for (int db = 0; db < D / 32; ++db)
-      if (vs[db] == kScaleNaN && t <= s.last) s.nan |= 1u << db;
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t k = cvt_fp4<T, 0>(kc[(d + x) / 2 + y], 1.f);
+          sum += low_f32<T>(q[y]) * low_f32<T>(k) + low_f32<T>(q[y] >> 16) * low_f32<T>(k >> 16);
+        }
+      }
+      const uint32_t e = ks[d / 32];
+      z += sum * (e == kScaleNaN ? NAN : __builtin_ldexpf(1.f, (int)e - 127));
+    }
+    z += __shfl_xor(z, 32, 64);
+    if (t > s.last) continue;
+    const float by = (float)(T)__builtin_amdgcn_exp2f(__builtin_fmaf(z, a.scale2, -s.m));
+#pragma unroll
+    for (int db = 0; db < D / 32; ++db) {
+      if constexpr (D == 256) asm volatile("" : "+a"(s.o[db]));   // where tile_products has them: registers
+      const uint32_t scale = vs[db];
+      if (!is_odd<T>(scale)) continue;
+#pragma unroll
+      for (int d = 0; d < 16; d += 2) {
+        const uint32_t v = cvt_fp4<T, 0>(vc[16 * db + 8 * h + d / 2], exponent(scale));
+        s.o[db][d % 4 * 4 + d / 4] += by * low_f32<T>(v);
+        s.o[db][(d + 1) % 4 * 4 + d / 4] += by * low_f32<T>(v >> 16);
+      }
+      if constexpr (D == 256) asm volatile("" : "+a"(s.o[db]));
+    }
   }
 }
 
@@ -1239,16 +1301,14 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, const uint32_t bloc
   s.last = i < rq.n ? rq.kv - rq.n + i : -1;
   s.m = kLowest;
   s.l = 0.f;
-  s.nan = 0;
 #pragma unroll
   for (int db = 0; db < D / 32; ++db)
 #pragma unroll
     for (int x = 0; x < 16; ++x) s.o[db][x] = 0.f;
-  {
-    const uint16_t* q = a.q + (int64_t)(rq.q0 + min(i, rq.n - 1)) * a.q_ts + (int64_t)(kh * a.group + row % a.group) * a.q_hs;
+  const uint16_t* query =
+      a.q + (int64_t)(rq.q0 + min(i, rq.n - 1)) * a.q_ts + (int64_t)(kh * a.group + row % a.group) * a.q_hs;
 #pragma unroll
-    for (int kb = 0; kb < D / 64; ++kb) s.qs[kb] = split_query<T>(a, q + 64 * kb + 32 * h, s.q[kb]);
-  }
+  for (int kb = 0; kb < D / 64; ++kb) s.qs[kb] = split_query<T>(a, query + 64 * kb + 32 * h, s.q[kb]);
   constexpr int kUnits = Tile<D>::kUnits;
   constexpr auto kUnitList = std::make_integer_sequence<int, kUnits>{};
   const int unit_t = 16 * (64 * wave / (D / 2));        // the first of a wave's units' tokens
@@ -1277,7 +1337,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, const uint32_t bloc
     uint32_t note = 0;
     each([&](auto u) {
       const int unit = tid + u * kTileThreads;
-      note |= prepare_values<D>(f[u], sc[u], t0, end, t0 + kTokens - 1 > first, unit);
+      note |= prepare_values<T, D>(f[u], sc[u], t0, end, t0 + kTokens - 1 > first, unit);
       if (real && !f[u].ok && t0 + 16 * (unit / (D / 2)) < end && a.error) atomicOr(a.error, kErrBlock);
     }, kUnitList);
     if (__builtin_expect(real && note != 0, 0)) atomicOr(&s_note[j & 3], note);
@@ -1304,16 +1364,11 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, const uint32_t bloc
       const int jn = min(j + 1, j1 - 1);
       tile_products<T, D>(s, s_tile[j & 1], t0, masked, note, a.scale2, lane,
                           [&](auto part) { load(part, jn); }, [&] { prepare(jn, j + 1 < j1); }, [&](auto step) { put(step, j + 1); });
-      if (__builtin_expect(note & kNoteNaN, 0)) tile_nan_values<T, D>(s, a, table, kh, t0, end);
+      if (__builtin_expect(note & kNoteOdd, 0)) tile_add_odd<T, D>(s, a, table, kh, t0, end, query, h);
       __syncthreads();
     }
   }
   s.l += __shfl_xor(s.l, 32, 64);
-  if (__any(s.nan)) {
-#pragma unroll
-    for (int db = 0; db < D / 32; ++db)
-      if (s.nan >> db & 1u) s.o[db] *= NAN;
-  }
   const bool valid = row - row0 < nr;
   const int64_t at = (int64_t)(rq.q0 + i) * a.heads + kh * a.group + row % a.group;
   if (parts == 1) {
