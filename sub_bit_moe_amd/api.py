@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import struct
+import threading
 from dataclasses import dataclass
 
 import numpy as np
@@ -490,7 +491,8 @@ class KVPlan:
     block_table: object
 
 
-_error_words = {}                                  # (device, stream) -> [zeroed int32 words, how many were given out]
+_error_words = {}                                  # (device, stream) -> (zeroed int32 words, how many were given out)
+_error_lock = threading.Lock()                     # threads share the default stream
 
 
 def _error_word(at: int):
@@ -498,11 +500,13 @@ def _error_word(at: int):
     import torch
     if torch.cuda.is_current_stream_capturing():   # the graph zeroes it at each replay
         return torch.zeros(1, dtype=torch.int32, device=f"cuda:{at}")
-    pool = _error_words.setdefault((at, _stream()), [None, 1024])
-    if pool[1] == 1024:
-        pool[:] = torch.zeros(1024, dtype=torch.int32, device=f"cuda:{at}"), 0
-    pool[1] += 1
-    return pool[0][pool[1] - 1:pool[1]]
+    key = at, _stream()
+    with _error_lock:
+        words, given = _error_words.get(key, (None, 1024))
+        if given == 1024:
+            words, given = torch.zeros(1024, dtype=torch.int32, device=f"cuda:{at}"), 0
+        _error_words[key] = words, given + 1
+    return words[given:given + 1]
 
 
 def alloc_kv_plan(n_requests: int, max_tokens: int, block_table=None, device="cuda") -> KVPlan:
