@@ -3,6 +3,10 @@
 Every step of the codec and of the fused decode + matvec runs in libsbm.so
 (host C++ for dictionary/encoding, HIP kernels on the GPU).  numpy arrays are
 used for host buffers, torch tensors for device memory and streams.
+
+A call with stream= runs on that stream, which has to have waited for whatever
+wrote the call's inputs.  Results and workspaces that the call makes belong to
+that stream; another one waits for it before it reads them.
 """
 from __future__ import annotations
 
@@ -42,6 +46,16 @@ def _stream(stream=None) -> int:
         else:
             _current_stream = lambda: raw(device())                                  # noqa: E731
     return _current_stream()
+
+
+def _made_on(stream, make, *args, **kw):
+    """make(*args, **kw), a tensor that a call on `stream` writes: allocated, and filled, on that stream.  Memory of the
+    current stream could still be in use there, or be given out again there before the call has written it."""
+    if stream is None:
+        return make(*args, **kw)
+    import torch
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
 
 # ------------------------------------------------------------------ dictionary
 
@@ -240,9 +254,9 @@ def decode_ref(codes_t, row_off_t, rows: int, cols: int, words_t, stream=None, o
     """GPU reference decode of one matrix -> (symbols uint8 [rows, cols], bad_rows)."""
     import torch
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.uint8, device=codes_t.device)
+        out = _made_on(stream, torch.empty, (rows, cols), dtype=torch.uint8, device=codes_t.device)
     if bad is None:
-        bad = torch.zeros(1, dtype=torch.int32, device=codes_t.device)
+        bad = _made_on(stream, torch.zeros, 1, dtype=torch.int32, device=codes_t.device)
     check(lib().sbm_decode_ref(_ptr(codes_t), _ptr(row_off_t), rows, cols, _ptr(words_t), _ptr(out),
                                _ptr(bad), _stream(stream)))
     return out, bad
@@ -254,9 +268,9 @@ def decode_dense(stack: "ExpertStack", e: int, image_t, out=None, bad=None, stre
     import torch
     d = stack.host_desc[e]
     if out is None:
-        out = torch.empty((stack.rows, stack.cols), dtype=torch.float16, device=stack.codes.device)
+        out = _made_on(stream, torch.empty, (stack.rows, stack.cols), dtype=torch.float16, device=stack.codes.device)
     if bad is None:
-        bad = torch.zeros(1, dtype=torch.int32, device=stack.codes.device)
+        bad = _made_on(stream, torch.zeros, 1, dtype=torch.int32, device=stack.codes.device)
     check(lib().sbm_decode_dense(_ptr(stack.codes[d.code_base:]), int(d.n_codes), _ptr(stack.bstart[d.blk_base:]),
                                  stack.rows, stack.cols, _ptr(image_t), int(d.dict_tag), _ptr(out), _ptr(bad),
                                  _stream(stream)))
@@ -295,10 +309,10 @@ def moe_fused_decode_matvec(stack: ExpertStack, image_t, x, expert_ids, relu: bo
     import torch
     T = int(x.shape[0]) if x is not None else 0
     if y is None:
-        y = torch.empty((T, stack.rows), dtype=torch.float32 if out_f32 else torch.float16,
-                        device=stack.codes.device)
+        y = _made_on(stream, torch.empty, (T, stack.rows), dtype=torch.float32 if out_f32 else torch.float16,
+                     device=stack.codes.device)
     if workspace is None:
-        workspace = alloc_workspace(stack.n_experts, T, device=stack.codes.device)
+        workspace = _made_on(stream, alloc_workspace, stack.n_experts, T, device=stack.codes.device)
     flags = (N.SBM_F_RELU if relu else 0) | (N.SBM_F_OUT_F32 if out_f32 else 0) | (N.SBM_F_IN_RMS if in_rms else 0)
     flags |= N.SBM_F_MFMA if mfma else 0
     flags |= N.SBM_F_MINMAX if minmax else 0
@@ -343,11 +357,11 @@ def moe_fused_ffn(up: ExpertStack, down: ExpertStack, image_t, x, expert_ids, h=
     T = int(x.shape[0])
     dev = up.codes.device
     if h is None:
-        h = torch.empty((T, up.rows), dtype=torch.float16, device=dev)
+        h = _made_on(stream, torch.empty, (T, up.rows), dtype=torch.float16, device=dev)
     if y is None:
-        y = torch.empty((T, down.rows), dtype=torch.float32 if out_f32 else torch.float16, device=dev)
+        y = _made_on(stream, torch.empty, (T, down.rows), dtype=torch.float32 if out_f32 else torch.float16, device=dev)
     if workspace is None:
-        workspace = alloc_ffn_workspace(up.n_experts, T, dev)
+        workspace = _made_on(stream, alloc_ffn_workspace, up.n_experts, T, dev)
     flags = (N.SBM_F_IN_RMS if in_rms else 0) | (N.SBM_F_OUT_F32 if out_f32 else 0) | _x_flag(x)
     pu, pd = _projection(up), _projection(down)
     check(lib().sbm_moe_fused_ffn(C.addressof(pu), C.addressof(pd), _ptr(image_t), _ptr(x), _ptr(expert_ids), T,
@@ -379,12 +393,12 @@ def moe_fused_layers(ups, downs, image_t, x, expert_ids, h=None, y=None, workspa
     T = int(x.shape[0])
     dev = ups[0].codes.device
     if h is None:
-        h = torch.empty((L, T, ups[0].rows), dtype=torch.float16, device=dev)
+        h = _made_on(stream, torch.empty, (L, T, ups[0].rows), dtype=torch.float16, device=dev)
     if y is None:
-        y = torch.empty((L, T, downs[0].rows), dtype=torch.float16, device=dev)
+        y = _made_on(stream, torch.empty, (L, T, downs[0].rows), dtype=torch.float16, device=dev)
     assert h.numel() >= L * T * ups[0].rows and y.numel() >= L * T * downs[0].rows
     if workspace is None:
-        workspace = alloc_layers_workspace(L, ups[0].n_experts, T, dev)
+        workspace = _made_on(stream, alloc_layers_workspace, L, ups[0].n_experts, T, dev)
     flags = (N.SBM_F_IN_RMS if in_rms else 0) | _x_flag(x)
     pu = (N.Projection * L)(*[_projection(u) for u in ups])
     pd = (N.Projection * L)(*[_projection(d) for d in downs])
@@ -540,11 +554,7 @@ def kv_plan(context_lens, new_lens, free_blocks, n_free, block_table, n_blocks: 
            _dev(free_blocks, "free_blocks", i32, at), free_blocks.numel(), _dev(n_free, "n_free", i32, at),
            _dev(block_table, "block_table", i32, at))
     if plan is None:
-        if stream is None:
-            plan = alloc_kv_plan(R, max_tokens, block_table)
-        else:
-            with torch.cuda.stream(stream):
-                plan = alloc_kv_plan(R, max_tokens, block_table)
+        plan = _made_on(stream, alloc_kv_plan, R, max_tokens, block_table)
         n = 4 * max_tokens
         p = plan.cu_q.data_ptr() - 3 * n           # one buffer, in this order
         outs = (p, p + n, p + 2 * n, p + 3 * n, p + 3 * n + 4 * R + 4, p + 3 * n + 8 * R + 4, plan.error.data_ptr())
@@ -587,12 +597,12 @@ def _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours,
             raise ValueError(f"positions must hold {T} elements")
         pos = _dev(positions, "positions", torch.int32, at)
     if q_out is None:
-        q_out = q.new_empty(shape)
+        q_out = _made_on(stream, q.new_empty, shape)
         ho = _pack_heads(q_out.data_ptr(), H * D, D)
     else:
         ho = _heads(q_out, "q_out", dtype, at, shape)
     if k_out is None and cache is None:
-        k_out = q.new_empty(kshape)
+        k_out = _made_on(stream, q.new_empty, kshape)
         hko = _pack_heads(k_out.data_ptr(), Hk * D, D)
     else:
         hko = None if k_out is None else _heads(k_out, "k_out", dtype, at, kshape)
@@ -651,9 +661,9 @@ def kv_load(cache: KVCache, slots, dtype=None, k=None, v=None, error=None, strea
     data, nb, Hk = _cache(cache, at)
     shape = (n, Hk, cache.head_dim)
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=slots.device)
+        k = _made_on(stream, torch.empty, shape, dtype=dtype, device=slots.device)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=slots.device)
+        v = _made_on(stream, torch.empty, shape, dtype=dtype, device=slots.device)
     if k.shape != shape or v.shape != shape:
         raise ValueError(f"k and v must be {shape}, not {tuple(k.shape)} and {tuple(v.shape)}")
     check(lib().sbm_kv_load(data, nb, Hk, cache.block_size, cache.head_dim, _slots(slots, n, at), n, _dev(k, "k", dtype, at),
@@ -696,7 +706,7 @@ def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: flo
     hq = _heads(q, "q", dtype, at, shape)
     data, nb, _ = _cache(cache, at)
     if out is None:
-        out = q.new_empty(shape)
+        out = _made_on(stream, q.new_empty, shape)
         po = out.data_ptr()
     elif out.shape != shape:
         raise ValueError(f"out must be {tuple(shape)}, not {tuple(out.shape)}")
@@ -708,14 +718,10 @@ def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: flo
             raise ValueError(f"lse must be {(T, H)}, not {tuple(lse.shape)}")
         pl = _dev(lse, "lse", torch.float32, at)
     elif return_lse:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _made_on(stream, torch.empty, (T, H), dtype=torch.float32, device=q.device)
         pl = lse.data_ptr()
     if workspace is None:
-        if stream is None:
-            workspace = alloc_attention_workspace(R, T, H, Hk, D, q.device)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = alloc_attention_workspace(R, T, H, Hk, D, q.device)
+        workspace = _made_on(stream, alloc_attention_workspace, R, T, H, Hk, D, q.device)
     check(lib().sbm_attention_kv4(
         hq, data, nb, cache.block_size, _dev(block_table, "block_table", i32, at), block_table.shape[1],
         _dev(kv_lens, "kv_lens", i32, at), 0 if cu_q is None else _dev(cu_q, "cu_q", i32, at), R, T, H, Hk, D,
@@ -771,6 +777,6 @@ def rms_glue(y, out=None, stream=None):
     """Stack glue (not the method): x_next = y / rms(y) per token, fp16."""
     import torch
     if out is None:
-        out = torch.empty_like(y)
+        out = _made_on(stream, torch.empty_like, y)
     check(lib().sbm_rms_glue(_ptr(y), int(y.shape[0]), int(y.shape[1]), _ptr(out), _stream(stream)))
     return out
