@@ -745,9 +745,13 @@ def generate_stack(seed: int, layer: int, n_experts: int, mat: int, rows: int, c
     dict_checksum: the checksum of the dictionary the trie was built from."""
     import torch
     from . import synth
+    if stream is not None:                             # sizes are read back and buffers made between the passes
+        with torch.cuda.stream(stream):
+            return generate_stack(seed, layer, n_experts, mat, rows, cols, p0, trie_t, scale_table_t,
+                                  dict_checksum=dict_checksum)
     dev = trie_t.device
     z = synth.zero_threshold16(p0)
-    s = _stream(stream)
+    s = _stream()
     counts = torch.empty(n_experts * rows, dtype=torch.int32, device=dev)
     check(lib().sbm_gen_count(seed, layer, n_experts, mat, rows, cols, z, _ptr(trie_t), _ptr(counts), s))
     row_off = torch.empty(n_experts * (rows + 1), dtype=torch.int32, device=dev)

@@ -22,9 +22,12 @@ def expert_ffn(up: "api.ExpertStack", down: "api.ExpertStack", e: int, image_t, 
     (2).  Returns (y fp16 [T, d], h fp16 [T, f])."""
     import torch
     import torch.nn.functional as F
+    if stream is not None:                             # the products are the current stream's
+        with torch.cuda.stream(stream):
+            return expert_ffn(up, down, e, image_t, x, wu, wd, bad)
     du, dd = up.host_desc[e], down.host_desc[e]
-    wu, bad = api.decode_dense(up, e, image_t, out=wu, bad=bad, stream=stream)
-    wd, bad = api.decode_dense(down, e, image_t, out=wd, bad=bad, stream=stream)
+    wu, bad = api.decode_dense(up, e, image_t, out=wu, bad=bad)
+    wd, bad = api.decode_dense(down, e, image_t, out=wd, bad=bad)
     su = up.scales[du.scale_base:du.scale_base + up.rows]
     sd = down.scales[dd.scale_base:dd.scale_base + down.rows]
     h = torch.relu(F.linear(x, wu) * su)

@@ -74,3 +74,31 @@ def test_expert_calls(dev, side):
     _owned(side, *api.moe_fused_ffn(up, down, image, x, ids, stream=side))
     _owned(side, *api.moe_fused_layers([up], [down], image, x, ids[None], stream=side))
     _owned(side, api.rms_glue(x, stream=side))
+
+
+def test_calls_of_several_steps(dev, side):
+    """The generator, which reads sizes back between its passes, and decode + library products: all on one stream."""
+    from sub_bit_moe_amd import api, hybrid, synth
+    words, checksum = api.build_dictionary(0.885)
+    trie = torch.from_numpy(api.build_trie(words)).to(dev)
+    table = torch.from_numpy(synth.scale_table().view("int16")).to(dev)
+    image = api.device_image(words, dev)
+    made = lambda **k: [api.generate_stack(7, 0, 2, m, *s, 0.885, trie, table, dict_checksum=checksum, **k)    # noqa: E731
+                        for m, s in ((0, (768, 512)), (1, (512, 768)))]
+    here = made()
+    side.wait_stream(torch.cuda.current_stream())
+    there = made(stream=side)
+    for a, b in zip(here, there):
+        _owned(side, b.codes, b.scales)
+        assert bytes(a.host_desc[0]) + bytes(a.host_desc[1]) == bytes(b.host_desc[0]) + bytes(b.host_desc[1])
+        for d in a.host_desc:
+            part = slice(d.code_base, d.code_base + d.n_codes)
+            assert torch.equal(a.codes[part], b.codes[part])
+        assert torch.equal(a.scales, b.scales)
+    x = torch.randn(3, 512, device=dev).half()
+    side.wait_stream(torch.cuda.current_stream())
+    y, h = hybrid.expert_ffn(*there, 1, image, x, stream=side)
+    _owned(side, y, h)
+    torch.cuda.current_stream().wait_stream(side)
+    want = hybrid.expert_ffn(*here, 1, image, x)
+    assert torch.equal(y, want[0]) and torch.equal(h, want[1])
