@@ -483,6 +483,10 @@ __device__ __forceinline__ void init_rows(Rows<D>& s, const AttnArgs& a, int kh,
 // 256).  Two under way against one: 64 requests of up to 16000 tokens, heads of 128, 121 us and 127; three waves against
 // two: 40 requests of up to 12000 tokens, heads of 64, 50 us and 54.
 constexpr int few_ring(int dim) { return dim == 256 ? 1 : 2; }
+// A request's tokens at most.  Positions are 32-bit, and reads run ahead of the last token: in the few-row kernel by a ring, a step
+// more for the pages, and a wave's share; in the tile kernel by a tile that is not there after one that may be.
+constexpr int kMostTokens = 0x7FFFF000;
+static_assert(0x7FFFFFFF - kMostTokens >= (few_ring(64) + 2) * kStep && few_ring(64) >= few_ring(256));
 constexpr int few_waves(int dim) { return dim == 64 ? 3 : 2; }
 // Workgroups of the few-row kernel at most: as many as the chip holds at once.
 constexpr int few_wgs(int dim) { return 256 * few_waves(dim); }
@@ -878,6 +882,7 @@ constexpr int tile_units(int dim) { return dim == 256 ? 2 : 1; }       // what a
 template <int D>
 struct Tile {
   static constexpr int kUnits = tile_units(D), kTokens = 32 * kTileThreads * kUnits / D;
+  static_assert(0x7FFFFFFF - kMostTokens >= 2 * kTokens);
   uint8_t k[kTokens * D / 2], v[kTokens * D * 2], ks[kTokens * D / 32];
 };
 
@@ -1506,7 +1511,7 @@ int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks
   if (n_blocks <= 0 || table_width < 0 || !kv_shape_ok(block_size, head_dim))
     return fail(SBM_EINVAL, "bad cache: n_blocks=%d, block_size=%d, head_dim=%d, table_width=%d", n_blocks, block_size,
                 head_dim, table_width);
-  if ((int64_t)table_width * block_size > 0x7FFFFF00)
+  if ((int64_t)table_width * block_size > kMostTokens)
     return fail(SBM_ERANGE, "%d blocks of %d tokens in one request", table_width, block_size);
   if ((int64_t)n_tokens * (n_heads / n_kv_heads) > 0x7FFFFF00) return fail(SBM_ERANGE, "too many rows");
   if ((int64_t)n_blocks * n_kv_heads > 0x7FFFFFFF) return fail(SBM_ERANGE, "%d blocks of %d heads", n_blocks, n_kv_heads);
