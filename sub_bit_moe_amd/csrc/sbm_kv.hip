@@ -531,7 +531,7 @@ int sbm_kv_plan(const int32_t* context_lens, const int32_t* new_lens, int32_t n_
   if (n_requests < 0 || n_requests > kMaxRequests)
     return fail(SBM_EINVAL, "n_requests=%d outside 0..%d", n_requests, kMaxRequests);
   if (!kv_shape_ok(block_size, 64)) return fail(SBM_EINVAL, "block_size=%d is no power of two from 16 to 4096", block_size);
-  if (free_capacity < 0 || table_width < 0 || n_blocks < 0 || max_tokens < 0 || max_tokens > (1 << 30))
+  if (free_capacity < 0 || table_width < 0 || n_blocks < 0 || max_tokens < 0 || max_tokens >= (1 << 30))
     return fail(SBM_EINVAL, "bad free_capacity=%d, table_width=%d, n_blocks=%d or max_tokens=%d", free_capacity,
                 table_width, n_blocks, max_tokens);
   if ((int64_t)n_blocks * block_size > 0x7FFFFFFF)
