@@ -419,7 +419,8 @@ size_t sbm_kv_cache_bytes(int32_t n_blocks, int32_t n_kv_heads, int32_t block_si
  *   block_table: device int32 [n_requests x table_width], in and out; columns
  *            that the step does not fill keep what they hold
  *   slots, positions, requests: device int32 [max_tokens], out (max_tokens below
- *            2^30); the new tokens in request order, then (-1, 0, -1).  No output overlaps an input
+ *            2^30); the new tokens in request order, then (-1, 0, -1).  No output
+ *            overlaps an input or another output
  *   cu_q:    device int32 [n_requests + 1], out: each request's first new token
  *   kv_lens: device int32 [n_requests], out: context + new
  *   n_free_out: device int32 [1], out (not n_free itself: a call may be repeated)

@@ -489,6 +489,17 @@ __global__ __launch_bounds__(kQThreads) void load_kernel(const uint8_t* cache, i
   *(uint4*)((is_v ? v : k) + ((int64_t)t * kv_heads + kh) * D + d0) = out;
 }
 
+// int32 arrays of a plan.
+struct Ints {
+  const void* p;
+  int64_t n;
+};
+
+bool overlap(Ints a, Ints b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return a.n > 0 && b.n > 0 && x < y + 4 * (uintptr_t)b.n && y < x + 4 * (uintptr_t)a.n;
+}
+
 bool vec_ok(const void* p, int64_t ts, int64_t hs) {
   return !p || (((uintptr_t)p & 15u) == 0 && ts % 8 == 0 && hs % 8 == 0);
 }
@@ -543,6 +554,17 @@ int sbm_kv_plan(const int32_t* context_lens, const int32_t* new_lens, int32_t n_
   if (n_free == n_free_out) return fail(SBM_EINVAL, "n_free_out must not be n_free");
   if (n_requests && (kv_lens == context_lens || kv_lens == new_lens))
     return fail(SBM_EINVAL, "kv_lens must not be one of the input lengths");
+  // lengths are read again where blocks are filled in: overwritten by then, they would index past the table
+  const Ints ins[] = {{context_lens, n_requests}, {new_lens, n_requests}, {free_blocks, free_capacity}, {n_free, 1}};
+  const Ints outs[] = {{block_table, (int64_t)n_requests * table_width}, {slots, max_tokens}, {positions, max_tokens},
+                       {requests, max_tokens}, {cu_q, (int64_t)n_requests + 1}, {kv_lens, n_requests}, {n_free_out, 1},
+                       {error, error ? 1 : 0}};
+  for (const Ints& o : outs) {
+    for (const Ints& i : ins)
+      if (overlap(o, i)) return fail(SBM_EINVAL, "an output overlaps an input");
+    for (const Ints& other : outs)
+      if (&other < &o && overlap(o, other)) return fail(SBM_EINVAL, "outputs overlap");
+  }
   PlanArgs a{context_lens, new_lens, free_blocks, n_free, block_table, slots, positions, requests, cu_q, kv_lens,
              n_free_out, error, n_requests, free_capacity, table_width, n_blocks, __builtin_ctz((unsigned)block_size),
              max_tokens};
