@@ -300,11 +300,27 @@ __device__ __forceinline__ void norm_rope8(const uint16_t* raw, uint16_t* other,
     ss = fused(x[j], x[j], ss);
   }
   ss = group_sum<D / 8>(ss);
-  const C inv = inverse_root(ss * ((C)1 / (C)D) + (C)a.eps);
   if (l.turn && !l.split) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) other[j] = raw[j ^ 1];
   }
+  const C mean = ss * ((C)1 / (C)D) + (C)a.eps;
+  if constexpr (sizeof(C) == 4 && __is_same(T, __bf16)) {
+    // squares that 32 bits do not hold (beyond 1e15 and, with an eps of 0, below 1e-15): the mean in 64; a head's lanes all
+    // come here or none
+    if (__builtin_expect(!(mean > 1e-30f && mean < 1e30f), 0)) {
+      double sum = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fused((double)x[j], (double)x[j], sum);
+      const double inv = inverse_root(group_sum<D / 8>(sum) * (1. / D) + a.eps);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        out[j] = round_once<T>(fused((float)((double)to_f32<T>(other[j]) * inv), r.with[j],
+                                     (float)((double)x[j] * inv) * r.own[j]));
+      return;
+    }
+  }
+  const C inv = inverse_root(mean);
   // the norm first: its results are sqrt(D) at most, whatever the elements and the weights are
 #pragma unroll
   for (int j = 0; j < 8; ++j)
