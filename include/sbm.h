@@ -493,13 +493,16 @@ size_t sbm_attention_kv4_workspace_bytes(int32_t n_requests, int32_t n_tokens, i
  * token that no request has get out = 0 and lse = -inf.  Query head h reads
  * key head h / (n_heads / n_kv_heads).
  *   q, out:   fp16 (bf16 with SBM_F_IN_BF16); q's data 16-byte aligned with
- *             strides that are multiples of 8 elements; out: [n_tokens x n_heads x
- *             head_dim], 16-byte aligned;  lse: fp32 [n_tokens x n_heads]
+ *             strides that are multiples of 8 elements (that of tokens with more
+ *             than one token, that of heads with more than one head); out:
+ *             [n_tokens x n_heads x head_dim], 16-byte aligned;  lse: fp32
+ *             [n_tokens x n_heads]
  *   block_table: device int32 [n_requests x table_width], table_width *
- *             block_size at most 2^31 - 4096; a block outside [0, n_blocks) hides its tokens and sets bit 0 of `error`; a length
- *             above table_width * block_size is cut to it and sets bit 1; cu_q
- *             that falls, or passes n_tokens, sets bit 2 (that request's rows
- *             may be left unwritten)
+ *             block_size at most 2^31 - 4096; a block outside [0, n_blocks)
+ *             hides its tokens and sets bit 0 of `error`; a length above
+ *             table_width * block_size is cut to it and sets bit 1; cu_q that
+ *             falls, or passes n_tokens, sets bit 2 (that request's rows may be
+ *             left unwritten)
  *   workspace: device, 16-byte aligned, of sbm_attention_kv4_workspace_bytes(...)
  *             or more, its first SBM_ATTENTION_ZEROED bytes ZEROED by the caller
  *             before its first use; every call leaves it ready for the next (calls

@@ -1525,7 +1525,7 @@ int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks
     return fail(SBM_EINVAL, "null pointer");
   if (((uintptr_t)q->data | (uintptr_t)cache | (uintptr_t)out | (uintptr_t)workspace) & 15u)
     return fail(SBM_EINVAL, "q, cache, out and workspace must be 16-byte aligned");
-  if (q->token_stride % 8 || q->head_stride % 8) return fail(SBM_EINVAL, "q's strides must be multiples of 8 elements");
+  if ((n_tokens > 1 && q->token_stride % 8) || (n_heads > 1 && q->head_stride % 8)) return fail(SBM_EINVAL, "q's strides must be multiples of 8 elements");
   const size_t need = sbm_attention_kv4_workspace_bytes(n_requests, n_tokens, n_heads, n_kv_heads, head_dim);
   if (workspace_bytes < need) return fail(SBM_ENOSPACE, "workspace %zu < %zu bytes", workspace_bytes, need);
   AttnArgs a{(const uint16_t*)q->data, q->token_stride, q->head_stride, cache, block_table, kv_lens, cu_q, out, lse,
