@@ -577,6 +577,8 @@ def _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours,
     flags = _x_flag(q) | (N.SBM_F_NEIGHBOURS if neighbours else 0)
     hq = _heads(q, "q", dtype, at, shape)
     T, H, D = shape
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, heads, head_dim]")
     Hk = k.shape[1]
     kshape = (T, Hk, D)
     hk = _heads(k, "k", dtype, at, kshape)
@@ -591,9 +593,11 @@ def _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours,
             raise ValueError(f"k_weight must hold {D} elements")
         wk = _dev(k_weight, "k_weight", dtype, at)
     if rope is not None:
+        if rope.dim() != 2:
+            raise ValueError("rope must be [positions, rot_dim]")
         rows, rot = rope.shape
         rp = _dev(rope, "rope", torch.float32, at)
-        if positions.numel() != T:
+        if positions is None or positions.numel() != T:
             raise ValueError(f"positions must hold {T} elements")
         pos = _dev(positions, "positions", torch.int32, at)
     if q_out is None:
@@ -611,6 +615,8 @@ def _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours,
         data, nb, hc = _cache(cache, at)
         if hc != Hk or cache.head_dim != D:
             raise ValueError(f"the cache holds {hc} heads of {cache.head_dim}, not {Hk} of {D}")
+        if v is None:
+            raise ValueError("v must be given with a cache")
         sl, bs = _slots(slots, T, at), cache.block_size
     check(lib().sbm_qk_norm_rope(hq, hk, hv, wq, wk, pos, rp, rows, rot, eps, T, H, Hk, D, ho, hko, sl, data, nb, bs, flags,
                                  _error(error, at), _stream(stream)))
@@ -619,7 +625,7 @@ def _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours,
 
 def _slots(slots, n: int, at: int):
     import torch
-    if slots.numel() != n:
+    if slots is None or slots.numel() != n:
         raise ValueError(f"slots must hold {n} elements")
     return _dev(slots, "slots", torch.int32, at)
 
@@ -696,6 +702,8 @@ def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: flo
     import torch
     i32 = torch.int32
     dtype, at, shape = q.dtype, q.get_device(), q.shape
+    if len(shape) != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
     T, H, D = shape
     R = kv_lens.numel()
     Hk = cache.n_kv_heads

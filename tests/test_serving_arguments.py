@@ -2,7 +2,10 @@
 import pytest
 
 from sub_bit_moe_amd import _native as N
+from sub_bit_moe_amd import api
 from tests.test_serving_refusals import ATT, EINVAL, _heads
+
+torch = pytest.importorskip("torch")
 
 
 @pytest.mark.parametrize("shape,ts,hs", [((1, 4), 12, 64), ((1, 4), 1, 64), ((2, 1), 64, 4), ((1, 1), 3, 5), ((1, 1), 0, 0)])
@@ -18,3 +21,44 @@ def test_strides_that_addresses_are_made_from_are_refused(shape, ts, hs):
     T, H = shape
     call = {**ATT, "R": T, "T": T, "H": H, "Hk": 1, "q": _heads(4096, ts, hs), "ws_bytes": 0}
     assert N.lib().sbm_attention_kv4(*call.values()) == EINVAL
+
+
+class _There:
+    """A CPU tensor that says it is on the GPU."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return 0
+
+
+def _rows(*shape):
+    return _There(torch.zeros(shape, dtype=torch.float16))
+
+
+def _ints(*shape):
+    return _There(torch.zeros(shape, dtype=torch.int32))
+
+
+def test_missing_arguments_are_named():
+    q, k = _rows(2, 4, 64), _rows(2, 2, 64)
+    rope = _There(torch.zeros(9, 64))
+    cache = api.KVCache(_There(torch.zeros(3, 2, 16 * 68, dtype=torch.uint8)), 16, 64)
+    with pytest.raises(ValueError, match="positions"):
+        api.qk_norm_rope(q, k, None, None, None, rope)
+    with pytest.raises(ValueError, match="slots"):
+        api.qk_norm_rope_store(q, k, k, None, None, None, None, None, cache)
+    with pytest.raises(ValueError, match="v "):
+        api.qk_norm_rope_store(q, k, None, None, None, None, None, _ints(2), cache)
+    with pytest.raises(ValueError, match="rope"):
+        api.qk_norm_rope(q, k, None, None, _ints(2), _There(torch.zeros(9)))
+    with pytest.raises(ValueError, match="q must be"):
+        api.qk_norm_rope(_rows(2, 64), k, None, None, None, None)
+    with pytest.raises(ValueError, match="k must be"):
+        api.qk_norm_rope(q, _rows(2 * 64), None, None, None, None)
+    with pytest.raises(ValueError, match="q must be"):
+        api.attention_kv4(_rows(2, 64), cache, _ints(2, 3), _ints(2))
