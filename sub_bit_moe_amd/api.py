@@ -32,9 +32,12 @@ def _ptr(a) -> int:
 _current_stream = None
 
 
-def _stream(stream=None) -> int:
-    """The stream's handle; of the current stream without building a Stream object (2.6 us) for it."""
+def _stream(stream=None, at=None) -> int:
+    """The stream's handle; of the current stream without building a Stream object (2.6 us) for it.  at: the index of the device
+    that the call's tensors are on, which has to be the stream's."""
     if stream is not None:
+        if at is not None and stream.device_index != at:
+            raise ValueError(f"the tensors are on device {at}, the stream on device {stream.device_index}")
         return int(stream.cuda_stream)
     global _current_stream
     if _current_stream is None:
@@ -42,10 +45,14 @@ def _stream(stream=None) -> int:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         device = getattr(torch._C, "_cuda_getDevice", None)
         if raw is None or device is None:
-            _current_stream = lambda: int(torch.cuda.current_stream().cuda_stream)   # noqa: E731
+            _current_stream = (lambda d: int(torch.cuda.current_stream(d).cuda_stream)), torch.cuda.current_device
         else:
-            _current_stream = lambda: raw(device())                                  # noqa: E731
-    return _current_stream()
+            _current_stream = raw, device
+    raw, device = _current_stream
+    now = device()
+    if at is not None and now != at:
+        raise ValueError(f"the tensors are on device {at}, the current device is {now}")
+    return raw(now)
 
 
 def _made_on(stream, make, *args, **kw):
@@ -566,7 +573,7 @@ def kv_plan(context_lens, new_lens, free_blocks, n_free, block_table, n_blocks: 
         outs = (_dev(plan.slots, "slots", i32, at), _dev(plan.positions, "positions", i32, at),
                 _dev(plan.requests, "requests", i32, at), _dev(plan.cu_q, "cu_q", i32, at),
                 _dev(plan.kv_lens, "kv_lens", i32, at), _dev(plan.n_free, "plan.n_free", i32, at), _error(plan.error, at))
-    check(lib().sbm_kv_plan(*ins, block_table.shape[1], n_blocks, block_size, max_tokens, *outs, _stream(stream)))
+    check(lib().sbm_kv_plan(*ins, block_table.shape[1], n_blocks, block_size, max_tokens, *outs, _stream(stream, at)))
     return plan
 
 
@@ -619,7 +626,7 @@ def _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours,
             raise ValueError("v must be given with a cache")
         sl, bs = _slots(slots, T, at), cache.block_size
     check(lib().sbm_qk_norm_rope(hq, hk, hv, wq, wk, pos, rp, rows, rot, eps, T, H, Hk, D, ho, hko, sl, data, nb, bs, flags,
-                                 _error(error, at), _stream(stream)))
+                                 _error(error, at), _stream(stream, at)))
     return q_out, k_out
 
 
@@ -673,7 +680,7 @@ def kv_load(cache: KVCache, slots, dtype=None, k=None, v=None, error=None, strea
     if k.shape != shape or v.shape != shape:
         raise ValueError(f"k and v must be {shape}, not {tuple(k.shape)} and {tuple(v.shape)}")
     check(lib().sbm_kv_load(data, nb, Hk, cache.block_size, cache.head_dim, _slots(slots, n, at), n, _dev(k, "k", dtype, at),
-                            _dev(v, "v", dtype, at), _x_flag(k), _error(error, at), _stream(stream)))
+                            _dev(v, "v", dtype, at), _x_flag(k), _error(error, at), _stream(stream, at)))
     return k, v
 
 
@@ -734,7 +741,7 @@ def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: flo
         hq, data, nb, cache.block_size, _dev(block_table, "block_table", i32, at), block_table.shape[1],
         _dev(kv_lens, "kv_lens", i32, at), 0 if cu_q is None else _dev(cu_q, "cu_q", i32, at), R, T, H, Hk, D,
         D ** -0.5 if scale is None else scale, po, pl, _x_flag(q), _dev(workspace, "workspace", torch.uint8, at),
-        workspace.numel(), _error(error, at), _stream(stream)))
+        workspace.numel(), _error(error, at), _stream(stream, at)))
     return out if lse is None else (out, lse)
 
 # ------------------------------------------------------------------ synthetic stacks

@@ -62,3 +62,25 @@ def test_missing_arguments_are_named():
         api.qk_norm_rope(q, _rows(2 * 64), None, None, None, None)
     with pytest.raises(ValueError, match="q must be"):
         api.attention_kv4(_rows(2, 64), cache, _ints(2, 3), _ints(2))
+
+
+def test_tensors_of_another_device_than_the_stream_are_refused(monkeypatch):
+    """A launch goes to the device of its stream, which is the current one where none is given."""
+    class Stream:
+        device_index, cuda_stream = 1, 7
+
+    monkeypatch.setattr(api, "_current_stream", (lambda d: 40 + d, lambda: 1))
+    monkeypatch.setattr(api, "_made_on", lambda stream, make, *a, **k: _There(torch.zeros(2, 4, 64)))
+    monkeypatch.setattr(api, "check", lambda status: pytest.fail("launched"))
+    q = _rows(2, 4, 64)
+    cache = api.KVCache(_There(torch.zeros(3, 4, 16 * 68, dtype=torch.uint8)), 16, 64)
+    plan = api.KVPlan(_ints(8), _ints(8), _ints(8), _ints(3), _ints(2), _ints(1), _ints(1), None)
+    for kw in ({}, {"stream": Stream()}):
+        for call in (lambda: api.qk_norm_rope(q, q, None, None, None, None, **kw),
+                     lambda: api.kv_load(cache, _ints(2), k=_rows(2, 4, 64), v=_rows(2, 4, 64), **kw),
+                     lambda: api.attention_kv4(q, cache, _ints(2, 3), _ints(2), out=_rows(2, 4, 64),
+                                               workspace=_There(torch.zeros(64, dtype=torch.uint8)), **kw),
+                     lambda: api.kv_plan(_ints(2), _ints(2), _ints(4), _ints(1), _ints(2, 3), 4, 16, 8, plan=plan, **kw)):
+            with pytest.raises(ValueError, match="on device 0"):
+                call()
+    assert api._stream(None, 1) == 41 and api._stream(Stream(), 1) == 7 and api._stream() == 41
