@@ -491,7 +491,12 @@ size_t sbm_attention_kv4_workspace_bytes(int32_t n_requests, int32_t n_tokens, i
  *   out = sum softmax(s) v,   lse = ln sum exp s   (lse may be NULL).
  * A row that sees nothing (kv_lens 0, or more tokens than the cache holds) and a
  * token that no request has get out = 0 and lse = -inf.  Query head h reads
- * key head h / (n_heads / n_kv_heads).
+ * key head h / (n_heads / n_kv_heads).  The probabilities are rounded to the
+ * call's type before the sum over v, as the outputs are; sums are fp32.  Where a
+ * request has more than 128 rows (tokens x heads of a key head) a query counts to
+ * 20 bits below the largest of each 32 of its dimensions, unless that would cut
+ * more than 6 of them short: 128 rows with such a query are computed from whole
+ * queries (in 1.7 times the time).
  *   q, out:   fp16 (bf16 with SBM_F_IN_BF16); q's data 16-byte aligned with
  *             strides that are multiples of 8 elements (that of tokens with more
  *             than one token, that of heads with more than one head); out:

@@ -20,7 +20,8 @@
 // K's codes and scales are the instruction's own 4-bit type, so they go into it as
 // they are.  A query row's 32 dimensions become four times 32 numbers of 6 bits
 // (E2M3, held to multiples of 1/8 up to 2: 5 bits and a sign) under the power of two of the
-// largest and 2^-5, 2^-10 and 2^-15 of that: 20 bits.  At 32 cycles each the four cost what
+// largest and 2^-5, 2^-10 and 2^-15 of that: 20 bits.  (Where that cuts some short, the
+// workgroup's rows go the few-row kernel's way.)  At 32 cycles each the four cost what
 // the 16-bit product costs, and no K is converted.  The instruction aligns
 // eight products at a time to the largest and keeps 13 bits below it, which holds
 // multiples of 1/16 up to 12 exactly; sums beyond that are fp32.  Measured over normally
@@ -837,9 +838,15 @@ __device__ __forceinline__ f32x16 mfma_k(u32x4 k, const uint32_t* q, f32x16 c, u
 constexpr int kPieces = 4;
 
 // 32 dimensions of a row as kPieces x 32 numbers of 6 bits; returns the pieces' scale bytes.  Each conversion
-// rounds what the ones before left to a multiple of 1/8 of its scale, up to 2.
+// rounds what the ones before left to a multiple of 1/8 of its scale, up to 2.  *exact becomes false where more than kInexact of
+// the 32 are not met: one far beyond the others leaves those too few bits.  Of 4 million blocks of normally distributed fp16
+// queries one had 5 and none more, of bf16 none more than 3 (a limit of 4 makes a few of 2 million blocks, and the whole call
+// wait for them: four prompts of 511 in a step of 24, 142 us, 194); with one of the 32 at 128 (fp16) or 1024 (bf16) times the
+// others' size 8 are not met, which would put scores off by 1e-4 or 8e-4 of their spread, a fifth of the step that
+// probabilities are rounded to.
+constexpr int kInexact = 6;
 template <typename T>
-__device__ __forceinline__ uint32_t split_query(const AttnArgs& a, const uint16_t* q, uint32_t (&out)[kPieces][6]) {
+__device__ __forceinline__ uint32_t split_query(const AttnArgs& a, const uint16_t* q, uint32_t (&out)[kPieces][6], bool* exact) {
   typedef float f32x32 __attribute__((ext_vector_type(32)));
   typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
   f32x16 even, odd;
@@ -860,17 +867,23 @@ __device__ __forceinline__ uint32_t split_query(const AttnArgs& a, const uint16_
     }
   }
   const uint32_t e = max(top >> 23, 16u);            // the last piece's scale is 2^-126 or more
+  int left = 0;
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) {
     const float scale = exponent(e - 5 * p);
     const u32x6 c = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, scale);     // the two in turn
 #pragma unroll
     for (int i = 0; i < 6; ++i) out[p][i] = c[i];
-    if (p + 1 == kPieces) break;
     const f32x32 got = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(c, scale);
+    if (p + 1 < kPieces) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) even[i] -= got[2 * i], odd[i] -= got[2 * i + 1];       // exact
+      for (int i = 0; i < 16; ++i) even[i] -= got[2 * i], odd[i] -= got[2 * i + 1];       // exact
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) left += (even[i] != got[2 * i]) + (odd[i] != got[2 * i + 1]);
+    }
   }
+  if (left > kInexact && top < 0x7F800000u) *exact = false;
   // an infinity or a NaN among them: NaN
   return top >= 0x7F800000u ? 0xFFFFFFFFu : e * 0x01010101u - (15u << 24 | 10u << 16 | 5u << 8);
 }
@@ -959,6 +972,7 @@ __device__ __forceinline__ void fetch(Fetch<D>& f, const AttnArgs& a, const Bloc
 // border: some row of the workgroup does not see all of the tile.  Returns what
 // the waves have to know: a bit for each 16 tokens without a block, kNoteOdd: odd blocks among V that went in as nothing.
 constexpr uint32_t kNoteOdd = 1u << 31;
+constexpr uint32_t kNoteExact = 1u << 30;      // split queries will not do
 constexpr int kPutSteps = 5;
 template <typename T, int D>
 __device__ __forceinline__ uint32_t prepare_values(const Fetch<D>& f, uint32_t (&sc)[4], int t0, int end, bool border, int unit) {
@@ -1218,6 +1232,30 @@ __device__ __forceinline__ uint32_t parts_of(const Share& s, uint64_t total) {
   return (uint32_t)max(min(parts, (uint64_t)(s.steps / min_tiles(D))), (uint64_t)1);
 }
 
+// 16 of the tile kernel's rows where split queries would not do: as the few-row kernel has them, by one wave, over tokens t0 ..
+// stop.  The waves share nothing: two prompts of 4000 tokens, heads of 128, take 569 us if all their queries are so, 340 if none is
+// (1024 tokens behind 19000, heads of 256: 788 and 472).
+template <typename T, int D>
+__device__ __forceinline__ void exact_rows(Rows<D>& s, const AttnArgs& a, const int32_t* table, int kh, const Request& rq, int row0,
+                                           int t0, int stop, int lane) {
+  init_rows<T, D>(s, a, kh, rq, row0, lane);
+  const int first = max(rq.kv - rq.n + row0 / a.group, -1);
+  bool hole = false;
+  if (t0 < stop) {
+    Raw<D> raw, ahead;
+    load_tokens<D>(raw, a, pages(a, table, t0, stop), kh, t0, lane);
+    for (; t0 < stop; t0 += 32) {
+      load_tokens<D>(ahead, a, pages(a, table, t0 + 32, stop), kh, t0 + 32, lane);       // past the last: block 0
+      hole |= !raw.ok[0] || (!raw.ok[1] && t0 + 16 < stop);
+      step<T, D>(s, raw, a, table, kh, t0, stop, first, lane);
+      raw = ahead;
+    }
+  }
+  if (hole && lane == 0 && a.error) atomicOr(a.error, kErrBlock);
+  s.l += __shfl_xor(s.l, 16, 64);
+  s.l += __shfl_xor(s.l, 32, 64);
+}
+
 // A workgroup takes 128 rows of a key head and a run of tiles of tokens: it reads a tile's codes once for all of them, converts
 // V into one half of its LDS while the products read the other.  Four 6-bit pieces of a query cost the matrix pipes what one
 // 16-bit product does, and save K's conversion, the vector instructions being the next limit.  Two prompts of 4000 tokens
@@ -1312,8 +1350,10 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, const uint32_t bloc
     for (int x = 0; x < 16; ++x) s.o[db][x] = 0.f;
   const uint16_t* query =
       a.q + (int64_t)(rq.q0 + min(i, rq.n - 1)) * a.q_ts + (int64_t)(kh * a.group + row % a.group) * a.q_hs;
+  bool exact = true;
 #pragma unroll
-  for (int kb = 0; kb < D / 64; ++kb) s.qs[kb] = split_query<T>(a, query + 64 * kb + 32 * h, s.q[kb]);
+  for (int kb = 0; kb < D / 64; ++kb) s.qs[kb] = split_query<T>(a, query + 64 * kb + 32 * h, s.q[kb], &exact);
+  if (!exact) atomicOr(&s_note[j0 & 3], kNoteExact);
   constexpr int kUnits = Tile<D>::kUnits;
   constexpr auto kUnitList = std::make_integer_sequence<int, kUnits>{};
   const int unit_t = 16 * (64 * wave / (D / 2));        // the first of a wave's units' tokens
@@ -1354,12 +1394,49 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, const uint32_t bloc
   auto put_all = [&](int j) {
     each([&](auto step) { put(step, j); }, std::make_integer_sequence<int, kPutSteps * kUnits>{});
   };
+  const uint32_t item = unit / (uint32_t)a.kv_heads / parts * (uint32_t)a.kv_heads + (uint32_t)kh;
+  const uint32_t slot0 = slots0 + item * parts;
+  float* p0 = a.parts + kPart<D, 16> * 2 * few_wgs(D) + (int64_t)slot0 * kPart<D, kTileRows>;
+  float* mine = p0 + (int64_t)part * kPart<D, kTileRows>;
+  auto exact_path = [&] {
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+      const int r0 = 32 * wave + 16 * x, r = r0 + (lane & 15);
+      if (r0 >= nr) break;
+      Rows<D> e;
+      exact_rows<T, D>(e, a, table, kh, rq, row0 + r0, j0 * kTokens, min(end, j1 * kTokens), lane);
+      if (r >= nr) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int c = 0; c < D / 16; c += 4) {
+          const int d = (4 * (lane >> 4) + j) * (D / 16) + c;
+          const float4 o = make_float4(e.o[c][j], e.o[c + 1][j], e.o[c + 2][j], e.o[c + 3][j]);
+          if (parts == 1) {
+            store4<T, D>(a, kh, rq, row0 + r, d, o, e.m, e.l);
+          } else {                                       // as TileLayout has them
+            float* to = mine + wave * 32 * D + ((d / 32 * 4 + d / 4 % 4) * 128 + (r & 31) + d / 16 % 2 * 32) * 2;
+            put2(to, o.x, o.y);
+            put2(to + TileLayout<D>::kNext, o.z, o.w);
+          }
+        }
+      }
+      if (parts > 1 && lane < 16) put2(mine + kTileRows * D + 2 * r, e.m, e.l);
+    }
+  };
+  bool split = true;
   if (j0 < j1) {
     blocks_at(j0, next);
     each([&](auto part) { load(part, j0); }, std::make_integer_sequence<int, kFetchParts * kUnits>{});
     prepare(j0, true);
     put_all(j0);
     __syncthreads();
+    split = !(__builtin_amdgcn_readfirstlane(s_note[j0 & 3]) & kNoteExact);
+  }
+  if (__builtin_expect(!split, 0)) {
+    exact_path();
+    if (parts == 1) return;
+  } else {
     for (int j = j0; j < j1; ++j) {
       const int t0 = j * kTokens;
       const uint32_t note = __builtin_amdgcn_readfirstlane(s_note[j & 3]);
@@ -1372,42 +1449,38 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, const uint32_t bloc
       if (__builtin_expect(note & kNoteOdd, 0)) tile_add_odd<T, D>(s, a, table, kh, t0, end, query, h);
       __syncthreads();
     }
-  }
-  s.l += __shfl_xor(s.l, 32, 64);
-  const bool valid = row - row0 < nr;
-  const int64_t at = (int64_t)(rq.q0 + i) * a.heads + kh * a.group + row % a.group;
-  if (parts == 1) {
-    if (!valid) return;
-    const float by = s.l == 0.f ? 0.f : 1.f / s.l;
-    uint16_t* out = a.out + at * D + 16 * h;
+    s.l += __shfl_xor(s.l, 32, 64);
+    const bool valid = row - row0 < nr;
+    const int64_t at = (int64_t)(rq.q0 + i) * a.heads + kh * a.group + row % a.group;
+    if (parts == 1) {
+      if (!valid) return;
+      const float by = s.l == 0.f ? 0.f : 1.f / s.l;
+      uint16_t* out = a.out + at * D + 16 * h;
 #pragma unroll
-    for (int db = 0; db < D / 32; ++db) {
-      uint32_t w[8];
+      for (int db = 0; db < D / 32; ++db) {
+        uint32_t w[8];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int b = x >> 1, lo = x & 1 ? 2 : 0;      // dimensions 2x and 2x + 1 of the lane's 16: o's 4a + b, a = lo, lo + 1
-        w[x] = pack2<T>(s.o[db][4 * lo + b] * by, s.o[db][4 * lo + 4 + b] * by);
+        for (int x = 0; x < 8; ++x) {
+          const int b = x >> 1, lo = x & 1 ? 2 : 0;      // dimensions 2x and 2x + 1 of the lane's 16: o's 4a + b, a = lo, lo + 1
+          w[x] = pack2<T>(s.o[db][4 * lo + b] * by, s.o[db][4 * lo + 4 + b] * by);
+        }
+        *(uint4*)(out + 32 * db) = make_uint4(w[0], w[1], w[2], w[3]);
+        *(uint4*)(out + 32 * db + 8) = make_uint4(w[4], w[5], w[6], w[7]);
       }
-      *(uint4*)(out + 32 * db) = make_uint4(w[0], w[1], w[2], w[3]);
-      *(uint4*)(out + 32 * db + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+      if (a.lse && h == 0) a.lse[at] = s.l == 0.f ? -INFINITY : (s.m + __log2f(s.l)) * kLn2;
+      return;
     }
-    if (a.lse && h == 0) a.lse[at] = s.l == 0.f ? -INFINITY : (s.m + __log2f(s.l)) * kLn2;
-    return;
-  }
-  const uint32_t item = unit / (uint32_t)a.kv_heads / parts * (uint32_t)a.kv_heads + (uint32_t)kh;
-  const uint32_t slot0 = slots0 + item * parts;
-  float* p0 = a.parts + kPart<D, 16> * 2 * few_wgs(D) + (int64_t)slot0 * kPart<D, kTileRows>;
-  float* mine = p0 + (int64_t)part * kPart<D, kTileRows>;
-  if (32 * wave < nr) {                                // rows that are not there are written with the others, and not read
-    float* o = mine + wave * 32 * D + 2 * lane;
+    if (32 * wave < nr) {                                // rows that are not there are written with the others, and not read
+      float* o = mine + wave * 32 * D + 2 * lane;
 #pragma unroll
-    for (int db = 0; db < D / 32; ++db)
+      for (int db = 0; db < D / 32; ++db)
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int b = x >> 1, lo = x & 1 ? 2 : 0;
-        put2(o + (db * 8 + x) * 128, s.o[db][4 * lo + b], s.o[db][4 * lo + 4 + b]);
-      }
-    if (h == 0) put2(mine + kTileRows * D + 2 * (row - row0), s.m, s.l);
+        for (int x = 0; x < 8; ++x) {
+          const int b = x >> 1, lo = x & 1 ? 2 : 0;
+          put2(o + (db * 8 + x) * 128, s.o[db][4 * lo + b], s.o[db][4 * lo + 4 + b]);
+        }
+      if (h == 0) put2(mine + kTileRows * D + 2 * (row - row0), s.m, s.l);
+    }
   }
   join<T, D, kTileRows, 8, kTileThreads, TileLayout<D>>(a, [&](int p) { return p0 + (int64_t)p * kPart<D, kTileRows>; }, part, (int)parts,
                            a.counters + kLevels * kFewCounters + slot0, tile_slots(64), (float*)&s_tile[0], &s_unit[0], kh, rq,
