@@ -48,16 +48,16 @@ def _stream(stream=None, at=None) -> int:
             _current_stream = (lambda d: int(torch.cuda.current_stream(d).cuda_stream)), torch.cuda.current_device
         else:
             _current_stream = raw, device
-    raw, device = _current_stream
-    now = device()
+    now = _current_stream[1]()
     if at is not None and now != at:
         raise ValueError(f"the tensors are on device {at}, the current device is {now}")
-    return raw(now)
+    return _current_stream[0](now)
 
 
 def _made_on(stream, make, *args, **kw):
     """make(*args, **kw), a tensor that a call on `stream` writes: allocated, and filled, on that stream.  Memory of the
-    current stream could still be in use there, or be given out again there before the call has written it."""
+    current stream could still be in use there, or be given out again there before the call has written it.  The serving
+    calls, which are bound by the host, come here only with a stream."""
     if stream is None:
         return make(*args, **kw)
     import torch
@@ -561,7 +561,8 @@ def kv_plan(context_lens, new_lens, free_blocks, n_free, block_table, n_blocks: 
            _dev(free_blocks, "free_blocks", i32, at), free_blocks.numel(), _dev(n_free, "n_free", i32, at),
            _dev(block_table, "block_table", i32, at))
     if plan is None:
-        plan = _made_on(stream, alloc_kv_plan, R, max_tokens, block_table)
+        plan = alloc_kv_plan(R, max_tokens, block_table) if stream is None else \
+            _made_on(stream, alloc_kv_plan, R, max_tokens, block_table)
         n = 4 * max_tokens
         p = plan.cu_q.data_ptr() - 3 * n           # one buffer, in this order
         outs = (p, p + n, p + 2 * n, p + 3 * n, p + 3 * n + 4 * R + 4, p + 3 * n + 8 * R + 4, plan.error.data_ptr())
@@ -608,12 +609,12 @@ def _qk_norm_rope(q, k, v, q_weight, k_weight, positions, rope, eps, neighbours,
             raise ValueError(f"positions must hold {T} elements")
         pos = _dev(positions, "positions", torch.int32, at)
     if q_out is None:
-        q_out = _made_on(stream, q.new_empty, shape)
+        q_out = q.new_empty(shape) if stream is None else _made_on(stream, q.new_empty, shape)
         ho = _pack_heads(q_out.data_ptr(), H * D, D)
     else:
         ho = _heads(q_out, "q_out", dtype, at, shape)
     if k_out is None and cache is None:
-        k_out = _made_on(stream, q.new_empty, kshape)
+        k_out = q.new_empty(kshape) if stream is None else _made_on(stream, q.new_empty, kshape)
         hko = _pack_heads(k_out.data_ptr(), Hk * D, D)
     else:
         hko = None if k_out is None else _heads(k_out, "k_out", dtype, at, kshape)
@@ -674,9 +675,9 @@ def kv_load(cache: KVCache, slots, dtype=None, k=None, v=None, error=None, strea
     data, nb, Hk = _cache(cache, at)
     shape = (n, Hk, cache.head_dim)
     if k is None:
-        k = _made_on(stream, torch.empty, shape, dtype=dtype, device=slots.device)
+        k = slots.new_empty(shape, dtype=dtype) if stream is None else _made_on(stream, slots.new_empty, shape, dtype=dtype)
     if v is None:
-        v = _made_on(stream, torch.empty, shape, dtype=dtype, device=slots.device)
+        v = slots.new_empty(shape, dtype=dtype) if stream is None else _made_on(stream, slots.new_empty, shape, dtype=dtype)
     if k.shape != shape or v.shape != shape:
         raise ValueError(f"k and v must be {shape}, not {tuple(k.shape)} and {tuple(v.shape)}")
     check(lib().sbm_kv_load(data, nb, Hk, cache.block_size, cache.head_dim, _slots(slots, n, at), n, _dev(k, "k", dtype, at),
@@ -721,7 +722,7 @@ def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: flo
     hq = _heads(q, "q", dtype, at, shape)
     data, nb, _ = _cache(cache, at)
     if out is None:
-        out = _made_on(stream, q.new_empty, shape)
+        out = q.new_empty(shape) if stream is None else _made_on(stream, q.new_empty, shape)
         po = out.data_ptr()
     elif out.shape != shape:
         raise ValueError(f"out must be {tuple(shape)}, not {tuple(out.shape)}")
@@ -733,7 +734,8 @@ def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: flo
             raise ValueError(f"lse must be {(T, H)}, not {tuple(lse.shape)}")
         pl = _dev(lse, "lse", torch.float32, at)
     elif return_lse:
-        lse = _made_on(stream, torch.empty, (T, H), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((T, H), dtype=torch.float32) if stream is None else \
+            _made_on(stream, q.new_empty, (T, H), dtype=torch.float32)
         pl = lse.data_ptr()
     if workspace is None:
         workspace = _made_on(stream, alloc_attention_workspace, R, T, H, Hk, D, q.device)
