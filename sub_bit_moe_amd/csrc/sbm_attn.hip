@@ -1494,7 +1494,8 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) void attn_tile_kern
 
 // A step that may hold both: one launch, so that the few-row part, which waits for memory, and the prompts, which do not,
 // run at once.  A workgroup a CU of each comes first, then the rest.  Heads of 128, 24 requests with four prompts of 511
-// tokens: 140 us instead of 150 with two launches; two prompts of 1077 tokens and 6 heads beside five requests: 40, not 50.
+// tokens: 141 us instead of 151 with two launches; two prompts of 1077 tokens and 6 heads beside five requests: 41, not 48; heads of
+// 64, 32 over 8, one prompt of 500 tokens 22, not 26, one of 4000 124, not 131, two of 4000 222 and 222.
 // Heads of 256 take a whole CU's registers for a prompt's workgroup and are launched one after the other.
 constexpr uint32_t kCus = 256;
 template <typename T, int D>
@@ -1536,10 +1537,7 @@ void launch_attn(const AttnArgs& a, hipStream_t s) {
   const unsigned tiles = (unsigned)tile_wgs(a.n_requests, rows, a.kv_heads, D);
   const bool some_few = a.cu_q || a.group <= kFewRows, some_tiles = a.cu_q ? rows > kFewRows : a.group > kFewRows;
   if constexpr (D != 256) {
-    // with heads of 64 up to what the chip holds at once: 500 tiles of rows take 41 us, two launches 43; 1000 take 120
-    // and 114, 2000 take 223 and 201 (with heads of 128, 1000 tiles: 318 and 322)
-    const bool one = D != 64 || rows / kTileRows * a.kv_heads <= 2 * (int64_t)kCus;
-    if (some_few && some_tiles && one) {
+    if (some_few && some_tiles) {
       hipLaunchKernelGGL((attn_step_kernel<T, D>), dim3(few + tiles), dim3(kTileThreads), 0, s, a, few, tiles);
       return;
     }
