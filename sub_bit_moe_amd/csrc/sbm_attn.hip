@@ -622,9 +622,9 @@ __device__ __forceinline__ void join(const AttnArgs& a, At at, int p, int np, ui
 // whatever the lengths, its waves 32 tokens each; a run's first and last 16 rows may be
 // shared with neighbours, whose partial results the last one of them to end joins.
 // Bound by HBM with long caches (the codes are read once, K and V of 32 tokens
-// ahead): 64 requests of up to 16000 tokens, 8 key heads of 128 (573 MB) 121 us, 4.7
-// TB/s; two of 250000 (488 MB) 103 us, 4.7 TB/s.  By latency with short ones: one
-// request of 1000 tokens 9.5 us.
+// ahead): 64 requests of up to 16000 tokens, 8 key heads of 128 (573 MB) 122 us, 4.7
+// TB/s; two of 250000 (488 MB) 104 us, 4.7 TB/s.  By latency with short ones: one
+// request of 1000 tokens 10 us.
 template <typename T, int D>
 __device__ __forceinline__ void few_rows(const AttnArgs& a, const uint32_t block, const uint32_t grid) {
   constexpr int kPad = D + 4;
@@ -1259,10 +1259,10 @@ __device__ __forceinline__ void exact_rows(Rows<D>& s, const AttnArgs& a, const 
 // A workgroup takes 128 rows of a key head and a run of tiles of tokens: it reads a tile's codes once for all of them, converts
 // V into one half of its LDS while the products read the other.  Four 6-bit pieces of a query cost the matrix pipes what one
 // 16-bit product does, and save K's conversion, the vector instructions being the next limit.  Two prompts of 4000 tokens
-// (32 heads of 128 over 8, 2.6e11 operations): 280 to 299 us by the card, 880 to 935 TFLOP/s, with the matrix pipes busy 43 %
+// (32 heads of 128 over 8, 2.6e11 operations): 288 to 292 us in three runs, 897 to 909 TFLOP/s, with the matrix pipes busy 42 %
 // of the cycles and vector instructions issued in 58 %; the clock falls with random data (as two launches zeros took 296 us,
-// normally distributed values 350).  1024 tokens behind 19000 (16 heads of 256 over 4, 3.3e11): 427 us, 766 TFLOP/s, one wave
-// a SIMD, whose products wait for its exponentials (matrix pipes busy 33 %).
+// normally distributed values 350).  1024 tokens behind 19000 (16 heads of 256 over 4, 3.3e11): 439 us, 745 TFLOP/s, one wave
+// a SIMD, whose products wait for its exponentials (matrix pipes busy 32 %).
 template <typename T, int D>
 __device__ __forceinline__ void tile_rows(const AttnArgs& a, const uint32_t block) {
   constexpr int kTokens = Tile<D>::kTokens;
