@@ -5,8 +5,9 @@ Every step of the codec and of the fused decode + matvec runs in libsbm.so
 used for host buffers, torch tensors for device memory and streams.
 
 A call with stream= runs on that stream, which has to have waited for whatever
-wrote the call's inputs.  Results and workspaces that the call makes belong to
-that stream; another one waits for it before it reads them.
+wrote the call's inputs, and these have to be kept until it has read them.
+Results and workspaces that the call makes belong to that stream; another one
+waits for it before it reads them.
 """
 from __future__ import annotations
 
