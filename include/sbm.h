@@ -521,6 +521,106 @@ int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks
                       float scale, uint16_t* out, float* lse, uint32_t flags, void* workspace,
                       size_t workspace_bytes, uint32_t* error, void* stream);
 
+/* ------------------------------------------------- around the experts */
+/* What a decoder step has between its parts and at its end: the norm with the
+ * residual's addition and the sum over a token's experts, the routing that makes
+ * the expert calls' ids, and the choice of the next token. */
+#define SBM_F_SIGMOID 512u       /* sbm_moe_route: scores are 1 / (1 + e^-l); without it softmax */
+#define SBM_F_RENORM 1024u       /* sbm_moe_route: a token's gates are divided by their sum */
+#define SBM_F_IN_F32 2048u       /* sbm_moe_route, sbm_sample: logits are fp32; sbm_add_rms_norm: x is */
+#define SBM_F_RESIDUAL_F32 4096u /* sbm_add_rms_norm: residual and residual_out are fp32 */
+#define SBM_F_OUT_FP8 8192u      /* sbm_add_rms_norm: out is e4m3 (OCP: largest 448, no infinities), with scales */
+
+/* Root-mean-square norm of a residual stream's next state, in one pass:
+ *   h[t] = residual[t] + sum_j gates[t, j] x[t * k + j],   j = 0 .. k - 1
+ *   y[t] = h[t] / sqrt(mean(h[t]^2) + eps) * weight
+ * x's rows are what the expert calls give, one for each (token, expert) pair.  A
+ * gate of zero takes no part: its row is not looked at, whatever it holds (rows
+ * that an expert call left unwritten).  residual_out gets h, rounded once; y is
+ * made from the unrounded h.  out gets every y `repeat` times, rows t * repeat ..
+ * t * repeat + repeat - 1 (the next experts' input), rounded once to the call's
+ * type or, with SBM_F_OUT_FP8, to codes: y / scale, to the nearest e4m3 number,
+ * halves to even, at most 448 in magnitude.  The elements of a block share a scale:
+ *   scale_block 0 (the row) or 128: fp32, max|y| / 448 rounded to fp32, at least 2^-126
+ *   scale_block 32: a byte s for 2^(s - 127), the smallest s from 1 to 254 at which
+ *     no |y| passes 448 * 2^(s - 127) (254 where one does at any; codes are then 448)
+ * A block with a NaN or an infinity has scale NaN (byte 255) and zero codes.  The
+ * mean of squares is summed in 64 bits; 16-bit results are computed in 32 bits, 8-bit
+ * ones in 64.
+ *   x:        fp16 (bf16 with SBM_F_IN_BF16, fp32 with SBM_F_IN_F32): row i at
+ *             x + i * x_stride elements
+ *   gates:    device fp32 [n_tokens x k], or NULL with k = 1: a gate of one
+ *   residual: fp16 (bf16 / fp32 with SBM_F_RESIDUAL_F32), or NULL: zeros
+ *   weight:   [dim] fp16 (bf16), or NULL: ones
+ *   residual_out: of residual's type, may be residual itself (with its stride), or
+ *             NULL: not written
+ *   out:      fp16 (bf16), or bytes with SBM_F_OUT_FP8; with k = repeat = 1 it may be
+ *             x itself (same type and stride)
+ *   scales:   [n_tokens * repeat x ceil(dim / scale_block)] fp32 (scale_block 0: one a row) or
+ *             bytes (32); NULL without SBM_F_OUT_FP8
+ * Otherwise no output overlaps an input or another output.  dim 1..32768, any
+ * alignment of rows that their elements have, k and repeat 1..64. */
+int sbm_add_rms_norm(const void* x, int64_t x_stride, const float* gates, int32_t k, const void* residual,
+                     int64_t residual_stride, const uint16_t* weight, double eps, int32_t n_tokens, int32_t dim,
+                     void* residual_out, int64_t residual_out_stride, void* out, int64_t out_stride, int32_t repeat,
+                     void* scales, int32_t scale_block, uint32_t flags, void* stream);
+
+/* Routing: each token's k experts and their gates, from the router's logits l.
+ *   s = softmax(l), or 1 / (1 + e^-l) with SBM_F_SIGMOID
+ *   c = s + bias in 64 bits (the order of l itself where bias is NULL)
+ * With n_groups > 1 the experts are that many runs of n_experts / n_groups; a
+ * group's value is the sum of its group_best (1 or 2) largest c (of s without a
+ * bias), and only experts of the top_groups groups of largest value are chosen
+ * from.  ids get the k of largest c, falling; of equal values the lower expert or
+ * group comes first.  gates get scale * s of those, divided by the sum of the
+ * token's k scores first with SBM_F_RENORM (unless that is 0).
+ * An expert with l = -inf (or bias -inf) is never chosen; where fewer than k are
+ * left the rest are id -1, gate 0.  A token with requests[t] < 0 gets only
+ * those; so does one with a NaN or +inf among its logits (or biased scores), which
+ * is counted in `error` (device uint32 that the caller zeroes, may be NULL).  The
+ * expert calls leave the rows of id -1 out, and sbm_add_rms_norm leaves them out of
+ * the sum.
+ *   logits: fp16 (bf16 with SBM_F_IN_BF16, fp32 with SBM_F_IN_F32), token t at logits +
+ *           t * row_stride elements;  bias: device fp32 [n_experts] or NULL
+ *   requests: device int32 [n_tokens] (a step plan's) or NULL
+ *   ids:    device int32 [n_tokens x k];  gates: device fp32 [n_tokens x k]
+ * n_experts 1..4096, k 1..32 and at most the experts of top_groups groups, n_groups
+ * a divisor of n_experts up to 64.  No output overlaps an input or another output. */
+int sbm_moe_route(const void* logits, int64_t row_stride, const float* bias, const int32_t* requests,
+                  int32_t n_tokens, int32_t n_experts, int32_t k, int32_t n_groups, int32_t top_groups,
+                  int32_t group_best, float scale, int32_t* ids, float* gates, uint32_t flags, uint32_t* error,
+                  void* stream);
+
+/* Workspace bytes of sbm_sample; 0 for sizes that it does not take. */
+size_t sbm_sample_workspace_bytes(int32_t n_rows, int32_t vocab);
+
+/* The next token of each row of logits l, by a given number u in [0, 1):
+ *   w_i = exp((l_i - max l) / temperature)
+ *   in the order of falling l (of equal ones the lower index first), of those above -inf:
+ *   the first top_k with w_i >= min_p stay; of these the shortest beginning whose sum
+ *   reaches top_p times theirs stays;
+ *   token = the first, in the order of indices, at which the running sum of the w that
+ *   stayed passes u times their sum W;   logprob = ln(w_token / W).
+ * Weights are computed in 64 bits and summed as whole multiples of 2^-42, so a
+ * token does not depend on the order of a sum.  temperature 0: the largest l (the
+ * lowest index of equal ones), logprob 0.  top_k <= 0, top_p >= 1, min_p <= 0: not
+ * applied; top_p <= 0 and min_p >= 1 leave the first, and those equal to it; u below 0
+ * is 0, from 1 on the last token that stayed.  A row with a NaN or +inf logit, with
+ * nothing above -inf, with a negative or NaN temperature or a NaN among its numbers
+ * gets token -1, logprob NaN, and is counted in `error` (device uint32 that the caller
+ * zeroes, may be NULL).
+ *   logits:  fp16 (bf16 with SBM_F_IN_BF16, fp32 with SBM_F_IN_F32), row r at logits +
+ *            r * row_stride elements;  vocab 1..2^20
+ *   uniforms: device fp32 [n_rows];  temperature, top_p, min_p: device fp32 [n_rows], top_k:
+ *            device int32 [n_rows]; each of the four may be NULL (1, not applied)
+ *   tokens:  device int32 [n_rows];  logprobs: device fp32 [n_rows] or NULL
+ *   workspace: device, 16-byte aligned, sbm_sample_workspace_bytes(n_rows, vocab) bytes or
+ *            more, with anything in it (calls that share one must not overlap)
+ * No output overlaps an input or another output. */
+int sbm_sample(const void* logits, int64_t row_stride, int32_t n_rows, int32_t vocab, const float* uniforms,
+               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
+               float* logprobs, uint32_t flags, void* workspace, size_t workspace_bytes, uint32_t* error, void* stream);
+
 /* ------------------------------------------- synthetic stack generation */
 /* The QMoE page's c2048 stack (1.6T parameters, under 160 GB at ~0.8 bit per
  * parameter, ~88.6% zeros; Executive Summary and "Natural sparsity") cannot be

@@ -20,6 +20,11 @@ SBM_F_IMAGE4 = 32
 SBM_F_DETERMINISTIC = 64
 SBM_F_IN_BF16 = 128
 SBM_F_NEIGHBOURS = 256
+SBM_F_SIGMOID = 512
+SBM_F_RENORM = 1024
+SBM_F_IN_F32 = 2048
+SBM_F_RESIDUAL_F32 = 4096
+SBM_F_OUT_FP8 = 8192
 SBM_ATTENTION_ZEROED = 24576
 SBM_PLAN_EPOOL = 1
 SBM_PLAN_EWIDTH = 2
@@ -91,6 +96,11 @@ _SIGS = {
     "sbm_attention_kv4_workspace_bytes": (C.c_size_t, [I, I, I, I, I]),
     "sbm_attention_kv4": (C.c_int, [P, P, I, I, P, I, P, P, I, I, I, I, I, C.c_float, P, P, C.c_uint32, P, C.c_size_t,
                                     P, P]),
+    "sbm_add_rms_norm": (C.c_int, [P, C.c_int64, P, I, P, C.c_int64, P, C.c_double, I, I, P, C.c_int64, P, C.c_int64, I, P, I,
+                                   C.c_uint32, P]),
+    "sbm_moe_route": (C.c_int, [P, C.c_int64, P, P, I, I, I, I, I, I, C.c_float, P, P, C.c_uint32, P, P]),
+    "sbm_sample_workspace_bytes": (C.c_size_t, [I, I]),
+    "sbm_sample": (C.c_int, [P, C.c_int64, I, I, P, P, P, P, P, P, P, C.c_uint32, P, C.c_size_t, P, P]),
     "sbm_trie_words": (C.c_size_t, []),
     "sbm_build_trie": (C.c_int, [P, P]),
     "sbm_gen_count": (C.c_int, [C.c_uint64, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,

@@ -747,6 +747,219 @@ def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: flo
         workspace.numel(), _error(error, at), _stream(stream, at)))
     return out if lse is None else (out, lse)
 
+# ------------------------------------------------------------------ around the experts
+
+def _rows(t, what: str, dtype, at: int, n, width: int):
+    """[n, width] with neighbouring elements and any distance of rows: (address, row stride).  n None: any."""
+    if t.dim() != 2 or t.shape[1] != width or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{what} must be [{'rows' if n is None else n}, {width}], not {tuple(t.shape)}")
+    rs, es = t.stride()
+    if es != 1 and width > 1:
+        raise ValueError(f"{what} must have neighbouring elements")
+    return _dev(t, what, dtype, at, False), rs
+
+
+def _norm(x, weight, residual, gates, eps, repeat, out, residual_out, dtype, stream, block, scales):
+    import torch
+    f32, at, flags = torch.float32, x.get_device(), 0
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, dim], or [tokens * k, dim] with gates")
+    if dtype is None:                              # the call's 16-bit type
+        for t in (weight, x, residual, None if block is not None else out):
+            if t is not None and t.dtype is not f32:
+                dtype = t.dtype
+                break
+        else:
+            raise ValueError("dtype must be given where everything is float32")
+    if dtype is torch.bfloat16:
+        flags = N.SBM_F_IN_BF16
+    elif dtype is not torch.float16:
+        raise TypeError(f"the norm's type must be float16 or bfloat16, not {dtype}")
+    n, D = x.shape
+    k, pg = 1, 0
+    if gates is not None:
+        if gates.dim() != 2 or not gates.shape[1] or gates.shape[0] * gates.shape[1] != n:
+            raise ValueError(f"gates must be [tokens, k] of the {n} rows of x, not {tuple(gates.shape)}")
+        k, pg = gates.shape[1], _dev(gates, "gates", f32, at)
+    T = n // k
+    if x.dtype is f32:
+        flags |= N.SBM_F_IN_F32
+        px, sx = _rows(x, "x", f32, at, None, D)
+    else:
+        px, sx = _rows(x, "x", dtype, at, None, D)
+    pw = pr = sr = po = so = 0
+    if weight is not None:
+        if weight.numel() != D:
+            raise ValueError(f"weight must hold {D} elements")
+        pw = _dev(weight, "weight", dtype, at)
+    if residual is not None:
+        of = residual.dtype
+        if of is f32:
+            flags |= N.SBM_F_RESIDUAL_F32
+        pr, sr = _rows(residual, "residual", f32 if of is f32 else dtype, at, T, D)
+        if residual_out is None:
+            residual_out = residual.new_empty((T, D)) if stream is None else _made_on(stream, residual.new_empty, (T, D))
+            po, so = residual_out.data_ptr(), D
+    elif residual_out is not None:
+        of = residual_out.dtype
+        if of is f32:
+            flags |= N.SBM_F_RESIDUAL_F32
+    if residual_out is not None and not po:
+        po, so = _rows(residual_out, "residual_out", f32 if of is f32 else dtype, at, T, D)
+    rows, ps = T * repeat, 0
+    if block is None:
+        kind = dtype
+    else:
+        kind = torch.float8_e4m3fn
+        flags |= N.SBM_F_OUT_FP8
+        many, held = (-(-D // block) if block else 1), torch.uint8 if block == 32 else f32
+        if scales is None:
+            scales = x.new_empty((rows, many), dtype=held) if stream is None else \
+                _made_on(stream, x.new_empty, (rows, many), dtype=held)
+            ps = scales.data_ptr()
+        elif scales.shape != (rows, many):
+            raise ValueError(f"scales must be {(rows, many)}, not {tuple(scales.shape)}")
+        else:
+            ps = _dev(scales, "scales", held, at)
+    if out is None:
+        out = x.new_empty((rows, D), dtype=kind) if stream is None else _made_on(stream, x.new_empty, (rows, D), dtype=kind)
+        pout, sout = out.data_ptr(), D
+    else:
+        pout, sout = _rows(out, "out" if block is None else "codes", kind, at, rows, D)
+    check(lib().sbm_add_rms_norm(px, sx, pg, k, pr, sr, pw, eps, T, D, po, so, pout, sout, repeat, ps, block or 0, flags,
+                                 _stream(stream, at)))
+    return out, scales, residual_out
+
+
+def add_rms_norm(x, weight=None, residual=None, gates=None, eps: float = 1e-6, repeat: int = 1, out=None, residual_out=None,
+                 dtype=None, stream=None):
+    """Norm of residual + x, in one launch (sbm_add_rms_norm): x [T, D], or with
+    gates fp32 [T, k] the experts' rows [T * k, D], summed by them (a row of gate
+    0 is not read).  Returns (out [T * repeat, D], residual_out [T, D]): the
+    norm times weight [D] (None: ones), every row `repeat` times in turn, and the sum
+    before it (None without a residual, unless residual_out is given; it may be
+    residual).  x and residual may be float32; dtype: the 16-bit type, by default
+    weight's, x's or residual's."""
+    out, _, residual_out = _norm(x, weight, residual, gates, eps, repeat, out, residual_out, dtype, stream, None, None)
+    return out, residual_out
+
+
+def add_rms_norm_fp8(x, weight=None, residual=None, gates=None, eps: float = 1e-6, repeat: int = 1, scale_block: int = 0,
+                     codes=None, scales=None, residual_out=None, dtype=None, stream=None):
+    """add_rms_norm with 8-bit results: (codes float8_e4m3fn [T * repeat, D],
+    scales, residual_out).  scale_block 0: scales fp32 [T * repeat, 1], one for a
+    row; 128: fp32 [T * repeat, ceil(D / 128)]; 32: uint8 s for 2^(s - 127), [T *
+    repeat, ceil(D / 32)]."""
+    return _norm(x, weight, residual, gates, eps, repeat, codes, residual_out, dtype, stream, scale_block, scales)
+
+
+def _logits(t, at: int):
+    """(address, row stride, flags) of [rows, width] logits."""
+    import torch
+    if t.dim() != 2:
+        raise ValueError("logits must be [rows, width]")
+    flags = N.SBM_F_IN_F32 if t.dtype is torch.float32 else N.SBM_F_IN_BF16 if t.dtype is torch.bfloat16 else 0
+    if not flags and t.dtype is not torch.float16:
+        raise TypeError(f"logits must be float32, float16 or bfloat16, not {t.dtype}")
+    p, stride = _rows(t, "logits", t.dtype, at, None, t.shape[1])
+    return p, stride, flags
+
+
+def moe_route(logits, k: int, bias=None, sigmoid: bool = False, n_groups: int = 1, top_groups: int = 1, group_best: int = 2,
+              renormalise: bool = False, scale: float = 1.0, requests=None, ids=None, gates=None, error=None, stream=None):
+    """Each token's k experts from the router's logits [T, E] (sbm_moe_route):
+    (ids int32 [T, k], gates fp32 [T, k]) by falling softmax (or sigmoid) score, plus
+    bias [E] for the choice, out of the top_groups best of n_groups groups.
+    requests (a plan's, int32 [T]): negative ones get id -1, gate 0."""
+    import torch
+    i32, f32, at = torch.int32, torch.float32, logits.get_device()
+    p, stride, flags = _logits(logits, at)
+    T, E = logits.shape
+    if sigmoid:
+        flags |= N.SBM_F_SIGMOID
+    if renormalise:
+        flags |= N.SBM_F_RENORM
+    pb = pq = 0
+    if bias is not None:
+        if bias.numel() != E:
+            raise ValueError(f"bias must hold {E} elements")
+        pb = _dev(bias, "bias", f32, at)
+    if requests is not None:
+        if requests.numel() != T:
+            raise ValueError(f"requests must hold {T} elements")
+        pq = _dev(requests, "requests", i32, at)
+    if ids is None:
+        ids = logits.new_empty((T, k), dtype=i32) if stream is None else _made_on(stream, logits.new_empty, (T, k), dtype=i32)
+        pi = ids.data_ptr()
+    elif ids.shape != (T, k):
+        raise ValueError(f"ids must be {(T, k)}, not {tuple(ids.shape)}")
+    else:
+        pi = _dev(ids, "ids", i32, at)
+    if gates is None:
+        gates = logits.new_empty((T, k), dtype=f32) if stream is None else _made_on(stream, logits.new_empty, (T, k), dtype=f32)
+        pg = gates.data_ptr()
+    elif gates.shape != (T, k):
+        raise ValueError(f"gates must be {(T, k)}, not {tuple(gates.shape)}")
+    else:
+        pg = _dev(gates, "gates", f32, at)
+    check(lib().sbm_moe_route(p, stride, pb, pq, T, E, k, n_groups, top_groups, group_best, scale, pi, pg, flags,
+                              _error(error, at), _stream(stream, at)))
+    return ids, gates
+
+
+def sample_workspace_bytes(n_rows: int, vocab: int) -> int:
+    return int(lib().sbm_sample_workspace_bytes(n_rows, vocab))
+
+
+def alloc_sample_workspace(n_rows: int, vocab: int, device="cuda"):
+    import torch
+    return torch.empty(max(sample_workspace_bytes(n_rows, vocab), 16), dtype=torch.uint8, device=device)
+
+
+def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprobs=None,
+           return_logprobs: bool = False, workspace=None, error=None, stream=None):
+    """The next token of each row of logits [R, V] by the number uniforms[r] in
+    [0, 1) (sbm_sample): softmax of logits / temperature[r] over the top_k[r] tokens
+    of weight min_p[r] at least (that of the likeliest is 1), of these the
+    likeliest that hold top_p[r].  All fp32 [R], top_k int32 [R], None: not
+    applied.  Returns tokens int32 [R], or (tokens, logprobs fp32 [R]) with
+    return_logprobs or a logprobs buffer; -1 for a row that has no distribution."""
+    import torch
+    i32, f32, at = torch.int32, torch.float32, logits.get_device()
+    p, stride, flags = _logits(logits, at)
+    R, V = logits.shape
+    given = []
+    for what, t, kind in (("uniforms", uniforms, f32), ("temperature", temperature, f32), ("top_k", top_k, i32),
+                          ("top_p", top_p, f32), ("min_p", min_p, f32)):
+        if t is None:
+            if what == "uniforms":
+                raise ValueError("uniforms must be given")
+            given.append(0)
+        elif t.numel() != R:
+            raise ValueError(f"{what} must hold {R} elements")
+        else:
+            given.append(_dev(t, what, kind, at))
+    if tokens is None:
+        tokens = logits.new_empty(R, dtype=i32) if stream is None else _made_on(stream, logits.new_empty, R, dtype=i32)
+        pt = tokens.data_ptr()
+    elif tokens.numel() != R:
+        raise ValueError(f"tokens must hold {R} elements")
+    else:
+        pt = _dev(tokens, "tokens", i32, at)
+    pl = 0
+    if logprobs is not None:
+        if logprobs.numel() != R:
+            raise ValueError(f"logprobs must hold {R} elements")
+        pl = _dev(logprobs, "logprobs", f32, at)
+    elif return_logprobs:
+        logprobs = logits.new_empty(R, dtype=f32) if stream is None else _made_on(stream, logits.new_empty, R, dtype=f32)
+        pl = logprobs.data_ptr()
+    if workspace is None:
+        workspace = _made_on(stream, alloc_sample_workspace, R, V, logits.device)
+    check(lib().sbm_sample(p, stride, R, V, *given, pt, pl, flags, _dev(workspace, "workspace", torch.uint8, at),
+                           workspace.numel(), _error(error, at), _stream(stream, at)))
+    return tokens if logprobs is None else (tokens, logprobs)
+
 # ------------------------------------------------------------------ synthetic stacks
 
 def build_trie(words: np.ndarray) -> np.ndarray:

@@ -6,6 +6,7 @@
 #include <algorithm>
 
 #include "sbm_kv4.h"
+#include "sbm_num.h"
 
 namespace sbm {
 namespace {
@@ -168,12 +169,6 @@ struct QkArgs {
   int32_t per_token;     // log2 of the groups of lanes that a token has in a workgroup
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f32(uint16_t u) {
-  if constexpr (__is_same(T, __bf16)) return __uint_as_float((uint32_t)u << 16);
-  else return (float)__builtin_bit_cast(_Float16, u);
-}
-
 // Eight elements: one 16-byte access where every address allows it (kVec), else eight.
 template <bool kVec>
 __device__ __forceinline__ void load8(const uint16_t* p, uint16_t* x) {
@@ -193,21 +188,6 @@ __device__ __forceinline__ void store8(uint16_t* p, const uint16_t* x) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) p[j] = x[j];
   }
-}
-
-// One rounding to T.  From 64 bits the way goes over 32, so what those cannot
-// hold is first gathered in their lowest bit (round to odd): the second
-// rounding then sees on which side of a border the value was.
-template <typename T>
-__device__ __forceinline__ uint16_t round_once(float y) {
-  return __builtin_bit_cast(uint16_t, (T)y);
-}
-template <typename T>
-__device__ __forceinline__ uint16_t round_once(double y) {
-  uint64_t b = __builtin_bit_cast(uint64_t, y);
-  const uint32_t low = (uint32_t)b & 0x1FFFFFFFu;
-  b = (b & ~0x1FFFFFFFull) | (low ? 0x20000000u : 0u);
-  return round_once<T>((float)__builtin_bit_cast(double, b));
 }
 
 // v summed over groups of kL lanes, in all of them.
@@ -230,18 +210,6 @@ __device__ __forceinline__ C group_sum(C v) {
   if constexpr (kL > 8) v += other_lane<0x140>(v);
   if constexpr (kL > 16) v += __shfl_xor(v, 16, 64);
   return v;
-}
-
-// 1 / sqrt(x): the hardware's estimate and one step of third order (2^-23 to below 2^-60).
-__device__ __forceinline__ double inverse_root(double x) {
-  const double y = __builtin_amdgcn_rsq(x), e = __builtin_fma(-x * y, y, 1.0);
-  const double z = __builtin_fma(y * e, __builtin_fma(e, 0.375, 0.5), y);
-  return x == 0. || x == (double)INFINITY ? y : z;
-}
-__device__ __forceinline__ float inverse_root(float x) {
-  if (!(x > 1e-30f && x < 1e30f)) return 1.f / sqrtf(x);
-  const float y = __builtin_amdgcn_rsqf(x), e = __builtin_fmaf(-x * y, y, 1.f);
-  return __builtin_fmaf(y * e, 0.5f, y);
 }
 
 // What a lane keeps of its token and its eight dimensions for all the heads it takes.
@@ -285,9 +253,6 @@ __device__ __forceinline__ void load_turn(QkTurn<C>& r, const uint16_t* weight, 
     }
   }
 }
-
-__device__ __forceinline__ float fused(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
-__device__ __forceinline__ double fused(double a, double b, double c) { return __builtin_fma(a, b, c); }
 
 // Norm and rotation of a lane's eight elements of one head; C: the type it is computed in.
 template <typename T, typename C, int D>

@@ -1,0 +1,358 @@
+// The norm between a decoder's parts: the residual's addition, the sum over a
+// token's experts, root-mean-square norm, and results in 16 or in 8 bits.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "sbm_internal.h"
+#include "sbm_num.h"
+
+namespace sbm {
+namespace {
+
+constexpr int kMostDim = 32768;
+constexpr int kMostThreads = 1024;
+
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  void* residual_out;
+  const uint16_t* weight;
+  const float* gates;
+  void* out;
+  void* scales;
+  int64_t x_stride, r_stride, ro_stride, o_stride;      // elements
+  double eps;
+  int32_t dim, k, repeat, block;                        // block: elements that share a scale, the row's if `whole`
+  bool whole, powers;                                   // powers: scales are bytes
+};
+
+// Eight elements as they are in memory.  Rows may start anywhere an element may: the hardware takes a 16-byte access at any
+// address.
+template <bool kF32>
+struct Raw {
+  uint32_t v[kF32 ? 8 : 4];
+};
+
+template <bool kF32>
+__device__ __forceinline__ Raw<kF32> load_raw(const void* row, int d0, int dim) {
+  Raw<kF32> r;
+  if (d0 + 8 <= dim) {
+    __builtin_memcpy(&r, (const char*)row + (int64_t)d0 * (kF32 ? 4 : 2), sizeof r);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (kF32) {
+        r.v[j] = d0 + j < dim ? ((const uint32_t*)row)[d0 + j] : 0u;
+      } else {
+        const uint32_t u = d0 + j < dim ? ((const uint16_t*)row)[d0 + j] : 0u;
+        r.v[j >> 1] = j & 1 ? r.v[j >> 1] | u << 16 : u;
+      }
+    }
+  }
+  return r;
+}
+
+template <typename T, bool kF32>
+__device__ __forceinline__ float value(const Raw<kF32>& r, int j) {
+  if constexpr (kF32) return __uint_as_float(r.v[j]);
+  else return to_f32<T>((uint16_t)(r.v[j >> 1] >> 16 * (j & 1)));
+}
+
+// The first n of eight elements of kBytes each.
+template <int kBytes>
+__device__ __forceinline__ void store_raw(void* p, const void* x, int n) {
+  if (n >= 8) {
+    __builtin_memcpy(p, x, 8 * kBytes);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < n) __builtin_memcpy((char*)p + j * kBytes, (const char*)x + j * kBytes, kBytes);
+    }
+  }
+}
+
+
+template <typename C>
+struct Sum {
+  __device__ C operator()(C a, C b) const { return a + b; }
+};
+template <typename C>
+struct Most {      // NaN stays
+  __device__ C operator()(C a, C b) const { return a >= b || a != a ? a : b; }
+};
+
+// v joined over the workgroup's waves, in all of its threads, in an order that does not change.
+template <typename Op, typename C>
+__device__ __forceinline__ C over_row(C v, C* shared) {
+  Op op;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = op(v, __shfl_xor(v, d, 64));
+  const int waves = (int)blockDim.x >> 6;
+  if (waves > 1) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = shared[0];
+    for (int w = 1; w < waves; ++w) v = op(v, shared[w]);
+  }
+  return v;
+}
+
+// A workgroup holds a row in its registers, kN times eight elements a thread: everything is read once and written once.  The
+// mean of squares is summed in 64 bits (f64 runs at the rate of unpacked f32 here), so that no row of finite numbers
+// overflows it; what becomes 8 bits is computed in 64 bits throughout (C), so that a code beside the border of two does not
+// depend on the order of a sum.
+template <typename T, bool kXF, bool kRF, bool k8, int kN>
+__global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
+  using C = std::conditional_t<k8, double, float>;
+  __shared__ double s_sum[kMostThreads / 64];
+  const int64_t t = blockIdx.x;
+  const int G = (int)blockDim.x, tid = (int)threadIdx.x;
+  C h[kN][8];
+  if (a.residual) {
+    const char* row = (const char*)a.residual + t * a.r_stride * (kRF ? 4 : 2);
+    Raw<kRF> r[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) r[i] = load_raw<kRF>(row, (tid + i * G) * 8, a.dim);
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = (C)value<T, kRF>(r[i], j);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = (C)0;
+  }
+  for (int e = 0; e < a.k; ++e) {
+    const float gate = a.gates ? a.gates[t * a.k + e] : 1.f;
+    if (gate == 0.f) continue;
+    const char* row = (const char*)a.x + (t * a.k + e) * a.x_stride * (kXF ? 4 : 2);
+    Raw<kXF> r[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) r[i] = load_raw<kXF>(row, (tid + i * G) * 8, a.dim);
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = fused((C)gate, (C)value<T, kXF>(r[i], j), h[i][j]);
+  }
+  if (a.residual_out) {
+    char* row = (char*)a.residual_out + t * a.ro_stride * (kRF ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int d0 = (tid + i * G) * 8;
+      if constexpr (kRF) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = (float)h[i][j];
+        store_raw<4>(row + (int64_t)d0 * 4, y, a.dim - d0);
+      } else {
+        uint16_t y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = round_once<T>(h[i][j]);
+        store_raw<2>(row + (int64_t)d0 * 2, y, a.dim - d0);
+      }
+    }
+  }
+  double ss = 0;
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)h[i][j], (double)h[i][j], ss);
+  const double mean = over_row<Sum<double>>(ss, s_sum) / (double)a.dim + a.eps;
+  const double inv = inverse_root(mean);
+  // weights; what is behind the row's end is zero
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int d0 = (tid + i * G) * 8;
+    Raw<false> w;
+    if (a.weight) w = load_raw<false>(a.weight, d0, a.dim);
+    if (k8 || (mean > 1e-30 && mean < 1e30)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = (h[i][j] * (C)inv) * (a.weight ? (C)value<T, false>(w, j) : (C)1);
+    } else {                                            // its root is no normal number of 32 bits
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        h[i][j] = (C)((double)h[i][j] * inv) * (a.weight ? (C)value<T, false>(w, j) : (C)1);
+    }
+  }
+  if constexpr (!k8) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int d0 = (tid + i * G) * 8;
+      uint16_t y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = round_once<T>(h[i][j]);
+      for (int r = 0; r < a.repeat; ++r)
+        store_raw<2>((uint16_t*)a.out + (t * a.repeat + r) * a.o_stride + d0, y, a.dim - d0);
+    }
+  } else {
+    double top[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      top[i] = fabs(h[i][0]);
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top[i] = Most<double>()(top[i], fabs(h[i][j]));
+    }
+    if (a.whole) {
+      double all = top[0];
+#pragma unroll
+      for (int i = 1; i < kN; ++i) all = Most<double>()(all, top[i]);
+      all = over_row<Most<double>>(all, s_sum);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) top[i] = all;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {                    // 4 or 16 neighbouring lanes hold a block
+        top[i] = Most<double>()(top[i], __shfl_xor(top[i], 1, 64));
+        top[i] = Most<double>()(top[i], __shfl_xor(top[i], 2, 64));
+        if (a.block == 128) {
+          top[i] = Most<double>()(top[i], __shfl_xor(top[i], 4, 64));
+          top[i] = Most<double>()(top[i], __shfl_xor(top[i], 8, 64));
+        }
+      }
+    }
+    const int n_blocks = (a.dim + a.block - 1) / a.block;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int d0 = (tid + i * G) * 8;
+      if (d0 >= a.dim) continue;
+      const bool bad = !(top[i] < (double)INFINITY);
+      float scale;
+      uint8_t power = 255;
+      double by;
+      if (a.powers) {
+        // the least power of two at which nothing passes 448 = 1.75 * 2^8
+        const uint64_t b = __builtin_bit_cast(uint64_t, top[i]);
+        int e = (int)(b >> 52) - 1023 - 8 + ((b & 0xFFFFFFFFFFFFFull) > 0xC000000000000ull);
+        e = min(max(e, -126), 127);
+        if (!bad) power = (uint8_t)(e + 127);
+        by = __builtin_bit_cast(double, (uint64_t)(1023 - e) << 52);
+      } else {
+        scale = fmaxf((float)(top[i] / 448.), 0x1p-126f);
+        if (bad) scale = __builtin_nanf("");
+        by = 1. / (double)scale;
+      }
+      uint32_t y[2] = {0u, 0u};
+      if (!bad) {
+        float q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(to_odd(h[i][j] * by), -448.f), 448.f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          y[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * j], q[4 * j + 1], 0, false);
+          y[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * j + 2], q[4 * j + 3], (int)y[j], true);
+        }
+      }
+      for (int r = 0; r < a.repeat; ++r) {
+        const int64_t row = t * a.repeat + r;
+        store_raw<1>((uint8_t*)a.out + row * a.o_stride + d0, y, a.dim - d0);
+        if (d0 % a.block == 0) {
+          if (a.powers) ((uint8_t*)a.scales)[row * n_blocks + d0 / 32] = power;
+          else ((float*)a.scales)[row * n_blocks + d0 / a.block] = scale;
+        }
+      }
+    }
+  }
+}
+
+// Rows of a call: n of them, each `bytes` long, `stride` bytes apart.
+struct Rows {
+  const void* p;
+  int64_t n, bytes, stride;
+};
+
+bool overlap(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || a.n <= 0 || b.n <= 0) return false;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  const uintptr_t xe = x + (uintptr_t)((a.n - 1) * a.stride + a.bytes), ye = y + (uintptr_t)((b.n - 1) * b.stride + b.bytes);
+  if (xe <= y || ye <= x) return false;
+  if (a.stride != b.stride || a.stride < a.bytes + b.bytes) return true;
+  // columns of one array: the second's begin behind the first's end in every row, and end before its next row
+  const uintptr_t off = x <= y ? (y - x) % (uintptr_t)a.stride : (uintptr_t)a.stride - (x - y) % (uintptr_t)a.stride;
+  return off < (uintptr_t)a.bytes || off + (uintptr_t)b.bytes > (uintptr_t)a.stride;
+}
+
+template <typename T, bool kXF, bool kRF, bool k8>
+void launch_norm(const NormArgs& a, int32_t n_tokens, hipStream_t s) {
+  const int chunks = (a.dim + 7) / 8;
+  const int n = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+  const int threads = std::max(64, ((chunks + n - 1) / n + 63) / 64 * 64);
+  const dim3 grid((unsigned)n_tokens), block((unsigned)threads);
+  if (n == 1) hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, 1>), grid, block, 0, s, a);
+  else if (n == 2) hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, 4>), grid, block, 0, s, a);
+}
+
+template <typename T>
+void launch_norm(const NormArgs& a, int32_t n_tokens, uint32_t flags, hipStream_t s) {
+  const bool xf = flags & SBM_F_IN_F32, rf = flags & SBM_F_RESIDUAL_F32, f8 = flags & SBM_F_OUT_FP8;
+#define SBM_NORM(X, R, E) \
+  if (xf == X && rf == R && f8 == E) launch_norm<T, X, R, E>(a, n_tokens, s)
+  SBM_NORM(false, false, false);
+  SBM_NORM(false, false, true);
+  SBM_NORM(false, true, false);
+  SBM_NORM(false, true, true);
+  SBM_NORM(true, false, false);
+  SBM_NORM(true, false, true);
+  SBM_NORM(true, true, false);
+  SBM_NORM(true, true, true);
+#undef SBM_NORM
+}
+
+}  // namespace
+}  // namespace sbm
+
+using namespace sbm;
+
+extern "C" int sbm_add_rms_norm(const void* x, int64_t x_stride, const float* gates, int32_t k, const void* residual,
+                                int64_t residual_stride, const uint16_t* weight, double eps, int32_t n_tokens, int32_t dim,
+                                void* residual_out, int64_t residual_out_stride, void* out, int64_t out_stride,
+                                int32_t repeat, void* scales, int32_t scale_block, uint32_t flags, void* stream) {
+  if (flags & ~(SBM_F_IN_BF16 | SBM_F_IN_F32 | SBM_F_RESIDUAL_F32 | SBM_F_OUT_FP8))
+    return fail(SBM_EINVAL, "unknown flags 0x%x", flags);
+  if (n_tokens < 0 || dim < 1 || dim > kMostDim)
+    return fail(SBM_EINVAL, "bad n_tokens=%d or dim=%d (1..%d)", n_tokens, dim, kMostDim);
+  if (k < 1 || k > 64 || repeat < 1 || repeat > 64) return fail(SBM_EINVAL, "k=%d or repeat=%d outside 1..64", k, repeat);
+  if (!(eps >= 0.)) return fail(SBM_EINVAL, "bad eps");
+  const bool xf = flags & SBM_F_IN_F32, rf = flags & SBM_F_RESIDUAL_F32, f8 = flags & SBM_F_OUT_FP8;
+  if (f8 ? scale_block != 0 && scale_block != 32 && scale_block != 128 : scale_block != 0)
+    return fail(SBM_EINVAL, "scale_block=%d is not 0, 32 or 128 (0 for 16-bit results)", scale_block);
+  const int64_t most = (int64_t)1 << 40;
+  if (x_stride < 0 || residual_stride < 0 || residual_out_stride < 0 || out_stride < 0 || x_stride > most ||
+      residual_stride > most || residual_out_stride > most || out_stride > most)
+    return fail(SBM_EINVAL, "bad row stride");
+  if (n_tokens == 0) return SBM_OK;
+  if (k > 1 && !gates) return fail(SBM_EINVAL, "k=%d rows of a token need gates", k);
+  if (!x || !out || (f8 && !scales)) return fail(SBM_EINVAL, "null pointer");
+  if ((n_tokens > 1 && ((residual_out && residual_out_stride < dim) || out_stride < dim)) || (repeat > 1 && out_stride < dim))
+    return fail(SBM_EINVAL, "rows of a result overlap");
+  const int32_t block = scale_block ? scale_block : dim;
+  const int64_t xb = xf ? 4 : 2, rb = rf ? 4 : 2, ob = f8 ? 1 : 2, sb = scale_block == 32 ? 1 : 4;
+  const int64_t n_blocks = (dim + block - 1) / block, T = n_tokens;
+  if (((uintptr_t)x | (uintptr_t)0) % xb || (uintptr_t)residual % rb || (uintptr_t)residual_out % rb ||
+      (uintptr_t)weight % 2 || (uintptr_t)out % ob || (f8 && (uintptr_t)scales % sb) || (uintptr_t)gates % 4)
+    return fail(SBM_EINVAL, "misaligned array");
+  const Rows ins[] = {{x, T * k, dim * xb, x_stride * xb}, {residual, T, dim * rb, residual_stride * rb},
+                      {weight, 1, dim * 2, 0}, {gates, 1, T * k * 4, 0}};
+  const Rows outs[] = {{residual_out, T, dim * rb, residual_out_stride * rb}, {out, T * repeat, dim * ob, out_stride * ob},
+                       {f8 ? scales : nullptr, 1, T * repeat * n_blocks * sb, 0}};
+  // a row's workgroup has read the row before it writes
+  const bool in_place = residual_out == residual && (residual_out_stride == residual_stride || T == 1);
+  const bool over_x = out == x && k == 1 && repeat == 1 && xb == ob && (out_stride == x_stride || T == 1);
+  for (const Rows& o : outs) {
+    for (const Rows& i : ins)
+      if (!(in_place && &o == outs && &i == ins + 1) && !(over_x && &o == outs + 1 && &i == ins) && overlap(o, i))
+        return fail(SBM_EINVAL, "an output overlaps an input");
+    for (const Rows& other : outs)
+      if (&other < &o && overlap(o, other)) return fail(SBM_EINVAL, "outputs overlap");
+  }
+  const NormArgs a{x, residual, residual_out, weight, gates, out, scales, x_stride, residual_stride, residual_out_stride,
+                   out_stride, eps, dim, k, repeat, block, scale_block == 0, scale_block == 32};
+  if (flags & SBM_F_IN_BF16) launch_norm<__bf16>(a, n_tokens, flags, (hipStream_t)stream);
+  else launch_norm<_Float16>(a, n_tokens, flags, (hipStream_t)stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(SBM_EHIP, "add_rms_norm launch: %s", hipGetErrorString(e));
+  return SBM_OK;
+}
