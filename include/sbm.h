@@ -591,7 +591,8 @@ int sbm_moe_route(const void* logits, int64_t row_stride, const float* bias, con
                   int32_t group_best, float scale, int32_t* ids, float* gates, uint32_t flags, uint32_t* error,
                   void* stream);
 
-/* Workspace bytes of sbm_sample; 0 for sizes that it does not take. */
+/* Workspace bytes of sbm_sample, enough for fewer rows and a shorter vocabulary
+ * too; 0 for sizes that it does not take. */
 size_t sbm_sample_workspace_bytes(int32_t n_rows, int32_t vocab);
 
 /* The next token of each row of logits l, by a given number u in [0, 1):

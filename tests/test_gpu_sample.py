@@ -165,7 +165,7 @@ def test_strides_and_buffers(dev):
 def test_workspace_of_anything_is_used_again(dev):
     """Calls of other sizes and types one after the other in one workspace, whatever it held."""
     from sub_bit_moe_amd import api
-    ws = torch.full((max(api.sample_workspace_bytes(r, v) for r, v in ((1, 200000), (70, 9000), (300, 100))),), 0xA5, dtype=torch.uint8, device=dev)
+    ws = torch.full((max(api.sample_workspace_bytes(r, v) for r, v in ((2, 200000), (70, 9000), (300, 100))),), 0xA5, dtype=torch.uint8, device=dev)
     for rows, vocab, dtype in ((1, 200000, torch.float32), (70, 9000, torch.bfloat16), (300, 100, torch.float16), (2, 200000, torch.bfloat16)):
         l, u = (3 * torch.randn(rows, vocab, device=dev)).to(dtype), torch.rand(rows, device=dev)
         p = torch.full((rows,), 0.9, device=dev)
@@ -173,6 +173,16 @@ def test_workspace_of_anything_is_used_again(dev):
         for _ in range(3):
             assert torch.equal(api.sample(l, u, top_p=p, workspace=ws), want)
         ws.random_(0, 255)
+
+
+def test_a_workspace_serves_smaller_calls(dev):
+    """One made for the most rows and tokens, for every step of a batch that shrinks."""
+    from sub_bit_moe_amd import api
+    ws = api.alloc_sample_workspace(600, 70000, dev)
+    for rows, vocab in ((600, 70000), (300, 70000), (256, 70000), (255, 40000), (100, 33000), (3, 70000), (1, 50)):
+        l, u = 3 * torch.randn(rows, vocab, device=dev), torch.rand(rows, device=dev)
+        k = torch.full((rows,), 300, dtype=torch.int32, device=dev)
+        assert torch.equal(api.sample(l, u, top_k=k, workspace=ws), api.sample(l, u, top_k=k))
 
 
 def test_offsets_past_32_bits(dev):
