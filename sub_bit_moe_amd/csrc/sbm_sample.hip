@@ -18,6 +18,9 @@ constexpr int kMostTiles = kMostVocab / kTile;
 constexpr int kBins = 4096;                  // of the distance below the largest logit: 128 to a doubling, from 2^-12 on
 constexpr int kDigits = 1024;                // ten bits of an order at a time
 constexpr int kList = 6144;                  // tokens of a row that are put in order in LDS
+constexpr int kHeld = 2;                     // tiles of a wave that stay in its registers
+constexpr int kGroup = kPer;                 // neighbours of which one counts for a top_k
+constexpr int kMostGroups = 2048;
 constexpr int kMostParts = 64;               // workgroups of a row
 static_assert(kMostTiles <= kSThreads && kDigits == kSThreads, "a thread has a tile, or a digit");
 
@@ -34,8 +37,8 @@ struct SampleArgs {
   int32_t vocab, parts;
 };
 
-// What a row keeps between its filters: tokens in bins below lo stay (as far as min_p lets them), tokens in lo .. hi are put
-// in order to see.
+// Where the last token that stays is: tokens in bins below lo stay (as far as min_p lets them), tokens in lo .. hi are put in
+// order to see.
 struct Range {
   uint32_t lo, hi;
   uint64_t target;                           // how many of those in order, or how much weight
@@ -46,15 +49,21 @@ struct RowSpace {
   uint32_t done[2], n_list, first;           // workgroups that ended; tokens to be ordered; the first of the largest
   Range range;
   float part_max[kMostParts];
-  uint64_t bins[kBins];
+  uint64_t bins[kBins];                      // weights; counts in the first 4 bytes each
   uint64_t list[kList];
   uint64_t tiles[1];                         // one for each kTile tokens
 };
 
 constexpr int64_t row_space(int vocab) { return ((int64_t)sizeof(RowSpace) + 8 * ((vocab + kTile - 1) / kTile) + 255) / 256 * 256; }
 
-// Weights are whole numbers of 2^-42, so that their sums (at most 2^20 of at most 1) do not depend on an order.
-constexpr double kUnit = 0x1p42;
+// Weights are whole numbers of a unit, so that their sums do not depend on an order: 2^-62 times the least power of two that is
+// not below the vocabulary (or 2048), 2^-42 for the largest.
+struct Unit {
+  double magic;                              // 2^52 units: the low bits of magic + w are w in units, rounded
+  __device__ __forceinline__ uint64_t operator()(double w) const {
+    return __builtin_bit_cast(uint64_t, w + magic) - __builtin_bit_cast(uint64_t, magic);
+  }
+};
 
 // 32 bits that order as the numbers do; both zeros are one.
 __device__ __forceinline__ uint32_t key_of(float l) {
@@ -68,16 +77,21 @@ __device__ __forceinline__ uint64_t order_of(float l, uint32_t i) { return (uint
 __device__ __forceinline__ float logit_of(uint64_t order) { return of_key(~(uint32_t)(order >> 20)); }
 __device__ __forceinline__ uint32_t index_of(uint64_t order) { return (uint32_t)order & 0xFFFFFu; }
 
-// The bin of a logit d below the largest (d >= 0, or NaN where both are -inf).
+// The bin of a logit below the largest, by their distance; and the distance at which a bin begins.
+constexpr uint32_t kFirstBin = (127 - 12) << 7;
 __device__ __forceinline__ uint32_t bin_of(float most, float l) {
-  const uint32_t b = __float_as_uint(most - l) >> 16, from = (127 - 12) << 7;
-  return min(max(b, from) - from, (uint32_t)kBins - 1);
+  const uint32_t b = __float_as_uint(most - l) >> 16;
+  return min(max(b, kFirstBin) - kFirstBin, (uint32_t)kBins - 1);
+}
+__device__ __forceinline__ float begin_of(uint32_t bin) {
+  return bin == 0 ? 0.f : bin >= kBins ? INFINITY : __uint_as_float((bin + kFirstBin) << 16);
 }
 
 // A row's parameters.
 struct Row {
   const char* at;
   double most, slope, least;                 // the largest logit; log2(e) / temperature; min_p
+  Unit units;
   float u, top_p, temperature;
   int32_t top_k;                             // 0: all
   bool bad;
@@ -94,38 +108,43 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t r, int bytes)
   if (f.top_k < 0 || f.top_k >= a.vocab) f.top_k = 0;
   f.bad = f.u != f.u || !(f.temperature >= 0.f) || f.top_p != f.top_p || min_p != min_p;
   f.least = min_p > 0.f ? fmin((double)min_p, 1.) : 0.;
-  f.slope = f.temperature > 0.f ? 1.4426950408889634 / (double)f.temperature : 0.;
+  f.slope = f.temperature > 0.f ? fmax(1.4426950408889634 / (double)f.temperature, 1e-300) : 0.;      // not 0 * -inf
   f.most = 0;
+  const int bits = max(32 - __builtin_clz(max((unsigned)a.vocab, 2u) - 1u), 11);
+  f.units.magic = __builtin_amdgcn_ldexp(1., bits - 10);
   return f;
 }
 
+// a * b + c with c the same in all lanes: the compiler would copy c into a register that the sum then overwrites.
+__device__ __forceinline__ double fma_const(double a, double b, double c) {
+  double d;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+  return d;
+}
+
 // exp((l - most) / temperature) = 2^x, to 4e-14 of itself: x's whole part goes to the exponent, 2^f for the rest, |f| <= 1/2,
-// is a polynomial of degree 9 that interpolates it at Chebyshev's points (3.7e-14 off at most) and is 1 at 0.
+// is a polynomial of degree 9 that interpolates it at Chebyshev's points (3.7e-14 off at most) and is 1 at 0.  A logit of
+// -inf gives 0: its f is no number, which the maximum takes for -1/2, and its exponent is below all.
 __device__ __forceinline__ double weight(const Row& f, float l) {
-  const double x = fmax(((double)l - f.most) * f.slope, -100.);
-  const double n = rint(x), y = x - n;
-  double p = 0x1.b63880a30e9ffp-24;
-  p = __builtin_fma(p, y, 0x1.63d136366db24p-20);
-  p = __builtin_fma(p, y, 0x1.ffcb9515a8016p-17);
-  p = __builtin_fma(p, y, 0x1.4308ac85aa947p-13);
-  p = __builtin_fma(p, y, 0x1.5d87fe86fe88ep-10);
-  p = __builtin_fma(p, y, 0x1.3b2ab7181b755p-7);
-  p = __builtin_fma(p, y, 0x1.c6b08d7047e52p-5);
-  p = __builtin_fma(p, y, 0x1.ebfbdff823cedp-3);
-  p = __builtin_fma(p, y, 0x1.62e42fefa39efp-1);
+  const double x = ((double)l - f.most) * f.slope;
+  const double n = rint(x), y = fmax(x - n, -0.5);
+  double p = fma_const(0x1.b63880a30e9ffp-24, y, 0x1.63d136366db24p-20);
+  p = fma_const(p, y, 0x1.ffcb9515a8016p-17);
+  p = fma_const(p, y, 0x1.4308ac85aa947p-13);
+  p = fma_const(p, y, 0x1.5d87fe86fe88ep-10);
+  p = fma_const(p, y, 0x1.3b2ab7181b755p-7);
+  p = fma_const(p, y, 0x1.c6b08d7047e52p-5);
+  p = fma_const(p, y, 0x1.ebfbdff823cedp-3);
+  p = fma_const(p, y, 0x1.62e42fefa39efp-1);
   p = __builtin_fma(p, y, 1.);
   return __builtin_amdgcn_ldexp(p, (int)n);
 }
-// The low bits of 2^10 + w are w in units of 2^-42, rounded.
-__device__ __forceinline__ uint64_t units(double w) {
-  return __builtin_bit_cast(uint64_t, w + 0x1p10) - __builtin_bit_cast(uint64_t, 0x1p10);
-}
-
 // What a lane has of a wave's tile: 16 logits in runs of 16 bytes; -inf past the vocabulary's end.
 template <typename T>
 struct Tile {
   static constexpr int kRun = __is_same(T, float) ? 4 : 8;
-  float l[kPer];
+  static constexpr uint32_t kNone = __is_same(T, float) ? 0xFF800000u : __is_same(T, __bf16) ? 0xFF80u : 0xFC00u;
+  uint32_t raw[kPer / kRun][4];
 
   __device__ __forceinline__ static int index(int i) {
     return (i / kRun) * 64 * kRun + ((int)threadIdx.x & 63) * kRun + i % kRun;
@@ -133,38 +152,96 @@ struct Tile {
   __device__ __forceinline__ void load(const char* row, int first, int vocab) {
     constexpr int kBytes = 16 / kRun;
     if (first + kTile <= vocab) {
-      uint32_t raw[kPer / kRun][4];
 #pragma unroll
       for (int j = 0; j < kPer / kRun; ++j) __builtin_memcpy(raw[j], row + (int64_t)(first + index(j * kRun)) * kBytes, 16);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if constexpr (kRun == 4) l[i] = __uint_as_float(raw[i / 4][i % 4]);
-        else l[i] = to_f32<T>((uint16_t)(raw[i / 8][i % 8 / 2] >> 16 * (i & 1)));
-      }
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int at = first + index(i);
-        l[i] = -INFINITY;
+        uint32_t u = kNone;
         if (at < vocab) {
-          if constexpr (kRun == 4) l[i] = ((const float*)row)[at];
-          else l[i] = to_f32<T>(((const uint16_t*)row)[at]);
+          if constexpr (kRun == 4) u = ((const uint32_t*)row)[at];
+          else u = ((const uint16_t*)row)[at];
         }
+        if constexpr (kRun == 4) raw[i / 4][i % 4] = u;
+        else raw[i / 8][i % 8 / 2] = i & 1 ? raw[i / 8][i % 8 / 2] | u << 16 : u;
+      }
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (kRun == 4) return __uint_as_float(raw[i / 4][i % 4]);
+    else return to_f32<T>((uint16_t)(raw[i / 8][i % 8 / 2] >> 16 * (i & 1)));
+  }
+};
+
+// A wave's tiles, part, part + parts, ... of kSWaves each: loaded once and held in registers (kHold, which then has to be all),
+// or loaded whenever they are looked at.
+template <typename T, int kHold>
+struct Tiles {
+  Tile<T> held[kHold ? kHold : 1];
+  const char* row;
+  int vocab, first, step, n;
+
+  __device__ __forceinline__ Tiles(const Row& f, const SampleArgs& a, int part) {
+    row = f.at;
+    vocab = a.vocab;
+    n = (a.vocab + kTile - 1) / kTile;
+    first = part * kSWaves + (int)(threadIdx.x >> 6);
+    step = a.parts * kSWaves;
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+      if (first + j * step < n) held[j].load(row, (first + j * step) * kTile, vocab);
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F fn) const {
+    if constexpr (kHold > 0) {
+#pragma unroll
+      for (int j = 0; j < kHold; ++j)
+        if (first + j * step < n) fn(first + j * step, held[j]);
+    } else {
+      for (int t = first; t < n; t += step) {
+        Tile<T> x;
+        x.load(row, t * kTile, vocab);
+        fn(t, x);
       }
     }
   }
 };
 
-__device__ __forceinline__ uint64_t wave_sum(uint64_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+// Sums over a wave's lanes up to each (row shifts, then rows' and halves' last lanes to what is behind them).
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRows, 0xF, false);
+}
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint64_t moved(uint64_t v) {
+  return (uint64_t)moved<kCtrl, kRows>((uint32_t)(v >> 32)) << 32 | moved<kCtrl, kRows>((uint32_t)v);
+}
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float moved(float v) {
+  return __uint_as_float(moved<kCtrl, kRows>(__float_as_uint(v)));
+}
+template <typename V>
+__device__ __forceinline__ V wave_scan(V v) {
+  v += moved<0x111, 0xF>(v);
+  v += moved<0x112, 0xF>(v);
+  v += moved<0x114, 0xF>(v);
+  v += moved<0x118, 0xF>(v);
+  v += moved<0x142, 0xA>(v);
+  v += moved<0x143, 0xC>(v);
   return v;
 }
+__device__ __forceinline__ uint64_t of_lane(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+}
+__device__ __forceinline__ uint64_t wave_sum(uint64_t v) { return of_lane(wave_scan(v), 63); }
 
 // The LDS of a workgroup.
 struct Shared {
   union {
-    uint64_t bins[kBins];
+    uint64_t bins[kBins];                    // weights
+    uint32_t counts_of[kBins];
     uint64_t list[kList];
   };
   uint64_t tiles[kMostTiles];
@@ -178,22 +255,18 @@ struct Shared {
 };
 
 // Exclusive sums over the workgroup's threads, and the whole.
-__device__ __forceinline__ uint64_t scan(uint64_t v, Shared& s, uint64_t* all) {
-  const int lane = (int)threadIdx.x & 63;
-  uint64_t x = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t y = __shfl_up(x, d, 64);
-    if (lane >= d) x += y;
-  }
+template <typename V>
+__device__ __forceinline__ V scan(V v, Shared& s, V* all) {
+  V* waves = (V*)s.waves;
+  const V x = wave_scan(v);
   __syncthreads();
-  if (lane == 63) s.waves[threadIdx.x >> 6] = x;
+  if ((threadIdx.x & 63) == 63) waves[threadIdx.x >> 6] = x;
   __syncthreads();
-  uint64_t before = 0, sum = 0;
+  V before = 0, sum = 0;
 #pragma unroll
   for (int w = 0; w < kSWaves; ++w) {
-    if (w < (int)(threadIdx.x >> 6)) before += s.waves[w];
-    sum += s.waves[w];
+    if (w < (int)(threadIdx.x >> 6)) before += waves[w];
+    sum += waves[w];
   }
   *all = sum;
   return before + x - v;
@@ -224,20 +297,18 @@ __device__ bool is_last(uint32_t* done, int parts, Shared& s) {
 // ------------------------------------------------------------------ first: the largest
 
 // The largest logit of a workgroup's tiles, NaN where one is NaN or +inf.
-template <typename T>
-__device__ float largest(const Row& f, const SampleArgs& a, int part, Shared& s) {
-  const int wave = (int)threadIdx.x >> 6, tiles = (a.vocab + kTile - 1) / kTile;
+template <typename X>
+__device__ float largest(const X& tiles, Shared& s) {
+  const int wave = (int)threadIdx.x >> 6;
   float most = -INFINITY;
   bool bad = false;
-  for (int t = part * kSWaves + wave; t < tiles; t += a.parts * kSWaves) {
-    Tile<T> x;
-    x.load(f.at, t * kTile, a.vocab);
+  tiles.each([&](int, const auto& x) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      bad = bad || !(x.l[i] < INFINITY);
-      most = fmaxf(most, x.l[i]);
+      bad = bad || !(x[i] < INFINITY);
+      most = fmaxf(most, x[i]);
     }
-  }
+  });
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
   if (__any(bad)) most = __builtin_nanf("");
@@ -251,48 +322,68 @@ __device__ float largest(const Row& f, const SampleArgs& a, int part, Shared& s)
 
 // ------------------------------------------------------------------ second: where a filter ends
 
-// Tokens (top_k) or weights (top_p) by bins.
-template <typename T>
-__device__ void fill_bins(const Row& f, const SampleArgs& a, int part, Shared& s) {
-  const int tid = (int)threadIdx.x, wave = tid >> 6, tiles = (a.vocab + kTile - 1) / kTile;
+// A top_k that is found from the largest of each group of 16 neighbours: at least k tokens are not below the k-th largest of
+// those, and about as many as long as most groups have none (k up to half the groups).  That takes a sixteenth of the counting.
+__device__ __forceinline__ bool by_groups(const Row& f, const SampleArgs& a) {
+  return f.top_k <= min(kMostGroups, a.vocab / (2 * kGroup));
+}
+
+// Tokens or groups (top_k), or weights (top_p), by bins.  Whole numbers: the LDS adds fp32 numbers to a common place far slower
+// (64 x 131072: 48 instead of 15 us).
+template <typename X>
+__device__ void fill_bins(const X& tiles, const Row& f, const SampleArgs& a, Shared& s) {
+  const int tid = (int)threadIdx.x;
   for (int b = tid; b < kBins; b += kSThreads) s.bins[b] = 0;
   __syncthreads();
   const float most = (float)f.most;
-  for (int t = part * kSWaves + wave; t < tiles; t += a.parts * kSWaves) {
-    Tile<T> x;
-    x.load(f.at, t * kTile, a.vocab);
-    if (f.top_k) {
+  if (f.top_k && by_groups(f, a)) {
+    tiles.each([&](int, const auto& x) {
+      float l = x[0];
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) l = fmaxf(l, x[i]);
+      if (l > -INFINITY) atomicAdd(&s.counts_of[bin_of(most, l)], 1u);
+    });
+  } else if (f.top_k) {
+    tiles.each([&](int, const auto& x) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (x.l[i] > -INFINITY) atomicAdd((uint32_t*)&s.bins[bin_of(most, x.l[i])], 1u);
-    } else {
+        if (x[i] > -INFINITY) atomicAdd(&s.counts_of[bin_of(most, x[i])], 1u);
+    });
+  } else {
+    tiles.each([&](int, const auto& x) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const double w = weight(f, x.l[i]);
-        if (x.l[i] > -INFINITY && w >= f.least)
-          atomicAdd((unsigned long long*)&s.bins[bin_of(most, x.l[i])], (unsigned long long)units(w));
+        const double w = weight(f, x[i]);
+        const uint64_t u = f.units(w);
+        if (u && w >= f.least) atomicAdd((unsigned long long*)&s.bins[bin_of(most, x[i])], (unsigned long long)u);
       }
-    }
+    });
   }
   __syncthreads();
 }
 
-// The bins in which the filters' ends are, from all the row's tokens in s.bins.
-__device__ Range find_bins(const Row& f, Shared& s) {
+// What a top_p of a whole weight reaches.
+__device__ __forceinline__ uint64_t part_of(const Row& f, uint64_t total) {
+  return max((uint64_t)ceil(fmax((double)f.top_p, 0.) * (double)total), (uint64_t)1);
+}
+
+// The bins in which the filters' ends are, from all the row's tokens.
+template <typename V>
+__device__ Range find_bins(const V* bins, const Row& f, const SampleArgs& a, Shared& s) {
   constexpr int kMine = kBins / kSThreads;
   const int tid = (int)threadIdx.x;
-  uint64_t mine[kMine], sum = 0, total;
+  V mine[kMine], sum = 0, total;
 #pragma unroll
-  for (int j = 0; j < kMine; ++j) sum += mine[j] = s.bins[tid * kMine + j];
-  uint64_t before = scan(sum, s, &total);
-  const uint64_t want = f.top_k ? (uint64_t)f.top_k : max((uint64_t)ceil(fmax((double)f.top_p, 0.) * (double)total), (uint64_t)1);
-  if (tid == 0 && total < want) s.range = Range{0, kBins - 1, want};            // all of fewer
+  for (int j = 0; j < kMine; ++j) sum += mine[j] = bins[tid * kMine + j];
+  V before = scan(sum, s, &total);
+  const V want = f.top_k ? (V)f.top_k : (V)part_of(f, total);
+  if (tid == 0 && total < want) s.range = Range{0, kBins - 1, want};              // all of fewer
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
     if (before < want && before + mine[j] >= want) {
       const uint32_t b = (uint32_t)(tid * kMine + j);
-      // the tokens of top_k: all in order, where there are few, or a top_p applies to them
-      const bool whole = f.top_k && (before + mine[j] <= kList || f.top_p < 1.f);
+      // the tokens of a top_k: all in order, where there are few, or a top_p applies to them
+      const bool whole = f.top_k && (by_groups(f, a) || before + mine[j] <= kList || f.top_p < 1.f);
       s.range = whole ? Range{0, b, want} : Range{b, b, want - before};
     }
     before += mine[j];
@@ -300,40 +391,43 @@ __device__ Range find_bins(const Row& f, Shared& s) {
   __syncthreads();
   return s.range;
 }
+__device__ __forceinline__ Range find_bins(const Row& f, const SampleArgs& a, Shared& s) {
+  return f.top_k ? find_bins(s.counts_of, f, a, s) : find_bins(s.bins, f, a, s);
+}
 
 // ------------------------------------------------------------------ third: order, sums, draw
 
 // Each tile's sum of the weights that stay for certain, and a list of the tokens to be put in order.
-template <typename T, bool kOne>
-__device__ void sum_tiles(const Row& f, const SampleArgs& a, int part, const Range& r, uint64_t* sums, Shared& s) {
-  const int tid = (int)threadIdx.x, wave = tid >> 6, tiles = (a.vocab + kTile - 1) / kTile;
+template <bool kOne, typename X>
+__device__ void sum_tiles(const X& tiles, const Row& f, const Range& r, uint64_t* sums, Shared& s) {
+  const int tid = (int)threadIdx.x;
   if (tid == 0) s.n_list = 0, s.first = ~0u;
   __syncthreads();
   const float most = (float)f.most;
-  for (int t = part * kSWaves + wave; t < tiles; t += a.parts * kSWaves) {
-    Tile<T> x;
-    x.load(f.at, t * kTile, a.vocab);
+  // the last bin takes whatever is further off
+  const float from = begin_of(r.lo), to = r.hi + 1 >= kBins ? __builtin_inff() : begin_of(r.hi + 1);
+  tiles.each([&](int t, const auto& x) {
     if (f.temperature == 0.f) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (x.l[i] == most) atomicMin(&s.first, (uint32_t)(t * kTile + Tile<T>::index(i)));
-      continue;
+        if (x[i] == most) atomicMin(&s.first, (uint32_t)(t * kTile + x.index(i)));
+      return;
     }
     uint64_t sum = 0;
-    if (r.lo > 0) {
+    if (r.lo == kBins && f.least == 0.) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sum += f.units(weight(f, x[i]));
+    } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const double w = weight(f, x.l[i]);
-        sum += x.l[i] > -INFINITY && bin_of(most, x.l[i]) < r.lo && w >= f.least ? units(w) : 0ull;
-      }
-    }
-    if (r.lo < kBins) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const uint32_t b = bin_of(most, x.l[i]);
-        if (x.l[i] > -INFINITY && b >= r.lo && b <= r.hi) {
+        const float d = most - x[i];
+        if (__any(d < from)) {
+          const double w = weight(f, x[i]);
+          sum += d < from && w >= f.least ? f.units(w) : 0ull;
+        }
+        if (d >= from && d < to && x[i] > -INFINITY) {
           const uint32_t n = atomicAdd(&s.n_list, 1u);
-          if (n < kList) s.list[n] = order_of(x.l[i], (uint32_t)(t * kTile + Tile<T>::index(i)));
+          if (n < kList) s.list[n] = order_of(x[i], (uint32_t)(t * kTile + x.index(i)));
         }
       }
     }
@@ -342,7 +436,7 @@ __device__ void sum_tiles(const Row& f, const SampleArgs& a, int part, const Ran
       if constexpr (kOne) sums[t] = sum;
       else tell(&sums[t], sum);
     }
-  }
+  });
   __syncthreads();
 }
 
@@ -407,7 +501,7 @@ __device__ uint64_t descend(const Source<T>& from, const Row& f, bool weights, u
       atomicAdd(&s.counts[digit], 1u);
       if (weights) {
         const double w = weight(f, logit_of(o));
-        if (w >= f.least) atomicAdd((unsigned long long*)&s.sums[digit], (unsigned long long)units(w));
+        if (w >= f.least) atomicAdd((unsigned long long*)&s.sums[digit], (unsigned long long)f.units(w));
       }
     }
     __syncthreads();
@@ -437,6 +531,30 @@ __device__ uint64_t descend(const Source<T>& from, const Row& f, bool weights, u
   return prefix;
 }
 
+// Up to kSThreads tokens of the list, one a thread, in order (bitonic sort; ~0 behind them).
+__device__ uint64_t sorted(uint32_t n, Shared& s) {
+  const uint32_t tid = threadIdx.x;
+  uint64_t o = tid < n ? s.list[tid] : ~0ull;
+  __syncthreads();
+  for (uint32_t k = 2; k < 2 * n; k <<= 1) {
+    for (uint32_t j = k >> 1; j > 0; j >>= 1) {
+      uint64_t other;
+      if (j >= 64) {
+        s.list[tid] = o;
+        __syncthreads();
+        other = s.list[tid ^ j];
+        __syncthreads();
+      } else {
+        if ((tid & ~63u) >= 2 * n) continue;
+        other = (uint64_t)__shfl_xor(o, (int)j, 64);
+      }
+      const bool low = ((tid & j) == 0) == ((tid & k) == 0);
+      o = (other < o) == low ? other : o;
+    }
+  }
+  return o;
+}
+
 __device__ void refuse(const SampleArgs& a, int64_t r) {
   a.tokens[r] = -1;
   if (a.logprobs) a.logprobs[r] = __builtin_nanf("");
@@ -457,36 +575,50 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
   const bool few = s.n_list <= kList;
   const bool ordered = f.top_k || f.top_p < 1.f;
   uint64_t end = ~0ull - 1;                  // the last that stays; ~0 is no token
-  if (ordered) {
+  uint64_t mine, before, all, want = range.target;
+  if (ordered && s.n_list <= kSThreads) {
+    const uint32_t n = s.n_list, held = f.top_k && range.target < n ? (uint32_t)range.target : n;
+    const uint64_t o = sorted(n, s);
+    uint64_t u = 0, sum;
+    if ((uint32_t)tid < held) {
+      const double w = weight(f, logit_of(o));
+      if (w >= f.least) u = f.units(w);
+    }
+    before = scan(u, s, &sum);
+    if (f.top_k) want = f.top_p < 1.f ? part_of(f, sum) : ~0ull;
+    if ((uint32_t)tid < held && before < want) {
+      if (u) atomicAdd((unsigned long long*)&s.tiles[index_of(o) / kTile], (unsigned long long)u);
+      if ((uint32_t)tid + 1 == held || before + u >= want) s.found[3] = o;
+    }
+    __syncthreads();
+    end = s.found[3];
+  } else if (ordered) {
     // more than the list holds: the whole row, bit by bit
-    const Source<T> from{few ? nullptr : f.at, few ? s.n_list : (uint32_t)a.vocab, s.list};
-    const auto sum_of = [&]() {
-      uint64_t sum = 0, all;
+    const auto sum_of = [&](const Source<T>& from) {
+      uint64_t sum = 0;
       for (uint32_t i = tid; i < from.n; i += kSThreads) {
         const uint64_t o = from[i];
         if (o > end) continue;
         const double w = weight(f, logit_of(o));
-        if (w >= f.least) sum += units(w);
+        if (w >= f.least) sum += f.units(w);
       }
       scan(sum, s, &all);
       return all;
     };
+    const Source<T> from{few ? nullptr : f.at, few ? s.n_list : (uint32_t)a.vocab, s.list};
     if (f.top_k) {
-      uint64_t target = few ? range.target : (uint64_t)f.top_k, there = 0, all;
+      const uint64_t target = few ? range.target : (uint64_t)f.top_k;
+      uint64_t there = 0;
       for (uint32_t i = tid; i < from.n; i += kSThreads) there += from[i] != ~0ull;
       scan(there, s, &all);
       if (all >= target) end = descend(from, f, false, target, end, s);
     }
-    if (f.top_p < 1.f) {
-      uint64_t target = range.target;
-      if (f.top_k || !few) target = max((uint64_t)ceil(fmax((double)f.top_p, 0.) * (double)sum_of()), (uint64_t)1);
-      end = descend(from, f, true, target, end, s);
-    }
+    if (f.top_p < 1.f) end = descend(from, f, true, f.top_k || !few ? part_of(f, sum_of(from)) : want, end, s);
     if (few) {
       for (uint32_t i = tid; i < s.n_list; i += kSThreads) {
         const uint64_t o = s.list[i];
         const double w = weight(f, logit_of(o));
-        if (o <= end && w >= f.least) atomicAdd((unsigned long long*)&s.tiles[index_of(o) / kTile], (unsigned long long)units(w));
+        if (o <= end && w >= f.least) atomicAdd((unsigned long long*)&s.tiles[index_of(o) / kTile], (unsigned long long)f.units(w));
       }
     } else {
       for (int t = wave; t < tiles; t += kSWaves) {
@@ -495,8 +627,8 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
         uint64_t sum = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const double w = weight(f, x.l[i]);
-          if (x.l[i] > -INFINITY && order_of(x.l[i], (uint32_t)(t * kTile + Tile<T>::index(i))) <= end && w >= f.least) sum += units(w);
+          const double w = weight(f, x[i]);
+          if (x[i] > -INFINITY && order_of(x[i], (uint32_t)(t * kTile + x.index(i))) <= end && w >= f.least) sum += f.units(w);
         }
         sum = wave_sum(sum);
         if ((tid & 63) == 0) s.tiles[t] = sum;
@@ -505,8 +637,9 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
     __syncthreads();
   }
   // the first token whose running sum passes u * total
-  uint64_t mine = tid < tiles ? s.tiles[tid] : 0, total, all;
-  uint64_t before = scan(mine, s, &total);
+  uint64_t total;
+  mine = tid < tiles ? s.tiles[tid] : 0;
+  before = scan(mine, s, &total);
   const uint64_t at = min((uint64_t)(fmin(fmax((double)f.u, 0.), 1.) * (double)total), total - 1);
   if (before <= at && before + mine > at) {
     s.found[0] = (uint64_t)tid;
@@ -518,25 +651,26 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
   mine = 0;
   if (o <= end) {
     const double w = weight(f, logit_of(o));
-    if (w >= f.least) mine = units(w);
+    if (w >= f.least) mine = f.units(w);
   }
   before = scan(mine, s, &all);
   if (before <= left && before + mine > left) {
     a.tokens[r] = i;
     if (a.logprobs)
-      a.logprobs[r] = (float)(((double)logit_of(o) - f.most) / (double)f.temperature - log((double)total * (1. / kUnit)));
+      a.logprobs[r] = (float)(((double)logit_of(o) - f.most) / (double)f.temperature - log((double)total * (f.units.magic * 0x1p-52)));
   }
 }
 
 // ------------------------------------------------------------------ kernels
 
 // A workgroup has a row.
-template <typename T>
+template <typename T, int kHold>
 __global__ __launch_bounds__(kSThreads) void sample_row_kernel(SampleArgs a) {
   __shared__ Shared s;
   const int64_t r = blockIdx.x;
   Row f = row_of(a, r, __is_same(T, float) ? 4 : 2);
-  const float most = largest<T>(f, a, 0, s);
+  const Tiles<T, kHold> tiles(f, a, 0);
+  const float most = largest(tiles, s);
   if (f.bad || !(most > -INFINITY)) {
     if (threadIdx.x == 0) refuse(a, r);
     return;
@@ -544,10 +678,10 @@ __global__ __launch_bounds__(kSThreads) void sample_row_kernel(SampleArgs a) {
   f.most = (double)most;
   Range range{kBins, 0, 0};
   if (f.temperature > 0.f && (f.top_k || f.top_p < 1.f)) {
-    fill_bins<T>(f, a, 0, s);
-    range = find_bins(f, s);
+    fill_bins(tiles, f, a, s);
+    range = find_bins(f, a, s);
   }
-  sum_tiles<T, true>(f, a, 0, range, s.tiles, s);
+  sum_tiles<true>(tiles, f, range, s.tiles, s);
   draw<T>(f, a, r, range, s);
 }
 
@@ -574,7 +708,7 @@ __global__ __launch_bounds__(kSThreads) void sample_max_kernel(SampleArgs a) {
   if (part == 0 && tid == 0) w->done[0] = w->done[1] = w->n_list = 0, w->first = ~0u;
   for (int b = part * kSThreads + tid; b < kBins; b += a.parts * kSThreads) w->bins[b] = 0;
   const Row f = row_of(a, r, __is_same(T, float) ? 4 : 2);
-  const float most = largest<T>(f, a, part, s);
+  const float most = largest(Tiles<T, 0>(f, a, part), s);
   if (tid == 0) w->part_max[part] = most;
 }
 
@@ -588,13 +722,19 @@ __global__ __launch_bounds__(kSThreads) void sample_bins_kernel(SampleArgs a) {
   const float most = joined(w, a.parts);
   if (f.bad || !(most > -INFINITY) || f.temperature == 0.f || (!f.top_k && !(f.top_p < 1.f))) return;
   f.most = (double)most;
-  fill_bins<T>(f, a, part, s);
-  for (int b = tid; b < kBins; b += kSThreads)
-    if (s.bins[b]) atomicAdd((unsigned long long*)&w->bins[b], (unsigned long long)s.bins[b]);
+  fill_bins(Tiles<T, 0>(f, a, part), f, a, s);
+  for (int b = tid; b < kBins; b += kSThreads) {
+    if (f.top_k && s.counts_of[b])
+      __hip_atomic_fetch_add((uint32_t*)&w->bins[b], s.counts_of[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (!f.top_k && s.bins[b]) __hip_atomic_fetch_add(&w->bins[b], s.bins[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
   if (!is_last(&w->done[0], a.parts, s)) return;
-  for (int b = tid; b < kBins; b += kSThreads) s.bins[b] = read_back(&w->bins[b]);
+  for (int b = tid; b < kBins; b += kSThreads) {
+    if (f.top_k) s.counts_of[b] = read_back((uint32_t*)&w->bins[b]);
+    else s.bins[b] = read_back(&w->bins[b]);
+  }
   __syncthreads();
-  const Range range = find_bins(f, s);
+  const Range range = find_bins(f, a, s);
   if (tid == 0) w->range = range;
 }
 
@@ -613,7 +753,7 @@ __global__ __launch_bounds__(kSThreads) void sample_draw_kernel(SampleArgs a) {
   f.most = (double)most;
   Range range{kBins, 0, 0};
   if (f.temperature > 0.f && (f.top_k || f.top_p < 1.f)) range = w->range;
-  sum_tiles<T, false>(f, a, part, range, w->tiles, s);
+  sum_tiles<false>(Tiles<T, 0>(f, a, part), f, range, w->tiles, s);
   const uint32_t n = s.n_list;
   if (tid == 0) {
     s.found[0] = n ? atomicAdd(&w->n_list, n) : 0u;
@@ -635,18 +775,21 @@ __global__ __launch_bounds__(kSThreads) void sample_draw_kernel(SampleArgs a) {
   draw<T>(f, a, r, range, s);
 }
 
-// Workgroups of a row: one where there are rows enough to fill the card, or a row is short.
-constexpr int kFull = 512;
+// Workgroups of a row: one where its tiles stay in their registers, or where there are rows enough to fill the card.
+constexpr int kFull = 256;
 int parts_of(int32_t n_rows, int32_t vocab) {
   const int tiles = (vocab + kTile - 1) / kTile;
+  if (tiles <= kHeld * kSWaves) return 1;
   return std::max(1, std::min({(int)kMostParts, kFull / std::max(n_rows, 1), tiles / kSWaves}));
 }
 
 template <typename T>
 void launch_sample(const SampleArgs& a, int32_t n_rows, hipStream_t s) {
   const dim3 grid((unsigned)(n_rows * a.parts)), block(kSThreads);
-  if (a.parts == 1) {
-    hipLaunchKernelGGL((sample_row_kernel<T>), grid, block, 0, s, a);
+  if (a.vocab <= kHeld * kSWaves * kTile) {
+    hipLaunchKernelGGL((sample_row_kernel<T, kHeld>), grid, block, 0, s, a);
+  } else if (a.parts == 1) {
+    hipLaunchKernelGGL((sample_row_kernel<T, 0>), grid, block, 0, s, a);
   } else {
     hipLaunchKernelGGL((sample_max_kernel<T>), grid, block, 0, s, a);
     hipLaunchKernelGGL((sample_bins_kernel<T>), grid, block, 0, s, a);
