@@ -37,10 +37,9 @@ struct SampleArgs {
   int32_t vocab, parts;
 };
 
-// Where the last token that stays is: tokens in bins below lo stay (as far as min_p lets them), tokens in lo .. hi are put in
-// order to see.
+// Where the last token that stays is: logits from `from` on stay, those below it from `to` on are put in order to see.
 struct Range {
-  uint32_t lo, hi;
+  float from, to;
   uint64_t target;                           // how many of those in order, or how much weight
 };
 
@@ -90,9 +89,10 @@ __device__ __forceinline__ float begin_of(uint32_t bin) {
 // A row's parameters.
 struct Row {
   const char* at;
-  double most, slope, least;                 // the largest logit; log2(e) / temperature; min_p
+  double most, slope;                        // the largest logit; log2(e) / temperature
   Unit units;
-  float u, top_p, temperature;
+  float u, top_p, min_p, temperature;
+  float low;                                 // the least logit that stays by min_p; above -inf
   int32_t top_k;                             // 0: all
   bool bad;
 };
@@ -103,11 +103,11 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t r, int bytes)
   f.u = a.uniforms[r];
   f.temperature = a.temperature ? a.temperature[r] : 1.f;
   f.top_p = a.top_p ? a.top_p[r] : 1.f;
-  const float min_p = a.min_p ? a.min_p[r] : 0.f;
+  f.min_p = a.min_p ? a.min_p[r] : 0.f;
   f.top_k = a.top_k ? a.top_k[r] : 0;
   if (f.top_k < 0 || f.top_k >= a.vocab) f.top_k = 0;
-  f.bad = f.u != f.u || !(f.temperature >= 0.f) || f.top_p != f.top_p || min_p != min_p;
-  f.least = min_p > 0.f ? fmin((double)min_p, 1.) : 0.;
+  f.bad = f.u != f.u || !(f.temperature >= 0.f) || f.top_p != f.top_p || f.min_p != f.min_p;
+  f.low = -3.402823466e38f;
   f.slope = f.temperature > 0.f ? fmax(1.4426950408889634 / (double)f.temperature, 1e-300) : 0.;      // not 0 * -inf
   f.most = 0;
   const int bits = max(32 - __builtin_clz(max((unsigned)a.vocab, 2u) - 1u), 11);
@@ -123,11 +123,11 @@ __device__ __forceinline__ double fma_const(double a, double b, double c) {
 }
 
 // exp((l - most) / temperature) = 2^x, to 4e-14 of itself: x's whole part goes to the exponent, 2^f for the rest, |f| <= 1/2,
-// is a polynomial of degree 9 that interpolates it at Chebyshev's points (3.7e-14 off at most) and is 1 at 0.  A logit of
-// -inf gives 0: its f is no number, which the maximum takes for -1/2, and its exponent is below all.
+// is a polynomial of degree 9 that interpolates it at Chebyshev's points (3.7e-14 off at most) and is 1 at 0.  Below 2^-1000, and
+// for -inf, it stays there, which is no unit.
 __device__ __forceinline__ double weight(const Row& f, float l) {
-  const double x = ((double)l - f.most) * f.slope;
-  const double n = rint(x), y = fmax(x - n, -0.5);
+  const double x = fmax(((double)l - f.most) * f.slope, -1000.);
+  const double n = x + 0x1.8p52, y = x - (n - 0x1.8p52);             // n's low bits are x's nearest whole number
   double p = fma_const(0x1.b63880a30e9ffp-24, y, 0x1.63d136366db24p-20);
   p = fma_const(p, y, 0x1.ffcb9515a8016p-17);
   p = fma_const(p, y, 0x1.4308ac85aa947p-13);
@@ -137,8 +137,25 @@ __device__ __forceinline__ double weight(const Row& f, float l) {
   p = fma_const(p, y, 0x1.ebfbdff823cedp-3);
   p = fma_const(p, y, 0x1.62e42fefa39efp-1);
   p = __builtin_fma(p, y, 1.);
-  return __builtin_amdgcn_ldexp(p, (int)n);
+  const uint64_t u = __builtin_bit_cast(uint64_t, p);
+  return __builtin_bit_cast(double, (uint64_t)((uint32_t)(u >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, n) << 20)) << 32 | (uint32_t)u);
 }
+
+// The least key from lo to hi at which something holds that holds from there on, hi among it: 64 places at a time.
+template <typename F>
+__device__ __forceinline__ uint32_t first_key(uint32_t lo, uint32_t hi, F holds) {
+  const uint32_t lane = threadIdx.x & 63u;
+  while (lo < hi) {
+    const uint32_t step = (hi - lo + 62u) / 63u;
+    const uint32_t k = (uint32_t)min((uint64_t)lo + (uint64_t)lane * step, (uint64_t)hi);
+    const uint32_t j = (uint32_t)__builtin_ctzll(__ballot(holds(k)));
+    if (j == 0) return lo;
+    hi = (uint32_t)min((uint64_t)lo + (uint64_t)j * step, (uint64_t)hi);
+    lo += (j - 1u) * step + 1u;
+  }
+  return lo;
+}
+
 // What a lane has of a wave's tile: 16 logits in runs of 16 bytes; -inf past the vocabulary's end.
 template <typename T>
 struct Tile {
@@ -231,11 +248,37 @@ __device__ __forceinline__ V wave_scan(V v) {
   v += moved<0x143, 0xC>(v);
   return v;
 }
+__device__ __forceinline__ uint32_t of_lane(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
 __device__ __forceinline__ uint64_t of_lane(uint64_t v, int lane) {
-  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
-         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  return (uint64_t)of_lane((uint32_t)(v >> 32), lane) << 32 | of_lane((uint32_t)v, lane);
 }
 __device__ __forceinline__ uint64_t wave_sum(uint64_t v) { return of_lane(wave_scan(v), 63); }
+
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float larger(float v) {
+  return fmaxf(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(v), (int)__float_as_uint(v), kCtrl, kRows, 0xF, false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = larger<0x111, 0xF>(v);
+  v = larger<0x112, 0xF>(v);
+  v = larger<0x114, 0xF>(v);
+  v = larger<0x118, 0xF>(v);
+  v = larger<0x142, 0xA>(v);
+  v = larger<0x143, 0xC>(v);
+  return __uint_as_float(of_lane(__float_as_uint(v), 63));
+}
+
+// Up to 64 different numbers of a wave's lanes, n of them, in order.
+__device__ __forceinline__ uint64_t wave_sorted(uint64_t o, uint32_t n, uint64_t* space) {
+  const uint32_t lane = threadIdx.x & 63u;
+  uint32_t rank = 0;
+  for (uint32_t j = 0; j < n; ++j) rank += of_lane(o, (int)j) < o;
+  if (lane < n) space[rank] = o;
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  return lane < n ? space[lane] : ~0ull;
+}
 
 // The LDS of a workgroup.
 struct Shared {
@@ -248,9 +291,10 @@ struct Shared {
   uint64_t sums[kDigits];
   uint32_t counts[kDigits];
   uint64_t waves[kSWaves];
-  uint64_t found[4];
+  uint64_t found[4], few[64];
   float wave_max[kSWaves];
-  uint32_t n_list, first, last;
+  uint32_t n_list, n_few, first, last;
+  float low;
   Range range;
 };
 
@@ -259,17 +303,17 @@ template <typename V>
 __device__ __forceinline__ V scan(V v, Shared& s, V* all) {
   V* waves = (V*)s.waves;
   const V x = wave_scan(v);
+  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   __syncthreads();
-  if ((threadIdx.x & 63) == 63) waves[threadIdx.x >> 6] = x;
+  if (lane == 63) waves[wave] = x;
   __syncthreads();
-  V before = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kSWaves; ++w) {
-    if (w < (int)(threadIdx.x >> 6)) before += waves[w];
-    sum += waves[w];
-  }
-  *all = sum;
-  return before + x - v;
+  V w = lane < kSWaves ? waves[lane] : 0;
+  w += moved<0x111, 0xF>(w);                 // within 16 lanes
+  w += moved<0x112, 0xF>(w);
+  w += moved<0x114, 0xF>(w);
+  w += moved<0x118, 0xF>(w);
+  *all = of_lane(w, kSWaves - 1);
+  return (wave ? of_lane(w, wave - 1) : 0) + x - v;
 }
 
 // What the workgroups of a row tell each other within a launch goes past the caches of the chip's parts: a fence would write
@@ -296,6 +340,13 @@ __device__ bool is_last(uint32_t* done, int parts, Shared& s) {
 
 // ------------------------------------------------------------------ first: the largest
 
+// The largest of n <= 64 numbers, NaN where one is.
+__device__ __forceinline__ float join_max(const float* p, int n) {
+  const int lane = (int)threadIdx.x & 63;
+  const float v = lane < n ? p[lane] : -INFINITY;
+  return __any(v != v) ? __builtin_nanf("") : wave_max(v) + 0.f;              // one zero
+}
+
 // The largest logit of a workgroup's tiles, NaN where one is NaN or +inf.
 template <typename X>
 __device__ float largest(const X& tiles, Shared& s) {
@@ -309,15 +360,22 @@ __device__ float largest(const X& tiles, Shared& s) {
       most = fmaxf(most, x[i]);
     }
   });
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
+  most = wave_max(most);
   if (__any(bad)) most = __builtin_nanf("");
   if ((threadIdx.x & 63) == 0) s.wave_max[wave] = most;
   __syncthreads();
-  most = s.wave_max[0];
-#pragma unroll
-  for (int w = 1; w < kSWaves; ++w) most = s.wave_max[w] != s.wave_max[w] ? s.wave_max[w] : most != most ? most : fmaxf(most, s.wave_max[w]);
-  return most + 0.f;                         // one zero
+  return join_max(s.wave_max, kSWaves);
+}
+
+// The least logit that stays by min_p, into f.low.
+__device__ void find_low(Row& f, Shared& s) {
+  if (!(f.min_p > 0.f) || f.temperature == 0.f) return;
+  if (threadIdx.x < 64) {
+    const double least = fmin((double)f.min_p, 1.);
+    s.low = of_key(first_key(key_of(f.low), key_of((float)f.most), [&](uint32_t k) { return weight(f, of_key(k)) >= least; }));
+  }
+  __syncthreads();
+  f.low = s.low;
 }
 
 // ------------------------------------------------------------------ second: where a filter ends
@@ -353,9 +411,8 @@ __device__ void fill_bins(const X& tiles, const Row& f, const SampleArgs& a, Sha
     tiles.each([&](int, const auto& x) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const double w = weight(f, x[i]);
-        const uint64_t u = f.units(w);
-        if (u && w >= f.least) atomicAdd((unsigned long long*)&s.bins[bin_of(most, x[i])], (unsigned long long)u);
+        if (x[i] >= f.low)
+          atomicAdd((unsigned long long*)&s.bins[bin_of(most, x[i])], (unsigned long long)f.units(weight(f, x[i])));
       }
     });
   }
@@ -377,16 +434,28 @@ __device__ Range find_bins(const V* bins, const Row& f, const SampleArgs& a, Sha
   for (int j = 0; j < kMine; ++j) sum += mine[j] = bins[tid * kMine + j];
   V before = scan(sum, s, &total);
   const V want = f.top_k ? (V)f.top_k : (V)part_of(f, total);
-  if (tid == 0 && total < want) s.range = Range{0, kBins - 1, want};              // all of fewer
+  if (tid == 0) s.found[0] = 0, s.found[1] = kBins, s.found[2] = want;             // all of fewer
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
     if (before < want && before + mine[j] >= want) {
       const uint32_t b = (uint32_t)(tid * kMine + j);
       // the tokens of a top_k: all in order, where there are few, or a top_p applies to them
       const bool whole = f.top_k && (by_groups(f, a) || before + mine[j] <= kList || f.top_p < 1.f);
-      s.range = whole ? Range{0, b, want} : Range{b, b, want - before};
+      s.found[0] = whole ? 0 : b;
+      s.found[1] = b + 1;
+      s.found[2] = whole ? want : want - before;
     }
     before += mine[j];
+  }
+  __syncthreads();
+  // the bins' beginnings as logits
+  if (tid < 64) {
+    const float most = (float)f.most, below_from = begin_of((uint32_t)s.found[0]), below_to = begin_of((uint32_t)s.found[1]);
+    const uint32_t lo = key_of(-3.402823466e38f), hi = key_of(most);
+    const float from = below_from > 0.f ? of_key(first_key(lo, hi, [&](uint32_t k) { return most - of_key(k) < below_from; })) : INFINITY;
+    const float to = below_to < INFINITY ? of_key(first_key(lo, hi, [&](uint32_t k) { return most - of_key(k) < below_to; })) : of_key(lo);
+    if (tid == 0) s.range = Range{fmaxf(from, f.low), fmaxf(to, f.low), s.found[2]};
   }
   __syncthreads();
   return s.range;
@@ -403,29 +472,27 @@ __device__ void sum_tiles(const X& tiles, const Row& f, const Range& r, uint64_t
   const int tid = (int)threadIdx.x;
   if (tid == 0) s.n_list = 0, s.first = ~0u;
   __syncthreads();
-  const float most = (float)f.most;
-  // the last bin takes whatever is further off
-  const float from = begin_of(r.lo), to = r.hi + 1 >= kBins ? __builtin_inff() : begin_of(r.hi + 1);
   tiles.each([&](int t, const auto& x) {
     if (f.temperature == 0.f) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (x[i] == most) atomicMin(&s.first, (uint32_t)(t * kTile + x.index(i)));
+        if (x[i] == (float)f.most) atomicMin(&s.first, (uint32_t)(t * kTile + x.index(i)));
       return;
     }
     uint64_t sum = 0;
-    if (r.lo == kBins && f.least == 0.) {
+    if (r.from < -3e38f) {                   // all: -inf weighs nothing
 #pragma unroll
       for (int i = 0; i < kPer; ++i) sum += f.units(weight(f, x[i]));
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const float d = most - x[i];
-        if (__any(d < from)) {
-          const double w = weight(f, x[i]);
-          sum += d < from && w >= f.least ? f.units(w) : 0ull;
+        if (!__any(x[i] >= r.to)) continue;
+        const bool certain = x[i] >= r.from;
+        if (__any(certain)) {
+          const uint64_t u = f.units(weight(f, x[i]));
+          sum += certain ? u : 0ull;
         }
-        if (d >= from && d < to && x[i] > -INFINITY) {
+        if (x[i] >= r.to && !certain) {
           const uint32_t n = atomicAdd(&s.n_list, 1u);
           if (n < kList) s.list[n] = order_of(x[i], (uint32_t)(t * kTile + x.index(i)));
         }
@@ -499,10 +566,8 @@ __device__ uint64_t descend(const Source<T>& from, const Row& f, bool weights, u
       if (o > end || o >> top != prefix) continue;
       const uint32_t digit = (uint32_t)(o >> shift) & ((1u << (top - shift)) - 1u);
       atomicAdd(&s.counts[digit], 1u);
-      if (weights) {
-        const double w = weight(f, logit_of(o));
-        if (w >= f.least) atomicAdd((unsigned long long*)&s.sums[digit], (unsigned long long)f.units(w));
-      }
+      if (weights && logit_of(o) >= f.low)
+        atomicAdd((unsigned long long*)&s.sums[digit], (unsigned long long)f.units(weight(f, logit_of(o))));
     }
     __syncthreads();
     const uint64_t mine = weights ? s.sums[tid] : s.counts[tid];
@@ -517,10 +582,21 @@ __device__ uint64_t descend(const Source<T>& from, const Row& f, bool weights, u
     prefix = prefix << (top - shift) | s.found[0];
     target = s.found[1];
     top = shift;
-    if (s.found[2] == 1 && top > 0) {        // one token: the rest of its bits
+    const uint32_t left = (uint32_t)s.found[2];
+    if (left <= 64 && top > 0) {             // few tokens: a wave puts them in order
+      if (tid == 0) s.n_few = 0;
+      __syncthreads();
       for (uint32_t i = tid; i < from.n; i += kSThreads) {
         const uint64_t o = from[i];
-        if (o <= end && o >> top == prefix) s.found[3] = o;
+        if (o <= end && o >> top == prefix) s.few[atomicAdd(&s.n_few, 1u)] = o;
+      }
+      __syncthreads();
+      if (tid < 64) {
+        const uint64_t o = wave_sorted((uint32_t)tid < left ? s.few[tid] : ~0ull, left, s.few);
+        uint64_t v = (uint32_t)tid < left;
+        if (weights) v = v && logit_of(o) >= f.low ? f.units(weight(f, logit_of(o))) : 0;
+        const uint64_t upto = wave_scan(v);
+        if (upto - v < target && upto >= target) s.found[3] = o;
       }
       __syncthreads();
       prefix = s.found[3];
@@ -529,30 +605,6 @@ __device__ uint64_t descend(const Source<T>& from, const Row& f, bool weights, u
   }
   __syncthreads();
   return prefix;
-}
-
-// Up to kSThreads tokens of the list, one a thread, in order (bitonic sort; ~0 behind them).
-__device__ uint64_t sorted(uint32_t n, Shared& s) {
-  const uint32_t tid = threadIdx.x;
-  uint64_t o = tid < n ? s.list[tid] : ~0ull;
-  __syncthreads();
-  for (uint32_t k = 2; k < 2 * n; k <<= 1) {
-    for (uint32_t j = k >> 1; j > 0; j >>= 1) {
-      uint64_t other;
-      if (j >= 64) {
-        s.list[tid] = o;
-        __syncthreads();
-        other = s.list[tid ^ j];
-        __syncthreads();
-      } else {
-        if ((tid & ~63u) >= 2 * n) continue;
-        other = (uint64_t)__shfl_xor(o, (int)j, 64);
-      }
-      const bool low = ((tid & j) == 0) == ((tid & k) == 0);
-      o = (other < o) == low ? other : o;
-    }
-  }
-  return o;
 }
 
 __device__ void refuse(const SampleArgs& a, int64_t r) {
@@ -575,20 +627,18 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
   const bool few = s.n_list <= kList;
   const bool ordered = f.top_k || f.top_p < 1.f;
   uint64_t end = ~0ull - 1;                  // the last that stays; ~0 is no token
-  uint64_t mine, before, all, want = range.target;
-  if (ordered && s.n_list <= kSThreads) {
-    const uint32_t n = s.n_list, held = f.top_k && range.target < n ? (uint32_t)range.target : n;
-    const uint64_t o = sorted(n, s);
-    uint64_t u = 0, sum;
-    if ((uint32_t)tid < held) {
-      const double w = weight(f, logit_of(o));
-      if (w >= f.least) u = f.units(w);
-    }
-    before = scan(u, s, &sum);
-    if (f.top_k) want = f.top_p < 1.f ? part_of(f, sum) : ~0ull;
-    if ((uint32_t)tid < held && before < want) {
-      if (u) atomicAdd((unsigned long long*)&s.tiles[index_of(o) / kTile], (unsigned long long)u);
-      if ((uint32_t)tid + 1 == held || before + u >= want) s.found[3] = o;
+  uint64_t mine, before, all, want = range.target, total;
+  if (ordered && s.n_list <= 64) {           // a wave puts them in order; none where min_p lets none of a bin stay
+    if (tid == 0) s.found[3] = end;
+    if (tid < 64 && s.n_list > 0) {
+      const uint32_t n = s.n_list, held = f.top_k && range.target < n ? (uint32_t)range.target : n;
+      const uint64_t o = wave_sorted((uint32_t)tid < n ? s.list[tid] : ~0ull, n, s.few);
+      const uint64_t u = (uint32_t)tid < held ? f.units(weight(f, logit_of(o))) : 0, upto = wave_scan(u);
+      if (f.top_k) want = f.top_p < 1.f ? part_of(f, of_lane(upto, 63)) : ~0ull;
+      const bool stays = (uint32_t)tid < held && upto - u < want;
+      if (stays) atomicAdd((unsigned long long*)&s.tiles[index_of(o) / kTile], (unsigned long long)u);
+      const uint64_t last = of_lane(o, 63 - __builtin_clzll(__ballot(stays)));
+      if (tid == 0) s.found[3] = last;
     }
     __syncthreads();
     end = s.found[3];
@@ -598,9 +648,7 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
       uint64_t sum = 0;
       for (uint32_t i = tid; i < from.n; i += kSThreads) {
         const uint64_t o = from[i];
-        if (o > end) continue;
-        const double w = weight(f, logit_of(o));
-        if (w >= f.least) sum += f.units(w);
+        if (o <= end && logit_of(o) >= f.low) sum += f.units(weight(f, logit_of(o)));
       }
       scan(sum, s, &all);
       return all;
@@ -617,8 +665,8 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
     if (few) {
       for (uint32_t i = tid; i < s.n_list; i += kSThreads) {
         const uint64_t o = s.list[i];
-        const double w = weight(f, logit_of(o));
-        if (o <= end && w >= f.least) atomicAdd((unsigned long long*)&s.tiles[index_of(o) / kTile], (unsigned long long)f.units(w));
+        if (o <= end)
+          atomicAdd((unsigned long long*)&s.tiles[index_of(o) / kTile], (unsigned long long)f.units(weight(f, logit_of(o))));
       }
     } else {
       for (int t = wave; t < tiles; t += kSWaves) {
@@ -627,8 +675,7 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
         uint64_t sum = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const double w = weight(f, x[i]);
-          if (x[i] > -INFINITY && order_of(x[i], (uint32_t)(t * kTile + x.index(i))) <= end && w >= f.least) sum += f.units(w);
+          if (x[i] >= f.low && order_of(x[i], (uint32_t)(t * kTile + x.index(i))) <= end) sum += f.units(weight(f, x[i]));
         }
         sum = wave_sum(sum);
         if ((tid & 63) == 0) s.tiles[t] = sum;
@@ -637,7 +684,6 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
     __syncthreads();
   }
   // the first token whose running sum passes u * total
-  uint64_t total;
   mine = tid < tiles ? s.tiles[tid] : 0;
   before = scan(mine, s, &total);
   const uint64_t at = min((uint64_t)(fmin(fmax((double)f.u, 0.), 1.) * (double)total), total - 1);
@@ -648,11 +694,7 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
   __syncthreads();
   const int i = (int)s.found[0] * kTile + tid;
   const uint64_t left = s.found[1], o = i < a.vocab ? Source<T>{f.at, 0, nullptr}[(uint32_t)i] : ~0ull;
-  mine = 0;
-  if (o <= end) {
-    const double w = weight(f, logit_of(o));
-    if (w >= f.least) mine = f.units(w);
-  }
+  mine = o <= end && logit_of(o) >= f.low ? f.units(weight(f, logit_of(o))) : 0;
   before = scan(mine, s, &all);
   if (before <= left && before + mine > left) {
     a.tokens[r] = i;
@@ -676,7 +718,8 @@ __global__ __launch_bounds__(kSThreads) void sample_row_kernel(SampleArgs a) {
     return;
   }
   f.most = (double)most;
-  Range range{kBins, 0, 0};
+  find_low(f, s);
+  Range range{f.low, f.low, 0};
   if (f.temperature > 0.f && (f.top_k || f.top_p < 1.f)) {
     fill_bins(tiles, f, a, s);
     range = find_bins(f, a, s);
@@ -686,16 +729,6 @@ __global__ __launch_bounds__(kSThreads) void sample_row_kernel(SampleArgs a) {
 }
 
 __device__ __forceinline__ RowSpace* space_of(const SampleArgs& a, int64_t r) { return (RowSpace*)(a.workspace + r * a.ws_row); }
-
-// The parts' largest logits; NaN where one is.
-__device__ __forceinline__ float joined(const RowSpace* w, int parts) {
-  const int lane = (int)threadIdx.x & 63;
-  const float v = lane < parts ? w->part_max[lane] : -INFINITY;
-  float most = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
-  return __any(v != v) ? __builtin_nanf("") : most;
-}
 
 // Several workgroups share a row; three launches, and the last workgroup of a row to end the second and the third joins what
 // they found.
@@ -719,9 +752,10 @@ __global__ __launch_bounds__(kSThreads) void sample_bins_kernel(SampleArgs a) {
   const int part = (int)(blockIdx.x - r * a.parts), tid = (int)threadIdx.x;
   RowSpace* w = space_of(a, r);
   Row f = row_of(a, r, __is_same(T, float) ? 4 : 2);
-  const float most = joined(w, a.parts);
+  const float most = join_max(w->part_max, a.parts);
   if (f.bad || !(most > -INFINITY) || f.temperature == 0.f || (!f.top_k && !(f.top_p < 1.f))) return;
   f.most = (double)most;
+  find_low(f, s);
   fill_bins(Tiles<T, 0>(f, a, part), f, a, s);
   for (int b = tid; b < kBins; b += kSThreads) {
     if (f.top_k && s.counts_of[b])
@@ -745,13 +779,14 @@ __global__ __launch_bounds__(kSThreads) void sample_draw_kernel(SampleArgs a) {
   const int part = (int)(blockIdx.x - r * a.parts), tid = (int)threadIdx.x;
   RowSpace* w = space_of(a, r);
   Row f = row_of(a, r, __is_same(T, float) ? 4 : 2);
-  const float most = joined(w, a.parts);
+  const float most = join_max(w->part_max, a.parts);
   if (f.bad || !(most > -INFINITY)) {
     if (part == 0 && tid == 0) refuse(a, r);
     return;
   }
   f.most = (double)most;
-  Range range{kBins, 0, 0};
+  find_low(f, s);
+  Range range{f.low, f.low, 0};
   if (f.temperature > 0.f && (f.top_k || f.top_p < 1.f)) range = w->range;
   sum_tiles<false>(Tiles<T, 0>(f, a, part), f, range, w->tiles, s);
   const uint32_t n = s.n_list;
