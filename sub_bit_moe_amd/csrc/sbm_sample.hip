@@ -19,6 +19,7 @@ constexpr int kBins = 4096;                  // of the distance below the larges
 constexpr int kDigits = 1024;                // ten bits of an order at a time
 constexpr int kList = 6144;                  // tokens of a row that are put in order in LDS
 constexpr int kHeld = 2;                     // tiles of a wave that stay in its registers
+constexpr int kBeside = 4;                   // logits of a lane whose weights are computed beside one another
 constexpr int kGroup = kPer;                 // neighbours of which one counts for a top_k
 constexpr int kMostGroups = 2048;
 constexpr int kMostParts = 64;               // workgroups of a row
@@ -115,28 +116,21 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t r, int bytes)
   return f;
 }
 
-// a * b + c with c the same in all lanes: the compiler would copy c into a register that the sum then overwrites.
-__device__ __forceinline__ double fma_const(double a, double b, double c) {
-  double d;
-  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
-  return d;
-}
-
 // exp((l - most) / temperature) = 2^x, to 4e-14 of itself: x's whole part goes to the exponent, 2^f for the rest, |f| <= 1/2,
 // is a polynomial of degree 9 that interpolates it at Chebyshev's points (3.7e-14 off at most) and is 1 at 0.  Below 2^-1000, and
 // for -inf, it stays there, which is no unit.
 __device__ __forceinline__ double weight(const Row& f, float l) {
   const double x = fmax(((double)l - f.most) * f.slope, -1000.);
   const double n = x + 0x1.8p52, y = x - (n - 0x1.8p52);             // n's low bits are x's nearest whole number
-  double p = fma_const(0x1.b63880a30e9ffp-24, y, 0x1.63d136366db24p-20);
-  p = fma_const(p, y, 0x1.ffcb9515a8016p-17);
-  p = fma_const(p, y, 0x1.4308ac85aa947p-13);
-  p = fma_const(p, y, 0x1.5d87fe86fe88ep-10);
-  p = fma_const(p, y, 0x1.3b2ab7181b755p-7);
-  p = fma_const(p, y, 0x1.c6b08d7047e52p-5);
-  p = fma_const(p, y, 0x1.ebfbdff823cedp-3);
-  p = fma_const(p, y, 0x1.62e42fefa39efp-1);
-  p = __builtin_fma(p, y, 1.);
+  // as one block, since the compiler would copy each coefficient into the register of the sum, an instruction more
+  double p;
+  asm("v_fma_f64 %0, %2, %1, %3\n\tv_fma_f64 %0, %0, %1, %4\n\tv_fma_f64 %0, %0, %1, %5\n\tv_fma_f64 %0, %0, %1, %6\n\t"
+      "v_fma_f64 %0, %0, %1, %7\n\tv_fma_f64 %0, %0, %1, %8\n\tv_fma_f64 %0, %0, %1, %9\n\tv_fma_f64 %0, %0, %1, %10\n\t"
+      "v_fma_f64 %0, %0, %1, 1.0"
+      : "=&v"(p)
+      : "v"(y), "v"(0x1.b63880a30e9ffp-24), "s"(0x1.63d136366db24p-20), "s"(0x1.ffcb9515a8016p-17), "s"(0x1.4308ac85aa947p-13),
+        "s"(0x1.5d87fe86fe88ep-10), "s"(0x1.3b2ab7181b755p-7), "s"(0x1.c6b08d7047e52p-5), "s"(0x1.ebfbdff823cedp-3),
+        "s"(0x1.62e42fefa39efp-1));
   const uint64_t u = __builtin_bit_cast(uint64_t, p);
   return __builtin_bit_cast(double, (uint64_t)((uint32_t)(u >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, n) << 20)) << 32 | (uint32_t)u);
 }
@@ -410,9 +404,13 @@ __device__ void fill_bins(const X& tiles, const Row& f, const SampleArgs& a, Sha
   } else {
     tiles.each([&](int, const auto& x) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (x[i] >= f.low)
-          atomicAdd((unsigned long long*)&s.bins[bin_of(most, x[i])], (unsigned long long)f.units(weight(f, x[i])));
+      for (int i = 0; i < kPer; i += kBeside) {
+        uint64_t u[kBeside];
+#pragma unroll
+        for (int j = 0; j < kBeside; ++j) u[j] = f.units(weight(f, x[i + j]));
+#pragma unroll
+        for (int j = 0; j < kBeside; ++j)
+          if (x[i + j] >= f.low) atomicAdd((unsigned long long*)&s.bins[bin_of(most, x[i + j])], (unsigned long long)u[j]);
       }
     });
   }
@@ -449,13 +447,15 @@ __device__ Range find_bins(const V* bins, const Row& f, const SampleArgs& a, Sha
     before += mine[j];
   }
   __syncthreads();
-  // the bins' beginnings as logits
-  if (tid < 64) {
-    const float most = (float)f.most, below_from = begin_of((uint32_t)s.found[0]), below_to = begin_of((uint32_t)s.found[1]);
-    const uint32_t lo = key_of(-3.402823466e38f), hi = key_of(most);
-    const float from = below_from > 0.f ? of_key(first_key(lo, hi, [&](uint32_t k) { return most - of_key(k) < below_from; })) : INFINITY;
-    const float to = below_to < INFINITY ? of_key(first_key(lo, hi, [&](uint32_t k) { return most - of_key(k) < below_to; })) : of_key(lo);
-    if (tid == 0) s.range = Range{fmaxf(from, f.low), fmaxf(to, f.low), s.found[2]};
+  // the bins' beginnings as logits, one by a wave each
+  if (tid < 128) {
+    const float most = (float)f.most, below = begin_of((uint32_t)s.found[tid >> 6]);
+    float l = below > 0.f ? -3.402823466e38f : INFINITY;
+    if (below > 0.f && below < INFINITY)
+      l = of_key(first_key(key_of(l), key_of(most), [&](uint32_t k) { return most - of_key(k) < below; }));
+    l = fmaxf(l, f.low);
+    if (tid == 0) s.range.from = l, s.range.target = s.found[2];
+    if (tid == 64) s.range.to = l;
   }
   __syncthreads();
   return s.range;
@@ -485,16 +485,24 @@ __device__ void sum_tiles(const X& tiles, const Row& f, const Range& r, uint64_t
       for (int i = 0; i < kPer; ++i) sum += f.units(weight(f, x[i]));
     } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (!__any(x[i] >= r.to)) continue;
-        const bool certain = x[i] >= r.from;
-        if (__any(certain)) {
-          const uint64_t u = f.units(weight(f, x[i]));
-          sum += certain ? u : 0ull;
+      for (int i = 0; i < kPer; i += kBeside) {
+        float top = x[i];
+#pragma unroll
+        for (int j = 1; j < kBeside; ++j) top = fmaxf(top, x[i + j]);
+        if (!__any(top >= r.to)) continue;
+        if (__any(top >= r.from)) {
+#pragma unroll
+          for (int j = 0; j < kBeside; ++j) {
+            const uint64_t u = f.units(weight(f, x[i + j]));
+            sum += x[i + j] >= r.from ? u : 0ull;
+          }
         }
-        if (x[i] >= r.to && !certain) {
-          const uint32_t n = atomicAdd(&s.n_list, 1u);
-          if (n < kList) s.list[n] = order_of(x[i], (uint32_t)(t * kTile + x.index(i)));
+#pragma unroll
+        for (int j = 0; j < kBeside; ++j) {
+          if (x[i + j] >= r.to && x[i + j] < r.from) {
+            const uint32_t n = atomicAdd(&s.n_list, 1u);
+            if (n < kList) s.list[n] = order_of(x[i + j], (uint32_t)(t * kTile + x.index(i + j)));
+          }
         }
       }
     }
@@ -657,8 +665,12 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
     if (f.top_k) {
       const uint64_t target = few ? range.target : (uint64_t)f.top_k;
       uint64_t there = 0;
-      for (uint32_t i = tid; i < from.n; i += kSThreads) there += from[i] != ~0ull;
-      scan(there, s, &all);
+      if (few) {
+        all = from.n;
+      } else {
+        for (uint32_t i = tid; i < from.n; i += kSThreads) there += from[i] != ~0ull;
+        scan(there, s, &all);
+      }
       if (all >= target) end = descend(from, f, false, target, end, s);
     }
     if (f.top_p < 1.f) end = descend(from, f, true, f.top_k || !few ? part_of(f, sum_of(from)) : want, end, s);
