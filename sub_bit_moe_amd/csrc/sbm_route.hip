@@ -27,148 +27,391 @@ struct RouteArgs {
   bool sigmoid, renorm;
 };
 
+constexpr int kRWaves = kRThreads / 64;
+
 template <typename T>
 __device__ __forceinline__ float logit_at(const void* row, int e) {
   if constexpr (__is_same(T, float)) return ((const float*)row)[e];
   else return to_f32<T>(((const uint16_t*)row)[e]);
 }
 
-// The larger of two choices, of equal ones the lower expert; no choice is -inf with any expert.
+// What a lane has of a token's kN * 64 experts: runs of four neighbours (single ones up to 128 experts), so that a wave reads
+// whole lines.
+template <int kN>
+__device__ __forceinline__ int expert(int i, int lane) {
+  if constexpr (kN < 4) return i * 64 + lane;
+  else return (i >> 2) * 256 + lane * 4 + (i & 3);
+}
+
+// The elements of a row as they are in memory; `none` behind its end.
+template <typename T, int kN>
+struct Row {
+  static constexpr int kWords = __is_same(T, float) ? kN : (kN + 1) / 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* row, int n, uint32_t none, int lane) {
+    constexpr bool kF = __is_same(T, float);
+    if constexpr (kN < 4) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const int e = expert<kN>(i, lane);
+        uint32_t u = none;
+        if (e < n) u = kF ? ((const uint32_t*)row)[e] : ((const uint16_t*)row)[e];
+        if constexpr (kF) w[i] = u;
+        else w[i >> 1] = i & 1 ? w[i >> 1] | u << 16 : u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; i += 4) {
+        const int e = expert<kN>(i, lane);
+        if (e + 4 <= n) {
+          __builtin_memcpy(&w[kF ? i : i / 2], (const char*)row + e * (kF ? 4 : 2), kF ? 16 : 8);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t u = none;
+            if (e + j < n) u = kF ? ((const uint32_t*)row)[e + j] : ((const uint16_t*)row)[e + j];
+            if constexpr (kF) w[i + j] = u;
+            else w[(i + j) >> 1] = j & 1 ? w[(i + j) >> 1] | u << 16 : u;
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (__is_same(T, float)) return __uint_as_float(w[i]);
+    else return to_f32<T>((uint16_t)(w[i >> 1] >> 16 * (i & 1)));
+  }
+};
+
+// 2^x, to 2^-22 of itself.
+__device__ __forceinline__ float exp2_f32(float x) { return __builtin_amdgcn_exp2f(x); }
+constexpr float kLog2e = 1.44269504f;
+
+// A score of an expert's logit in 64 bits; most, sum: the softmax's.  Where e^-l passes 2^700 the sigmoid is 0.
+__device__ __forceinline__ double score_of(const RouteArgs& a, float l, float most, double sum) {
+  constexpr double kLog2e64 = 1.4426950408889634;
+  if (!a.sigmoid) return exp2_f64(((double)l - (double)most) * kLog2e64) * inverse(sum);
+  const double x = -(double)l * kLog2e64;
+  return x > 700. ? 0. : inverse(1. + exp2_f64(x));
+}
+
+// The softmax's sum in 64 bits.
+template <typename T>
+__device__ double sum_of(const RouteArgs& a, const void* row, float most) {
+  double sum = 0;
+  for (int e = (int)threadIdx.x & 63; e < a.n_experts; e += 64) {
+    const float l = logit_at<T>(row, e);
+    sum += l == -INFINITY ? 0. : score_of(a, l, most, 1.);
+  }
+  return wave_sum(sum);
+}
+
+// The larger of two choices, of equal ones the lower expert.
 struct Choice {
   double c;
   int e;
 };
-__device__ __forceinline__ Choice better(Choice a, Choice b) { return b.c > a.c || (b.c == a.c && b.e < a.e) ? b : a; }
+__device__ __forceinline__ bool before(Choice a, Choice b) { return a.c > b.c || (a.c == b.c && a.e < b.e); }
 __device__ __forceinline__ Choice best_of_wave(Choice v) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = better(v, Choice{__shfl_xor(v.c, d, 64), __shfl_xor(v.e, d, 64)});
+  for (int d = 1; d < 64; d <<= 1) {
+    const Choice o{__shfl_xor(v.c, d, 64), __shfl_xor(v.e, d, 64)};
+    if (before(o, v)) v = o;
+  }
   return v;
 }
 
-// A wave has a token, kN experts a lane (expert i * 64 + lane).
-template <typename T, int kN>
-__global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
-  const int lane = (int)threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * (kRThreads / 64) + (threadIdx.x >> 6);
-  if (t >= a.n_tokens) return;
+// The choice of a token's experts in 64 bits, for the few tokens where two values are too near each other for 32: lane j has the
+// j-th expert, or -1.  Nothing is kept, so that it takes few registers: every round computes the scores again.
+template <typename T>
+__device__ int choose_exactly(const RouteArgs& a, const void* row, float most) {
+  const int lane = (int)threadIdx.x & 63, per = a.n_experts / a.n_groups;
   const double kNone = -(double)INFINITY;
-  int32_t* ids = a.ids + t * a.k;
-  float* gates = a.gates + t * a.k;
-  if (a.requests && a.requests[t] < 0) {
-    if (lane < a.k) ids[lane] = -1, gates[lane] = 0.f;
-    return;
-  }
-  const char* row = (const char*)a.logits + t * a.stride * (__is_same(T, float) ? 4 : 2);
-  double s[kN], c[kN], most = kNone;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    const int e = i * 64 + lane;
-    const float l = e < a.n_experts ? logit_at<T>(row, e) : -INFINITY;
-    bad = bad || !(l < INFINITY);
-    s[i] = (double)l;
-    most = fmax(most, s[i]);
-  }
-  double sum = 0;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) most = fmax(most, __shfl_xor(most, d, 64));
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    c[i] = s[i];
-    if (a.sigmoid) s[i] = 1. / (1. + exp(-s[i]));
-    else s[i] = s[i] == kNone ? 0. : exp(s[i] - most);
-    sum += s[i];
-  }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    if (!a.sigmoid) s[i] = sum > 0 ? s[i] / sum : 0.;
-    if (a.bias && c[i] != kNone) {
-      c[i] = s[i] + (double)a.bias[i * 64 + lane];
-      bad = bad || !(c[i] < (double)INFINITY);
+  const double sum = a.sigmoid ? 1. : sum_of<T>(a, row, most);
+  // the best of e0 .. e1 behind `last` in the order
+  const auto next = [&](int e0, int e1, bool scores, Choice last, uint64_t stay) {
+    Choice v{kNone, kMostExperts};
+    for (int e = e0 + lane; e < e1; e += 64) {
+      const float l = logit_at<T>(row, e);
+      if (l == -INFINITY || !((stay >> (e / per)) & 1)) continue;
+      Choice o{!scores && !a.bias ? (double)l : score_of(a, l, most, sum), e};
+      if (a.bias) o.c += (double)a.bias[e];
+      if (o.c > kNone && before(last, o) && before(o, v)) v = o;
     }
-  }
-  if (__any(bad)) {
-    if (lane < a.k) ids[lane] = -1, gates[lane] = 0.f;
-    if (lane == 0 && a.error) atomicAdd(a.error, 1u);
-    return;
-  }
+    return best_of_wave(v);
+  };
+  const Choice none{(double)INFINITY, -1};
+  uint64_t stay = ~0ull;
   if (a.n_groups > 1) {
-    // a group's value: the sum of its largest choices (scores where there is no bias); lane g keeps group g's
-    const int per = a.n_experts / a.n_groups;
     double mine = kNone;
     for (int g = 0; g < a.n_groups; ++g) {
-      double value = kNone;
-      int taken = -1;
-      for (int b = 0; b < a.group_best; ++b) {
-        Choice v{kNone, kMostExperts};
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int e = i * 64 + lane;
-          if (e >= g * per && e < (g + 1) * per && e != taken && c[i] != kNone) v = better(v, Choice{a.bias ? c[i] : s[i], e});
-        }
-        v = best_of_wave(v);
-        if (v.c == kNone) break;
-        value = b ? value + v.c : v.c;
-        taken = v.e;
+      Choice v = next(g * per, (g + 1) * per, true, none, ~0ull);
+      double value = v.c;
+      if (a.group_best == 2 && v.c > kNone) {
+        v = next(g * per, (g + 1) * per, true, v, ~0ull);
+        if (v.c > kNone) value += v.c;
       }
       if (lane == g) mine = value;
     }
-    // the groups that stay, as bits
-    uint64_t stay = 0;
+    stay = 0;
     for (int j = 0; j < a.top_groups; ++j) {
       const Choice v = best_of_wave(Choice{(stay >> lane) & 1 ? kNone : mine, lane});
       if (v.c == kNone) break;
       stay |= 1ull << v.e;
     }
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int e = i * 64 + lane;
-      if (e < a.n_experts && !((stay >> (e / per)) & 1)) c[i] = kNone;
-    }
   }
-  // the k best in turn; lane j keeps the j-th
-  int my_id = -1;
-  double my_score = 0, total = 0;
+  int id = -1;
+  Choice v = none;
   for (int j = 0; j < a.k; ++j) {
-    Choice v{kNone, kMostExperts};
-#pragma unroll
-    for (int i = 0; i < kN; ++i) v = better(v, Choice{c[i], i * 64 + lane});
-    v = best_of_wave(v);
+    v = next(0, a.n_experts, false, v, stay);
     if (v.c == kNone) break;
-    double score = 0;
+    if (lane == j) id = v.e;
+  }
+  return id;
+}
+
+// Lanes' space in LDS for a wave: tokens' candidates, and choices by expert for the groups' sums.
+template <int kN, bool kGroups>
+struct WaveSpace {
+  uint64_t order[64];
+  float logit[64];
+  float choice[kGroups ? kN * 64 : 1];
+};
+
+// A wave takes tokens, and has all of one in its lanes.  The k best: the (k + 1)-th largest of the lanes' largest choices is not
+// above the (k + 1)-th largest of all, so what is not below it (some k + 1 experts) holds those; they go to LDS, a lane each, and
+// are put in order.  Choices with a bias are compared in 32 bits, with what these may be off added to the candidates; where two
+// that follow each other are nearer than that (one token in some hundred to some thousand), the candidates' choices are computed
+// in 64.  Where groups at the border are that near, or there are more than 64 candidates, the whole token is.
+template <typename T, int kN, bool kGroups>
+__global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(RouteArgs a) {
+  __shared__ WaveSpace<kN, kGroups> s_space[kRWaves];
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  WaveSpace<kN, kGroups>& s = s_space[wave];
+  constexpr uint32_t kNoneBits = __is_same(T, float) ? 0xFF800000u : __is_same(T, __bf16) ? 0xFF80u : 0xFC00u;
+  constexpr int kSize = __is_same(T, float) ? 4 : 2;
+  // a bias that is no number or +inf refuses the tokens that it could be chosen for
+  bool odd = false;
+  if (a.bias)
+    for (int e = (int)threadIdx.x & 63; e < a.n_experts; e += 64) odd = odd || !(a.bias[e] < INFINITY);
+  odd = __any(odd);
+  const int64_t step = (int64_t)gridDim.x * kRWaves;
+  for (int64_t t = (int64_t)blockIdx.x * kRWaves + wave; t < a.n_tokens; t += step) {
+    const char* row = (const char*)a.logits + t * a.stride * kSize;
+    // what depends on these is made anew for each token: kept, it would fill the registers
+    int lane = (int)threadIdx.x & 63, n_experts = a.n_experts;
+    asm("" : "+v"(lane), "+s"(n_experts));
+    Row<T, kN> x;
+    x.load(row, n_experts, kNoneBits, lane);
+    const bool padding = a.requests && a.requests[t] < 0;
+    float most = x[0], low = x[0];
+    bool bad = !(x[0] < INFINITY);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      if (i * 64 + lane == v.e) {
-        c[i] = kNone;
-        score = s[i];
+    for (int i = 1; i < kN; ++i) {
+      most = fmaxf(most, x[i]);
+      low = fminf(low, x[i]);
+    }
+    if (a.sigmoid || (!a.bias && !kGroups && a.renorm)) {                  // else the softmax's sum tells
+#pragma unroll
+      for (int i = 1; i < kN; ++i) bad = bad || x[i] != x[i];
+    }
+    most = wave_max(most);
+    bad = __any(bad) || most == INFINITY;
+    const bool masked = __any(low == -INFINITY);
+    // choices
+    float c[kN];
+    float z = 1.f, score_most = 1.f;
+    if ((a.bias || kGroups || !a.renorm) && !a.sigmoid) {
+      z = 0.f;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        c[i] = exp2_f32((x[i] - most) * kLog2e);
+        z += c[i];
+      }
+      z = wave_sum(z);
+      bad = bad || (z != z && most > -INFINITY);
+      score_most = 1.f / z;
+    }
+    if (a.bias || kGroups) {
+      if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) c[i] = __builtin_amdgcn_rcpf(1.f + exp2_f32(-x[i] * kLog2e));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) c[i] *= score_most;
+      }
+      if (a.bias) {
+        Row<float, kN> bias;
+        bias.load(a.bias, n_experts, 0u, lane);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) c[i] += bias[i];
+      }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) c[i] = x[i] == -INFINITY ? -INFINITY : c[i];
+      }
+      if (odd) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) bad = bad || !(c[i] < INFINITY);
+        bad = __any(bad);
       }
     }
-    score = __shfl(score, v.e & 63, 64);
-    total += score;
-    if (lane == j) my_id = v.e, my_score = score;
+    // what two scores may be off together: exponentials of numbers rounded to 32 bits, sums of up to 64 + 6 additions
+    const float off = a.sigmoid ? 0x1p-19f : 0x1p-17f * score_most;
+    bool sure = true;
+    uint64_t stay = ~0ull;
+    const int per = kGroups ? a.n_experts / a.n_groups : 1;
+    if constexpr (kGroups) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) s.choice[expert<kN>(i, lane)] = c[i];
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      // neighbouring lanes share a group
+      int lanes = 1;
+      while (2 * lanes * a.n_groups <= 64) lanes *= 2;
+      const int g = lane / lanes;
+      float one = -INFINITY, two = -INFINITY;
+      if (g < a.n_groups) {
+        for (int e = lane % lanes; e < per; e += lanes) {
+          const float v = s.choice[g * per + e];
+          two = fmaxf(two, fminf(one, v));
+          one = fmaxf(one, v);
+        }
+      }
+      for (int d = 1; d < lanes; d <<= 1) {
+        const float o1 = __shfl_xor(one, d, 64), o2 = __shfl_xor(two, d, 64);
+        two = fmaxf(fmaxf(two, o2), fminf(one, o1));
+        one = fmaxf(one, o1);
+      }
+      const float value = a.group_best == 2 && two > -INFINITY ? one + two : one;
+      // each group's place
+      int place = 0;
+      for (int h = 0; h < a.n_groups; ++h) {
+        const float v = of_lane(value, h * lanes);
+        place += v > value || (v == value && h < g);
+      }
+      const bool first = g < a.n_groups && lane % lanes == 0 && value > -INFINITY;
+      const uint64_t kept = __ballot(first && place < a.top_groups);
+      const float least = -wave_max(first && place < a.top_groups ? -value : -INFINITY);
+      const float next = wave_max(first && place >= a.top_groups ? value : -INFINITY);
+      sure = next == -INFINITY || least - next > 2.f * off + 0x1p-21f * fmaxf(fabsf(least), fabsf(next));
+      stay = 0;
+      for (uint64_t m = kept; m; m &= m - 1) stay |= 1ull << (__builtin_ctzll(m) / lanes);
+    }
+    if (!a.bias) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) c[i] = x[i];
+    }
+    if constexpr (kGroups) {
+      const uint32_t magic = per > 1 ? (uint32_t)((0x100000000ull + per - 1) / per) : 0u;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t e = (uint32_t)expert<kN>(i, lane), g = per > 1 ? __umulhi(e, magic) : e;
+        c[i] = (stay >> (g & 63u)) & 1 ? c[i] : -INFINITY;
+      }
+    }
+    // the (k + 1)-th largest of the lanes' largest
+    float mine = c[0], border = -INFINITY;
+#pragma unroll
+    for (int i = 1; i < kN; ++i) mine = fmaxf(mine, c[i]);
+    for (int j = 0; j <= a.k; ++j) {
+      border = wave_max(mine);
+      if (border == -INFINITY) break;
+      if (lane == __builtin_ctzll(__ballot(mine == border))) mine = -INFINITY;
+    }
+    // candidates
+    if (a.bias) border -= off + 0x1p-22f * fabsf(border);
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const bool is = c[i] >= border && c[i] > -INFINITY;
+      const uint64_t m = __ballot(is);
+      if (!m) continue;
+      const uint32_t at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+      if (is && at < 64) {
+        s.order[at] = (uint64_t)~key_of(c[i]) << 32 | (uint32_t)expert<kN>(i, lane);
+        s.logit[at] = x[i];
+      }
+      n += (uint32_t)__popcll(m);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const uint32_t held = min(n, 64u);
+    uint64_t o = (uint32_t)lane < held ? s.order[lane] : ~0ull;
+    float l = (uint32_t)lane < held ? s.logit[lane] : -INFINITY;
+    uint32_t place = 0;
+    for (uint32_t j = 0; j < held; ++j) place += of_lane(o, (int)j) < o;
+    if ((uint32_t)lane < held) {
+      s.order[place] = o;
+      s.logit[place] = l;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const bool there = (uint32_t)lane < held;
+    o = there ? s.order[lane] : ~0ull;
+    l = there ? s.logit[lane] : 0.f;
+    int id = there && lane < a.k ? (int)(uint32_t)o : -1;
+    bool near = false;
+    if (a.bias) {
+      const float v = of_key(~(uint32_t)(o >> 32)), w = __shfl_down(v, 1, 64);
+      near = __any(lane < a.k && (uint32_t)lane + 1 < held && !(v - w > off + 0x1p-22f * fmaxf(fabsf(v), fabsf(w))));
+    }
+    __builtin_amdgcn_wave_barrier();
+    if ((n > 64 || near || !sure) && !bad && !padding) {
+      if (n > 64 || !sure) {
+        id = choose_exactly<T>(a, row, most);
+      } else {
+        const double sum = a.sigmoid ? 1. : sum_of<T>(a, row, most);
+        const int e = (int)(uint32_t)o;
+        const Choice v{there ? score_of(a, l, most, sum) + (double)a.bias[e] : -(double)INFINITY, there ? e : kMostExperts + lane};
+        uint32_t at = 0;
+        for (uint32_t j = 0; j < held; ++j) at += before(Choice{of_lane(v.c, (int)j), (int)of_lane((uint32_t)v.e, (int)j)}, v);
+        if (there) s.order[at] = (uint32_t)e;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        id = there && lane < a.k ? (int)s.order[lane] : -1;
+        __builtin_amdgcn_wave_barrier();
+      }
+      if (id >= 0) l = logit_at<T>(row, id);
+    }
+    if (bad || padding) id = -1;
+    if (bad && !padding && lane == 0 && a.error) atomicAdd(a.error, 1u);
+    // gates of the chosen, in 64 bits but for the sum over all experts
+    double g = id < 0 ? 0. : score_of(a, l, most, a.renorm ? 1. : (double)z);
+    if (a.renorm) {
+      const double total = wave_sum(g);
+      if (total > 0.) g *= 1. / total;
+    }
+    if (lane < a.k) {
+      a.ids[t * a.k + lane] = id;
+      a.gates[t * a.k + lane] = (float)(g * (double)a.scale);
+    }
   }
-  if (lane < a.k) {
-    double g = my_score;
-    if (a.renorm && total > 0) g /= total;
-    ids[lane] = my_id;
-    gates[lane] = (float)(g * (double)a.scale);
-  }
+}
+
+// Workgroups that fill the chip; each goes on to further tokens, with the bias in its registers.
+constexpr int kRFull = 1024;
+
+template <typename T, int kN>
+void launch_route(const RouteArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)std::min<int64_t>(((int64_t)a.n_tokens + kRWaves - 1) / kRWaves, kRFull)), block(kRThreads);
+  if (a.n_groups > 1) hipLaunchKernelGGL((route_kernel<T, kN, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((route_kernel<T, kN, false>), grid, block, 0, s, a);
 }
 
 template <typename T>
 void launch_route(const RouteArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.n_tokens + kRThreads / 64 - 1) / (kRThreads / 64))), block(kRThreads);
-#define SBM_ROUTE(N) hipLaunchKernelGGL((route_kernel<T, N>), grid, block, 0, s, a)
-  if (a.n_experts <= 64) SBM_ROUTE(1);
-  else if (a.n_experts <= 128) SBM_ROUTE(2);
-  else if (a.n_experts <= 256) SBM_ROUTE(4);
-  else if (a.n_experts <= 512) SBM_ROUTE(8);
-  else if (a.n_experts <= 1024) SBM_ROUTE(16);
-  else if (a.n_experts <= 2048) SBM_ROUTE(32);
-  else SBM_ROUTE(64);
-#undef SBM_ROUTE
+  if (a.n_experts <= 64) launch_route<T, 1>(a, s);
+  else if (a.n_experts <= 128) launch_route<T, 2>(a, s);
+  else if (a.n_experts <= 256) launch_route<T, 4>(a, s);
+  else if (a.n_experts <= 512) launch_route<T, 8>(a, s);
+  else if (a.n_experts <= 1024) launch_route<T, 16>(a, s);
+  else if (a.n_experts <= 2048) launch_route<T, 32>(a, s);
+  else launch_route<T, 64>(a, s);
 }
 
 bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
