@@ -60,19 +60,29 @@ struct Row {
         else w[i >> 1] = i & 1 ? w[i >> 1] | u << 16 : u;
       }
     } else {
+      // a run that passes the end is read from the row's last four elements (there are more than 128), then moved down
+#pragma unroll
+      for (int i = 0; i < kN; i += 4)
+        __builtin_memcpy(&w[kF ? i : i / 2], (const char*)row + min(expert<kN>(i, lane), n - 4) * (kF ? 4 : 2), kF ? 16 : 8);
 #pragma unroll
       for (int i = 0; i < kN; i += 4) {
-        const int e = expert<kN>(i, lane);
-        if (e + 4 <= n) {
-          __builtin_memcpy(&w[kF ? i : i / 2], (const char*)row + e * (kF ? 4 : 2), kF ? 16 : 8);
-        } else {
+        if (i / 4 * 256 + 256 <= n) continue;
+        const int past = expert<kN>(i, lane) - (n - 4);
+        if constexpr (kF) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t u = none;
-            if (e + j < n) u = kF ? ((const uint32_t*)row)[e + j] : ((const uint16_t*)row)[e + j];
-            if constexpr (kF) w[i + j] = u;
-            else w[(i + j) >> 1] = j & 1 ? w[(i + j) >> 1] | u << 16 : u;
+            const bool move = past > j;
+            w[i] = move ? w[i + 1] : w[i];
+            w[i + 1] = move ? w[i + 2] : w[i + 1];
+            w[i + 2] = move ? w[i + 3] : w[i + 2];
+            w[i + 3] = move ? none : w[i + 3];
           }
+        } else {
+          const uint64_t all = none * 0x0001000100010001ull, v = (uint64_t)w[i / 2 + 1] << 32 | w[i / 2];
+          const int by = 16 * max(past, 0);
+          const uint64_t u = by >= 64 ? all : by == 0 ? v : v >> by | all << (64 - by);
+          w[i / 2] = (uint32_t)u;
+          w[i / 2 + 1] = (uint32_t)(u >> 32);
         }
       }
     }
@@ -121,51 +131,88 @@ __device__ __forceinline__ Choice best_of_wave(Choice v) {
   return v;
 }
 
-// The choice of a token's experts in 64 bits, for the few tokens where two values are too near each other for 32: lane j has the
-// j-th expert, or -1.  Nothing is kept, so that it takes few registers: every round computes the scores again.
-template <typename T>
-__device__ int choose_exactly(const RouteArgs& a, const void* row, float most) {
-  const int lane = (int)threadIdx.x & 63, per = a.n_experts / a.n_groups;
-  const double kNone = -(double)INFINITY;
-  const double sum = a.sigmoid ? 1. : sum_of<T>(a, row, most);
-  // the best of e0 .. e1 behind `last` in the order
-  const auto next = [&](int e0, int e1, bool scores, Choice last, uint64_t stay) {
-    Choice v{kNone, kMostExperts};
-    for (int e = e0 + lane; e < e1; e += 64) {
-      const float l = logit_at<T>(row, e);
-      if (l == -INFINITY || !((stay >> (e / per)) & 1)) continue;
-      Choice o{!scores && !a.bias ? (double)l : score_of(a, l, most, sum), e};
-      if (a.bias) o.c += (double)a.bias[e];
-      if (o.c > kNone && before(last, o) && before(o, v)) v = o;
-    }
-    return best_of_wave(v);
-  };
-  const Choice none{(double)INFINITY, -1};
-  uint64_t stay = ~0ull;
-  if (a.n_groups > 1) {
-    double mine = kNone;
-    for (int g = 0; g < a.n_groups; ++g) {
-      Choice v = next(g * per, (g + 1) * per, true, none, ~0ull);
-      double value = v.c;
-      if (a.group_best == 2 && v.c > kNone) {
-        v = next(g * per, (g + 1) * per, true, v, ~0ull);
-        if (v.c > kNone) value += v.c;
-      }
-      if (lane == g) mine = value;
-    }
-    stay = 0;
-    for (int j = 0; j < a.top_groups; ++j) {
-      const Choice v = best_of_wave(Choice{(stay >> lane) & 1 ? kNone : mine, lane});
-      if (v.c == kNone) break;
-      stay |= 1ull << v.e;
+// As many neighbouring lanes for each group as a wave has.
+__device__ __forceinline__ int lanes_of(int n_groups) {
+  int lanes = 1;
+  while (2 * lanes * n_groups <= 64) lanes *= 2;
+  return lanes;
+}
+
+// The groups that stay, as bits, from the values that groups' lanes have; `near`: whether two at the border are nearer than `off`.
+template <typename C>
+__device__ __forceinline__ uint64_t best_groups(const RouteArgs& a, C value, int lanes, C off, bool* near) {
+  const int lane = (int)threadIdx.x & 63, g = lane / lanes;
+  int place = 0;
+  for (int h = 0; h < a.n_groups; ++h) {
+    const C v = of_lane(value, h * lanes);
+    place += v > value || (v == value && h < g);
+  }
+  const bool is = g < a.n_groups && lane % lanes == 0 && value > -(C)INFINITY;
+  const uint64_t kept = __ballot(is && place < a.top_groups);
+  if (near) {
+    const float least = -wave_max(is && place < a.top_groups ? -(float)value : -INFINITY);
+    const float next = wave_max(is && place >= a.top_groups ? (float)value : -INFINITY);
+    *near = next > -INFINITY && !(least - next > off + 0x1p-21f * fmaxf(fabsf(least), fabsf(next)));
+  }
+  uint64_t stay = 0;
+  for (uint64_t m = kept; m; m &= m - 1) stay |= 1ull << (__builtin_ctzll(m) / lanes);
+  return stay;
+}
+
+// The value of a lane's group from its two largest choices.
+template <typename C, typename F>
+__device__ __forceinline__ C group_value(const RouteArgs& a, int lanes, F choice) {
+  const int lane = (int)threadIdx.x & 63, g = lane / lanes, per = a.n_experts / a.n_groups;
+  C one = -(C)INFINITY, two = one;
+  if (g < a.n_groups) {
+    for (int e = lane % lanes; e < per; e += lanes) {
+      const C v = choice(g * per + e), less = one < v ? one : v;
+      two = two > less ? two : less;
+      one = one > v ? one : v;
     }
   }
+  for (int d = 1; d < lanes; d <<= 1) {
+    const C o1 = __shfl_xor(one, d, 64), o2 = __shfl_xor(two, d, 64), less = one < o1 ? one : o1;
+    two = two > o2 ? two : o2;
+    two = two > less ? two : less;
+    one = one > o1 ? one : o1;
+  }
+  return a.group_best == 2 && two > -(C)INFINITY ? one + two : one;
+}
+
+template <typename T>
+__device__ uint64_t groups_exactly(const RouteArgs& a, const void* row, float most) {
+  const double sum = a.sigmoid ? 1. : sum_of<T>(a, row, most);
+  const int lanes = lanes_of(a.n_groups);
+  const double value = group_value<double>(a, lanes, [&](int e) {
+    const float l = logit_at<T>(row, e);
+    return l == -INFINITY ? -(double)INFINITY : score_of(a, l, most, sum) + (a.bias ? (double)a.bias[e] : 0.);
+  });
+  return best_groups(a, value, lanes, 0., nullptr);
+}
+
+// The choice of a token's experts in 64 bits, where more are beside each other than a wave has lanes: lane j has the j-th expert, or
+// -1.  Nothing is kept, so that it takes few registers: every round computes the scores again.
+template <typename T>
+__device__ int choose_exactly(const RouteArgs& a, const void* row, float most) {
+  const int lane = (int)threadIdx.x & 63, per = a.n_groups > 1 ? a.n_experts / a.n_groups : kMostExperts;
+  const double kNone = -(double)INFINITY;
+  const double sum = a.sigmoid ? 1. : sum_of<T>(a, row, most);
+  const uint64_t stay = a.n_groups > 1 ? groups_exactly<T>(a, row, most) : ~0ull;
   int id = -1;
-  Choice v = none;
+  Choice last{(double)INFINITY, -1};
   for (int j = 0; j < a.k; ++j) {
-    v = next(0, a.n_experts, false, v, stay);
+    Choice v{kNone, kMostExperts};
+    for (int e = lane; e < a.n_experts; e += 64) {
+      const float l = logit_at<T>(row, e);
+      if (l == -INFINITY || !((stay >> (e / per)) & 1)) continue;
+      const Choice o{a.bias ? score_of(a, l, most, sum) + (double)a.bias[e] : (double)l, e};
+      if (o.c > kNone && before(last, o) && before(o, v)) v = o;
+    }
+    v = best_of_wave(v);
     if (v.c == kNone) break;
     if (lane == j) id = v.e;
+    last = v;
   }
   return id;
 }
@@ -174,7 +221,6 @@ __device__ int choose_exactly(const RouteArgs& a, const void* row, float most) {
 template <int kN, bool kGroups>
 struct WaveSpace {
   uint64_t order[64];
-  float logit[64];
   float choice[kGroups ? kN * 64 : 1];
 };
 
@@ -182,7 +228,7 @@ struct WaveSpace {
 // above the (k + 1)-th largest of all, so what is not below it (some k + 1 experts) holds those; they go to LDS, a lane each, and
 // are put in order.  Choices with a bias are compared in 32 bits, with what these may be off added to the candidates; where two
 // that follow each other are nearer than that (one token in some hundred to some thousand), the candidates' choices are computed
-// in 64.  Where groups at the border are that near, or there are more than 64 candidates, the whole token is.
+// in 64, as the groups' values are where two at the border are.  With more than 64 candidates the whole token is.
 template <typename T, int kN, bool kGroups>
 __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(RouteArgs a) {
   __shared__ WaveSpace<kN, kGroups> s_space[kRWaves];
@@ -218,28 +264,32 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
     most = wave_max(most);
     bad = __any(bad) || most == INFINITY;
     const bool masked = __any(low == -INFINITY);
+    uint32_t hidden[(kN + 31) / 32] = {};    // a bit for each -inf, so that the logits need not be kept beside the choices
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) hidden[i / 32] |= (x[i] == -INFINITY ? 1u : 0u) << (i % 32);
+    }
+    __builtin_amdgcn_sched_barrier(0);       // steps mixed with one another would take more registers than there are
     // choices
     float c[kN];
     float z = 1.f, score_most = 1.f;
-    if ((a.bias || kGroups || !a.renorm) && !a.sigmoid) {
-      z = 0.f;
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        c[i] = exp2_f32((x[i] - most) * kLog2e);
-        z += c[i];
-      }
-      z = wave_sum(z);
-      bad = bad || (z != z && most > -INFINITY);
-      score_most = 1.f / z;
-    }
     if (a.bias || kGroups) {
       if (a.sigmoid) {
 #pragma unroll
         for (int i = 0; i < kN; ++i) c[i] = __builtin_amdgcn_rcpf(1.f + exp2_f32(-x[i] * kLog2e));
       } else {
+        z = 0.f;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          c[i] = exp2_f32((x[i] - most) * kLog2e);
+          z += c[i];
+        }
+        z = wave_sum(z);
+        score_most = 1.f / z;
 #pragma unroll
         for (int i = 0; i < kN; ++i) c[i] *= score_most;
       }
+      __builtin_amdgcn_sched_barrier(0);
       if (a.bias) {
         Row<float, kN> bias;
         bias.load(a.bias, n_experts, 0u, lane);
@@ -248,17 +298,27 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       }
       if (masked) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) c[i] = x[i] == -INFINITY ? -INFINITY : c[i];
+        for (int i = 0; i < kN; ++i) c[i] = (hidden[i / 32] >> (i % 32)) & 1u ? -INFINITY : c[i];
       }
       if (odd) {
 #pragma unroll
         for (int i = 0; i < kN; ++i) bad = bad || !(c[i] < INFINITY);
         bad = __any(bad);
       }
+    } else {
+      if (!a.sigmoid && !a.renorm) {
+        z = 0.f;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) z += exp2_f32((x[i] - most) * kLog2e);
+        z = wave_sum(z);
+      }
+#pragma unroll
+      for (int i = 0; i < kN; ++i) c[i] = x[i];
     }
+    bad = bad || (z != z && most > -INFINITY);
+    __builtin_amdgcn_sched_barrier(0);
     // what two scores may be off together: exponentials of numbers rounded to 32 bits, sums of up to 64 + 6 additions
     const float off = a.sigmoid ? 0x1p-19f : 0x1p-17f * score_most;
-    bool sure = true;
     uint64_t stay = ~0ull;
     const int per = kGroups ? a.n_experts / a.n_groups : 1;
     if constexpr (kGroups) {
@@ -267,41 +327,17 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      // neighbouring lanes share a group
-      int lanes = 1;
-      while (2 * lanes * a.n_groups <= 64) lanes *= 2;
-      const int g = lane / lanes;
-      float one = -INFINITY, two = -INFINITY;
-      if (g < a.n_groups) {
-        for (int e = lane % lanes; e < per; e += lanes) {
-          const float v = s.choice[g * per + e];
-          two = fmaxf(two, fminf(one, v));
-          one = fmaxf(one, v);
-        }
-      }
-      for (int d = 1; d < lanes; d <<= 1) {
-        const float o1 = __shfl_xor(one, d, 64), o2 = __shfl_xor(two, d, 64);
-        two = fmaxf(fmaxf(two, o2), fminf(one, o1));
-        one = fmaxf(one, o1);
-      }
-      const float value = a.group_best == 2 && two > -INFINITY ? one + two : one;
-      // each group's place
-      int place = 0;
-      for (int h = 0; h < a.n_groups; ++h) {
-        const float v = of_lane(value, h * lanes);
-        place += v > value || (v == value && h < g);
-      }
-      const bool first = g < a.n_groups && lane % lanes == 0 && value > -INFINITY;
-      const uint64_t kept = __ballot(first && place < a.top_groups);
-      const float least = -wave_max(first && place < a.top_groups ? -value : -INFINITY);
-      const float next = wave_max(first && place >= a.top_groups ? value : -INFINITY);
-      sure = next == -INFINITY || least - next > 2.f * off + 0x1p-21f * fmaxf(fabsf(least), fabsf(next));
-      stay = 0;
-      for (uint64_t m = kept; m; m &= m - 1) stay |= 1ull << (__builtin_ctzll(m) / lanes);
+      const int lanes = lanes_of(a.n_groups);
+      bool near;
+      stay = best_groups(a, group_value<float>(a, lanes, [&](int e) { return s.choice[e]; }), lanes, 2.f * off, &near);
+      if (near && !bad && !padding) stay = groups_exactly<T>(a, row, most);
     }
-    if (!a.bias) {
+    if constexpr (kGroups) {
+      if (!a.bias) {                         // the order is the logits': read again, rather than kept
+        x.load(row, n_experts, kNoneBits, lane);
 #pragma unroll
-      for (int i = 0; i < kN; ++i) c[i] = x[i];
+        for (int i = 0; i < kN; ++i) c[i] = x[i];
+      }
     }
     if constexpr (kGroups) {
       const uint32_t magic = per > 1 ? (uint32_t)((0x100000000ull + per - 1) / per) : 0u;
@@ -311,6 +347,7 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
         c[i] = (stay >> (g & 63u)) & 1 ? c[i] : -INFINITY;
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
     // the (k + 1)-th largest of the lanes' largest
     float mine = c[0], border = -INFINITY;
 #pragma unroll
@@ -320,6 +357,7 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       if (border == -INFINITY) break;
       if (lane == __builtin_ctzll(__ballot(mine == border))) mine = -INFINITY;
     }
+    __builtin_amdgcn_sched_barrier(0);
     // candidates
     if (a.bias) border -= off + 0x1p-22f * fabsf(border);
     uint32_t n = 0;
@@ -329,30 +367,16 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       const uint64_t m = __ballot(is);
       if (!m) continue;
       const uint32_t at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
-      if (is && at < 64) {
-        s.order[at] = (uint64_t)~key_of(c[i]) << 32 | (uint32_t)expert<kN>(i, lane);
-        s.logit[at] = x[i];
-      }
+      if (is && at < 64) s.order[at] = (uint64_t)~key_of(c[i]) << 32 | (uint32_t)expert<kN>(i, lane);
       n += (uint32_t)__popcll(m);
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     const uint32_t held = min(n, 64u);
-    uint64_t o = (uint32_t)lane < held ? s.order[lane] : ~0ull;
-    float l = (uint32_t)lane < held ? s.logit[lane] : -INFINITY;
-    uint32_t place = 0;
-    for (uint32_t j = 0; j < held; ++j) place += of_lane(o, (int)j) < o;
-    if ((uint32_t)lane < held) {
-      s.order[place] = o;
-      s.logit[place] = l;
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     const bool there = (uint32_t)lane < held;
-    o = there ? s.order[lane] : ~0ull;
-    l = there ? s.logit[lane] : 0.f;
+    const uint64_t o = wave_sorted(there ? s.order[lane] : ~0ull, held, s.order);
+    float l = there ? logit_at<T>(row, (int)(uint32_t)o) : 0.f;
     int id = there && lane < a.k ? (int)(uint32_t)o : -1;
     bool near = false;
     if (a.bias) {
@@ -360,8 +384,8 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       near = __any(lane < a.k && (uint32_t)lane + 1 < held && !(v - w > off + 0x1p-22f * fmaxf(fabsf(v), fabsf(w))));
     }
     __builtin_amdgcn_wave_barrier();
-    if ((n > 64 || near || !sure) && !bad && !padding) {
-      if (n > 64 || !sure) {
+    if ((n > 64 || near) && !bad && !padding) {
+      if (n > 64) {
         id = choose_exactly<T>(a, row, most);
       } else {
         const double sum = a.sigmoid ? 1. : sum_of<T>(a, row, most);
