@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kMostDim = 32768;
 constexpr int kMostThreads = 1024;
+constexpr int kFewThreads = 256;               // of a workgroup that has several rows
 
 struct NormArgs {
   const void* x;
@@ -24,6 +25,7 @@ struct NormArgs {
   int64_t x_stride, r_stride, ro_stride, o_stride;      // elements
   double eps;
   int32_t dim, k, repeat, block;                        // block: elements that share a scale, the row's if `whole`
+  int32_t n_tokens, lanes;                              // lanes: threads of a row
   bool whole, powers;                                   // powers: scales are bytes
 };
 
@@ -73,22 +75,25 @@ __device__ __forceinline__ void store_raw(void* p, const void* x, int n) {
 }
 
 
-template <typename C>
 struct Sum {
-  __device__ C operator()(C a, C b) const { return a + b; }
+  __device__ double operator()(double a, double b) const { return a + b; }
 };
-template <typename C>
-struct Most {      // NaN stays
-  __device__ C operator()(C a, C b) const { return a >= b || a != a ? a : b; }
+// Magnitudes order as their bits do, NaN above infinity.
+__device__ __forceinline__ uint64_t magnitude(double x) { return __builtin_bit_cast(uint64_t, x) & 0x7FFFFFFFFFFFFFFFull; }
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+struct Most {
+  template <typename V>
+  __device__ V operator()(V a, V b) const {
+    return a > b ? a : b;
+  }
 };
 
-// v joined over the workgroup's waves, in all of its threads, in an order that does not change.
+// v joined over a row's threads, in all of them, in an order that does not change.
 template <typename Op, typename C>
-__device__ __forceinline__ C over_row(C v, C* shared) {
+__device__ __forceinline__ C over_row(C v, C* shared, int lanes) {
   Op op;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = op(v, __shfl_xor(v, d, 64));
-  const int waves = (int)blockDim.x >> 6;
+  const int waves = lanes >> 6;
+  for (int d = 1; d < min(lanes, 64); d <<= 1) v = op(v, __shfl_xor(v, d, 64));
   if (waves > 1) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
@@ -99,6 +104,28 @@ __device__ __forceinline__ C over_row(C v, C* shared) {
   return v;
 }
 
+// Eight elements of a row as codes, and the scale where a block begins; V: the scale's type.
+template <typename V>
+__device__ __forceinline__ void store_codes(const NormArgs& a, int64_t t, int d0, int n_blocks, const float* q, float by, bool bad, V scale) {
+  if (d0 >= a.dim) return;
+  uint32_t y[2] = {0u, 0u};
+  if (!bad) {
+    float c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = fminf(fmaxf(q[j] * by, -448.f), 448.f);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      y[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * j], c[4 * j + 1], 0, false);
+      y[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * j + 2], c[4 * j + 3], (int)y[j], true);
+    }
+  }
+  for (int r = 0; r < a.repeat; ++r) {
+    const int64_t row = t * a.repeat + r;
+    store_raw<1>((uint8_t*)a.out + row * a.o_stride + d0, y, a.dim - d0);
+    if (d0 % a.block == 0) ((V*)a.scales)[row * n_blocks + d0 / a.block] = scale;
+  }
+}
+
 // A workgroup holds a row in its registers, kN times eight elements a thread: everything is read once and written once.  The
 // mean of squares is summed in 64 bits (f64 runs at the rate of unpacked f32 here), so that no row of finite numbers
 // overflows it; what becomes 8 bits is computed in 64 bits throughout (C), so that a code beside the border of two does not
@@ -107,8 +134,10 @@ template <typename T, bool kXF, bool kRF, bool k8, int kN>
 __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
   using C = std::conditional_t<k8, double, float>;
   __shared__ double s_sum[kMostThreads / 64];
-  const int64_t t = blockIdx.x;
-  const int G = (int)blockDim.x, tid = (int)threadIdx.x;
+  // a workgroup has one row, or several of fewer threads than a wave each
+  const int G = a.lanes, tid = (int)threadIdx.x & (G < 64 ? G - 1 : -1);
+  const int64_t t = G < 64 ? (int64_t)blockIdx.x * (kFewThreads / G) + threadIdx.x / (uint32_t)G : (int64_t)blockIdx.x;
+  if (t >= a.n_tokens) return;
   C h[kN][8];
   if (a.residual) {
     const char* row = (const char*)a.residual + t * a.r_stride * (kRF ? 4 : 2);
@@ -160,7 +189,7 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
   for (int i = 0; i < kN; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)h[i][j], (double)h[i][j], ss);
-  const double mean = over_row<Sum<double>>(ss, s_sum) / (double)a.dim + a.eps;
+  const double mean = over_row<Sum>(ss, s_sum, G) / (double)a.dim + a.eps;
   const double inv = inverse_root(mean);
   // weights; what is behind the row's end is zero
 #pragma unroll
@@ -188,70 +217,58 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
         store_raw<2>((uint16_t*)a.out + (t * a.repeat + r) * a.o_stride + d0, y, a.dim - d0);
     }
   } else {
-    double top[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      top[i] = fabs(h[i][0]);
-#pragma unroll
-      for (int j = 1; j < 8; ++j) top[i] = Most<double>()(top[i], fabs(h[i][j]));
-    }
-    if (a.whole) {
-      double all = top[0];
-#pragma unroll
-      for (int i = 1; i < kN; ++i) all = Most<double>()(all, top[i]);
-      all = over_row<Most<double>>(all, s_sum);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) top[i] = all;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {                    // 4 or 16 neighbouring lanes hold a block
-        top[i] = Most<double>()(top[i], __shfl_xor(top[i], 1, 64));
-        top[i] = Most<double>()(top[i], __shfl_xor(top[i], 2, 64));
-        if (a.block == 128) {
-          top[i] = Most<double>()(top[i], __shfl_xor(top[i], 4, 64));
-          top[i] = Most<double>()(top[i], __shfl_xor(top[i], 8, 64));
-        }
-      }
-    }
     const int n_blocks = (a.dim + a.block - 1) / a.block;
+    if (a.powers) {
+      // a power of two does not change what is rounded: all the rest in 32 bits, with what is below gathered in the lowest
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int d0 = (tid + i * G) * 8;
-      if (d0 >= a.dim) continue;
-      const bool bad = !(top[i] < (double)INFINITY);
-      float scale;
-      uint8_t power = 255;
-      double by;
-      if (a.powers) {
+      for (int i = 0; i < kN; ++i) {
+        const int d0 = (tid + i * G) * 8;
+        float q[8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          q[j] = to_odd(h[i][j]);
+          top = Most()(top, magnitude(q[j]));
+        }
+        top = Most()(top, (uint32_t)__shfl_xor((int)top, 1, 64));          // four neighbouring lanes hold a block
+        top = Most()(top, (uint32_t)__shfl_xor((int)top, 2, 64));
         // the least power of two at which nothing passes 448 = 1.75 * 2^8
-        const uint64_t b = __builtin_bit_cast(uint64_t, top[i]);
-        int e = (int)(b >> 52) - 1023 - 8 + ((b & 0xFFFFFFFFFFFFFull) > 0xC000000000000ull);
-        e = min(max(e, -126), 127);
-        if (!bad) power = (uint8_t)(e + 127);
-        by = __builtin_bit_cast(double, (uint64_t)(1023 - e) << 52);
-      } else {
-        scale = fmaxf((float)(top[i] / 448.), 0x1p-126f);
-        if (bad) scale = __builtin_nanf("");
-        by = 1. / (double)scale;
+        const int e = min(max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u), -126), 127);
+        const bool bad = top >= 0x7F800000u;
+        const float by = __builtin_amdgcn_ldexpf(1.f, -e);
+        store_codes(a, t, d0, n_blocks, q, by, bad, (uint8_t)(bad ? 255 : e + 127));
       }
-      uint32_t y[2] = {0u, 0u};
-      if (!bad) {
+    } else {
+      uint64_t top[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        top[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top[i] = Most()(top[i], magnitude(h[i][j]));
+      }
+      if (a.whole) {
+        uint64_t all = top[0];
+#pragma unroll
+        for (int i = 1; i < kN; ++i) all = Most()(all, top[i]);
+        all = over_row<Most>(all, (uint64_t*)s_sum, G);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) top[i] = all;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)                    // 16 neighbouring lanes hold a block
+#pragma unroll
+          for (int d = 1; d < 16; d <<= 1) top[i] = Most()(top[i], (uint64_t)__shfl_xor(top[i], d, 64));
+      }
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const double most = __builtin_bit_cast(double, top[i]);
+        const bool bad = !(most < (double)INFINITY);
+        const float scale = fmaxf((float)(most / 448.), 0x1p-126f);
+        const double by = 1. / (double)scale;
         float q[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(to_odd(h[i][j] * by), -448.f), 448.f);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          y[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * j], q[4 * j + 1], 0, false);
-          y[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * j + 2], q[4 * j + 3], (int)y[j], true);
-        }
-      }
-      for (int r = 0; r < a.repeat; ++r) {
-        const int64_t row = t * a.repeat + r;
-        store_raw<1>((uint8_t*)a.out + row * a.o_stride + d0, y, a.dim - d0);
-        if (d0 % a.block == 0) {
-          if (a.powers) ((uint8_t*)a.scales)[row * n_blocks + d0 / 32] = power;
-          else ((float*)a.scales)[row * n_blocks + d0 / a.block] = scale;
-        }
+        for (int j = 0; j < 8; ++j) q[j] = to_odd(h[i][j] * by);
+        store_codes(a, t, (tid + i * G) * 8, n_blocks, q, 1.f, bad, bad ? __builtin_nanf("") : scale);
       }
     }
   }
@@ -275,11 +292,17 @@ bool overlap(const Rows& a, const Rows& b) {
 }
 
 template <typename T, bool kXF, bool kRF, bool k8>
-void launch_norm(const NormArgs& a, int32_t n_tokens, hipStream_t s) {
-  const int chunks = (a.dim + 7) / 8;
-  const int n = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
-  const int threads = std::max(64, ((chunks + n - 1) / n + 63) / 64 * 64);
-  const dim3 grid((unsigned)n_tokens), block((unsigned)threads);
+void launch_norm(NormArgs a, int32_t n_tokens, hipStream_t s) {
+  // Eight elements a thread as long as a workgroup has that many threads.  8-bit results, which keep the vector units busy, take
+  // sixteen from 256 threads on, so that more rows are in one CU (8192 rows of 4096: 55 instead of 61 us, 2080: 38 and 39); 16-bit
+  // ones do not (4096: 54 instead of 50).
+  const int chunks = (a.dim + 7) / 8, n = chunks > 2048 ? 4 : chunks > (k8 ? 256 : 1024) ? 2 : 1;
+  // rows of up to 256 elements share a wave; 16 lanes at least have a block of 128
+  a.lanes = ((chunks + n - 1) / n + 63) / 64 * 64;
+  if (chunks <= 32)
+    for (a.lanes = k8 ? 16 : 8; a.lanes < chunks;) a.lanes *= 2;
+  const int rows = a.lanes < 64 ? kFewThreads / a.lanes : 1;
+  const dim3 grid((unsigned)(((int64_t)n_tokens + rows - 1) / rows)), block((unsigned)(a.lanes * rows));
   if (n == 1) hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, 1>), grid, block, 0, s, a);
   else if (n == 2) hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, 2>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, 4>), grid, block, 0, s, a);
@@ -349,7 +372,7 @@ extern "C" int sbm_add_rms_norm(const void* x, int64_t x_stride, const float* ga
       if (&other < &o && overlap(o, other)) return fail(SBM_EINVAL, "outputs overlap");
   }
   const NormArgs a{x, residual, residual_out, weight, gates, out, scales, x_stride, residual_stride, residual_out_stride,
-                   out_stride, eps, dim, k, repeat, block, scale_block == 0, scale_block == 32};
+                   out_stride, eps, dim, k, repeat, block, n_tokens, 0, scale_block == 0, scale_block == 32};
   if (flags & SBM_F_IN_BF16) launch_norm<__bf16>(a, n_tokens, flags, (hipStream_t)stream);
   else launch_norm<_Float16>(a, n_tokens, flags, (hipStream_t)stream);
   const hipError_t e = hipGetLastError();
