@@ -89,11 +89,16 @@ struct Most {
 };
 
 // v joined over a row's threads, in all of them, in an order that does not change.
-template <typename Op, typename C>
+template <typename Op, bool kFew, typename C>
 __device__ __forceinline__ C over_row(C v, C* shared, int lanes) {
   Op op;
+  if constexpr (kFew) {
+    for (int d = 1; d < lanes; d <<= 1) v = op(v, __shfl_xor(v, d, 64));
+    return v;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = op(v, __shfl_xor(v, d, 64));
   const int waves = lanes >> 6;
-  for (int d = 1; d < min(lanes, 64); d <<= 1) v = op(v, __shfl_xor(v, d, 64));
   if (waves > 1) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
@@ -130,14 +135,17 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int64_t t, int d0
 // mean of squares is summed in 64 bits (f64 runs at the rate of unpacked f32 here), so that no row of finite numbers
 // overflows it; what becomes 8 bits is computed in 64 bits throughout (C), so that a code beside the border of two does not
 // depend on the order of a sum.
-template <typename T, bool kXF, bool kRF, bool k8, int kN>
+template <typename T, bool kXF, bool kRF, bool k8, int kN, bool kFew>
 __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
   using C = std::conditional_t<k8, double, float>;
   __shared__ double s_sum[kMostThreads / 64];
-  // a workgroup has one row, or several of fewer threads than a wave each
-  const int G = a.lanes, tid = (int)threadIdx.x & (G < 64 ? G - 1 : -1);
-  const int64_t t = G < 64 ? (int64_t)blockIdx.x * (kFewThreads / G) + threadIdx.x / (uint32_t)G : (int64_t)blockIdx.x;
-  if (t >= a.n_tokens) return;
+  // a workgroup has one row, or (kFew) several of fewer threads than a wave each
+  const int G = kFew ? a.lanes : (int)blockDim.x, tid = kFew ? (int)threadIdx.x & (G - 1) : (int)threadIdx.x;
+  int64_t t = blockIdx.x;
+  if constexpr (kFew) {
+    t = t * (kFewThreads / G) + threadIdx.x / (uint32_t)G;
+    if (t >= a.n_tokens) return;
+  }
   C h[kN][8];
   if (a.residual) {
     const char* row = (const char*)a.residual + t * a.r_stride * (kRF ? 4 : 2);
@@ -189,7 +197,7 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
   for (int i = 0; i < kN; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)h[i][j], (double)h[i][j], ss);
-  const double mean = over_row<Sum>(ss, s_sum, G) / (double)a.dim + a.eps;
+  const double mean = over_row<Sum, kFew>(ss, s_sum, G) / (double)a.dim + a.eps;
   const double inv = inverse_root(mean);
   // weights; what is behind the row's end is zero
 #pragma unroll
@@ -250,7 +258,7 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
         uint64_t all = top[0];
 #pragma unroll
         for (int i = 1; i < kN; ++i) all = Most()(all, top[i]);
-        all = over_row<Most>(all, (uint64_t*)s_sum, G);
+        all = over_row<Most, kFew>(all, (uint64_t*)s_sum, G);
 #pragma unroll
         for (int i = 0; i < kN; ++i) top[i] = all;
       } else {
@@ -303,9 +311,12 @@ void launch_norm(NormArgs a, int32_t n_tokens, hipStream_t s) {
     for (a.lanes = k8 ? 16 : 8; a.lanes < chunks;) a.lanes *= 2;
   const int rows = a.lanes < 64 ? kFewThreads / a.lanes : 1;
   const dim3 grid((unsigned)(((int64_t)n_tokens + rows - 1) / rows)), block((unsigned)(a.lanes * rows));
-  if (n == 1) hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, 1>), grid, block, 0, s, a);
-  else if (n == 2) hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, 4>), grid, block, 0, s, a);
+#define SBM_NORM(N, FEW) hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, N, FEW>), grid, block, 0, s, a)
+  if (rows > 1) SBM_NORM(1, true);
+  else if (n == 1) SBM_NORM(1, false);
+  else if (n == 2) SBM_NORM(2, false);
+  else SBM_NORM(4, false);
+#undef SBM_NORM
 }
 
 template <typename T>
