@@ -749,83 +749,94 @@ def attention_kv4(q, cache: KVCache, block_table, kv_lens, cu_q=None, scale: flo
 
 # ------------------------------------------------------------------ around the experts
 
-def _rows(t, what: str, dtype, at: int, n, width: int):
-    """[n, width] with neighbouring elements and any distance of rows: (address, row stride).  n None: any."""
-    if t.dim() != 2 or t.shape[1] != width or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{what} must be [{'rows' if n is None else n}, {width}], not {tuple(t.shape)}")
-    rs, es = t.stride()
-    if es != 1 and width > 1:
+def _rows(t, what: str, dtype, at: int, shape):
+    """[rows, width] with neighbouring elements and any distance of rows: (address, row stride)."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == at >= 0:
+        rs, es = t.stride()
+        if es == 1 or shape[1] <= 1:
+            return t.data_ptr(), rs
         raise ValueError(f"{what} must have neighbouring elements")
-    return _dev(t, what, dtype, at, False), rs
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {tuple(shape)}, not {tuple(t.shape)}")
+    return _dev(t, what, dtype, at, False), 0
 
 
 def _norm(x, weight, residual, gates, eps, repeat, out, residual_out, dtype, stream, block, scales):
     import torch
-    f32, at, flags = torch.float32, x.get_device(), 0
-    if x.dim() != 2:
+    f32, at, shape, kind, flags = torch.float32, x.get_device(), x.shape, x.dtype, 0
+    if len(shape) != 2:
         raise ValueError("x must be [tokens, dim], or [tokens * k, dim] with gates")
+    n, D = shape
     if dtype is None:                              # the call's 16-bit type
-        for t in (weight, x, residual, None if block is not None else out):
-            if t is not None and t.dtype is not f32:
-                dtype = t.dtype
-                break
+        if weight is not None:
+            dtype = weight.dtype
+        elif kind is not f32:
+            dtype = kind
         else:
-            raise ValueError("dtype must be given where everything is float32")
+            for t in (residual, None if block is not None else out):
+                if t is not None and t.dtype is not f32:
+                    dtype = t.dtype
+                    break
+            else:
+                raise ValueError("dtype must be given where everything is float32")
     if dtype is torch.bfloat16:
         flags = N.SBM_F_IN_BF16
     elif dtype is not torch.float16:
         raise TypeError(f"the norm's type must be float16 or bfloat16, not {dtype}")
-    n, D = x.shape
-    k, pg = 1, 0
-    if gates is not None:
-        if gates.dim() != 2 or not gates.shape[1] or gates.shape[0] * gates.shape[1] != n:
-            raise ValueError(f"gates must be [tokens, k] of the {n} rows of x, not {tuple(gates.shape)}")
-        k, pg = gates.shape[1], _dev(gates, "gates", f32, at)
-    T = n // k
-    if x.dtype is f32:
+    if kind is f32:
         flags |= N.SBM_F_IN_F32
-        px, sx = _rows(x, "x", f32, at, None, D)
-    else:
-        px, sx = _rows(x, "x", dtype, at, None, D)
-    pw = pr = sr = po = so = 0
+    elif kind is not dtype:
+        raise TypeError(f"x must be {dtype} or {f32}, not {kind}")
+    k, pg, T, held = 1, 0, n, shape                # held: the residual's shape
+    if gates is not None:
+        sg = gates.shape
+        if len(sg) != 2 or not sg[1] or sg[0] * sg[1] != n:
+            raise ValueError(f"gates must be [tokens, k] of the {n} rows of x, not {tuple(sg)}")
+        T, k = sg
+        pg = _dev(gates, "gates", f32, at)
+        if k > 1:
+            held = (T, D)
+    px, sx = _rows(x, "x", kind, at, shape)
+    pw = pr = sr = po = so = ps = 0
     if weight is not None:
         if weight.numel() != D:
             raise ValueError(f"weight must hold {D} elements")
         pw = _dev(weight, "weight", dtype, at)
-    if residual is not None:
-        of = residual.dtype
-        if of is f32:
+    of = residual if residual is not None else residual_out
+    if of is not None:
+        if of.dtype is f32:
             flags |= N.SBM_F_RESIDUAL_F32
-        pr, sr = _rows(residual, "residual", f32 if of is f32 else dtype, at, T, D)
-        if residual_out is None:
-            residual_out = residual.new_empty((T, D)) if stream is None else _made_on(stream, residual.new_empty, (T, D))
-            po, so = residual_out.data_ptr(), D
-    elif residual_out is not None:
-        of = residual_out.dtype
-        if of is f32:
-            flags |= N.SBM_F_RESIDUAL_F32
-    if residual_out is not None and not po:
-        po, so = _rows(residual_out, "residual_out", f32 if of is f32 else dtype, at, T, D)
-    rows, ps = T * repeat, 0
+            of = f32
+        else:
+            of = dtype
+        if residual is not None:
+            pr, sr = _rows(residual, "residual", of, at, held)
+            if residual_out is None:
+                residual_out = residual.new_empty(held) if stream is None else _made_on(stream, residual.new_empty, held)
+                po, so = residual_out.data_ptr(), D
+            elif residual_out is residual:
+                po, so = pr, sr
+        if po == 0:
+            po, so = _rows(residual_out, "residual_out", of, at, held)
+    rows = T * repeat
     if block is None:
         kind = dtype
     else:
         kind = torch.float8_e4m3fn
         flags |= N.SBM_F_OUT_FP8
-        many, held = (-(-D // block) if block else 1), torch.uint8 if block == 32 else f32
+        many, of = (-(-D // block) if block > 0 else 1), torch.uint8 if block == 32 else f32
         if scales is None:
-            scales = x.new_empty((rows, many), dtype=held) if stream is None else \
-                _made_on(stream, x.new_empty, (rows, many), dtype=held)
+            scales = x.new_empty((rows, many), dtype=of) if stream is None else _made_on(stream, x.new_empty, (rows, many), dtype=of)
             ps = scales.data_ptr()
         elif scales.shape != (rows, many):
             raise ValueError(f"scales must be {(rows, many)}, not {tuple(scales.shape)}")
         else:
-            ps = _dev(scales, "scales", held, at)
+            ps = _dev(scales, "scales", of, at)
     if out is None:
         out = x.new_empty((rows, D), dtype=kind) if stream is None else _made_on(stream, x.new_empty, (rows, D), dtype=kind)
         pout, sout = out.data_ptr(), D
     else:
-        pout, sout = _rows(out, "out" if block is None else "codes", kind, at, rows, D)
+        pout, sout = _rows(out, "out" if block is None else "codes", kind, at, (rows, D))
     check(lib().sbm_add_rms_norm(px, sx, pg, k, pr, sr, pw, eps, T, D, po, so, pout, sout, repeat, ps, block or 0, flags,
                                  _stream(stream, at)))
     return out, scales, residual_out
@@ -856,12 +867,13 @@ def add_rms_norm_fp8(x, weight=None, residual=None, gates=None, eps: float = 1e-
 def _logits(t, at: int):
     """(address, row stride, flags) of [rows, width] logits."""
     import torch
-    if t.dim() != 2:
+    kind, shape = t.dtype, t.shape
+    if len(shape) != 2:
         raise ValueError("logits must be [rows, width]")
-    flags = N.SBM_F_IN_F32 if t.dtype is torch.float32 else N.SBM_F_IN_BF16 if t.dtype is torch.bfloat16 else 0
-    if not flags and t.dtype is not torch.float16:
-        raise TypeError(f"logits must be float32, float16 or bfloat16, not {t.dtype}")
-    p, stride = _rows(t, "logits", t.dtype, at, None, t.shape[1])
+    flags = N.SBM_F_IN_F32 if kind is torch.float32 else N.SBM_F_IN_BF16 if kind is torch.bfloat16 else 0
+    if not flags and kind is not torch.float16:
+        raise TypeError(f"logits must be float32, float16 or bfloat16, not {kind}")
+    p, stride = _rows(t, "logits", kind, at, shape)
     return p, stride, flags
 
 
