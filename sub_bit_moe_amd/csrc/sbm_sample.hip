@@ -197,7 +197,7 @@ struct Tiles {
 };
 
 // The LDS of a workgroup.
-struct Shared {
+struct alignas(16) Shared {
   union {
     uint64_t bins[kBins];                    // weights
     uint32_t counts_of[kBins];
@@ -452,89 +452,71 @@ struct Source {
   }
 };
 
-// The place in the order at which `target` tokens, or units of weight, are reached among those up to `end`: ten bits at a
-// time, from the highest in which two differ.
+// Where in the order a filter ends.
+struct Reached {
+  uint64_t order, sum;                       // the last that stays; the weight up to it
+};
+
+// Where `target` tokens, or units of weight (by_weight; 0: top_p of all of it), are reached among those of orders base .. base + last
+// up to `end`; all of them where they are fewer.  The stretch is cut into 1024 equal parts, each with its tokens and (sums) their
+// weight, and the part in which the end is into 1024 again, until a wave can put a part's tokens in order.
 template <typename T>
-__device__ uint64_t descend(const Source<T>& from, const Row& f, bool weights, uint64_t target, uint64_t end, Shared& s) {
-  const int tid = (int)threadIdx.x;
-  uint64_t low = ~0ull, high = 0;
-  if (!from.row) {
-    for (uint32_t i = tid; i < from.n; i += kSThreads) {
-      const uint64_t o = from.list[i];
-      low = min(low, o);
-      high = max(high, o);
-    }
-    __syncthreads();
-    if (tid == 0) s.found[0] = ~0ull, s.found[1] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      low = min(low, (uint64_t)__shfl_xor(low, d, 64));
-      high = max(high, (uint64_t)__shfl_xor(high, d, 64));
-    }
-    if ((tid & 63) == 0) {
-      atomicMin((unsigned long long*)&s.found[0], (unsigned long long)low);
-      atomicMax((unsigned long long*)&s.found[1], (unsigned long long)high);
-    }
-    __syncthreads();
-    low = s.found[0];
-    high = s.found[1];
-  } else {
-    low = 0;
-    high = (1ull << 52) - 1;
-  }
-  int top = low == high ? 0 : 64 - __builtin_clzll(low ^ high);        // bits that are not known yet
-  uint64_t prefix = top < 52 ? low >> top : 0;
-  while (top > 0) {
-    const int shift = max(top - 10, 0);
+__device__ Reached reach(const Source<T>& from, const Row& f, uint64_t base, uint64_t last, bool by_weight, bool sums, uint64_t target,
+                         uint64_t end, Shared& s) {
+  const uint32_t tid = threadIdx.x;
+  uint64_t sum_before = 0;
+  for (bool first = true;; first = false) {
+    const int shift = max(54 - __builtin_clzll(last | 1), 0);
     __syncthreads();
     s.sums[tid] = 0;
     s.counts[tid] = 0;
+    if (tid == 0) s.n_few = 0;
     __syncthreads();
     for (uint32_t i = tid; i < from.n; i += kSThreads) {
-      const uint64_t o = from[i];
-      if (o > end || o >> top != prefix) continue;
-      const uint32_t digit = (uint32_t)(o >> shift) & ((1u << (top - shift)) - 1u);
-      atomicAdd(&s.counts[digit], 1u);
-      if (weights && logit_of(o) >= f.low)
-        atomicAdd((unsigned long long*)&s.sums[digit], (unsigned long long)f.units(weight(f, logit_of(o))));
+      const uint64_t o = from[i], off = o - base;
+      if (o > end || off > last) continue;
+      atomicAdd(&s.counts[off >> shift], 1u);
+      if (sums && logit_of(o) >= f.low)
+        atomicAdd((unsigned long long*)&s.sums[off >> shift], (unsigned long long)f.units(weight(f, logit_of(o))));
     }
     __syncthreads();
-    const uint64_t mine = weights ? s.sums[tid] : s.counts[tid];
-    uint64_t all;
-    const uint64_t before = scan(mine, s, &all);
-    if (before < target && before + mine >= target) {
-      s.found[0] = (uint64_t)tid;
-      s.found[1] = target - before;
-      s.found[2] = s.counts[tid];
+    const uint32_t count = s.counts[tid];
+    const uint64_t sum = s.sums[tid];
+    uint32_t all = 0, place = 0;
+    uint64_t total = 0, before = 0;
+    if (!by_weight) place = scan(count, s, &all);
+    if (sums) before = scan(sum, s, &total);
+    if (first) {
+      if (by_weight && target == 0) target = part_of(f, total);
+      if (!by_weight && all < target) return Reached{end, total};
+    }
+    const uint64_t here = by_weight ? before : place, more = by_weight ? sum : count;
+    if (here < target && here + more >= target) {
+      s.found[0] = tid;
+      s.found[1] = target - here;
+      s.found[2] = count;
+      s.found[3] = before;
     }
     __syncthreads();
-    prefix = prefix << (top - shift) | s.found[0];
+    base += s.found[0] << shift;
+    last = (1ull << shift) - 1;
     target = s.found[1];
-    top = shift;
-    const uint32_t left = (uint32_t)s.found[2];
-    if (left <= 64 && top > 0) {             // few tokens: a wave puts them in order
-      if (tid == 0) s.n_few = 0;
-      __syncthreads();
-      for (uint32_t i = tid; i < from.n; i += kSThreads) {
-        const uint64_t o = from[i];
-        if (o <= end && o >> top == prefix) s.few[atomicAdd(&s.n_few, 1u)] = o;
-      }
-      __syncthreads();
-      if (tid < 64) {
-        const uint64_t o = wave_sorted((uint32_t)tid < left ? s.few[tid] : ~0ull, left, s.few);
-        uint64_t v = (uint32_t)tid < left;
-        if (weights) v = v && logit_of(o) >= f.low ? f.units(weight(f, logit_of(o))) : 0;
-        const uint64_t upto = wave_scan(v);
-        if (upto - v < target && upto >= target) s.found[3] = o;
-      }
-      __syncthreads();
-      prefix = s.found[3];
-      top = 0;
+    const uint32_t there = (uint32_t)s.found[2];
+    sum_before += s.found[3];
+    if (there > 64) continue;
+    for (uint32_t i = tid; i < from.n; i += kSThreads) {
+      const uint64_t o = from[i];
+      if (o <= end && o - base <= last) s.few[atomicAdd(&s.n_few, 1u)] = o;
     }
+    __syncthreads();
+    if (tid < 64) {
+      const uint64_t o = wave_sorted(tid < there ? s.few[tid] : ~0ull, there, s.few);
+      const uint64_t u = sums && tid < there && logit_of(o) >= f.low ? f.units(weight(f, logit_of(o))) : 0, upto = wave_scan(u);
+      if (by_weight ? upto - u < target && upto >= target : tid + 1 == target) s.found[0] = o, s.found[1] = sum_before + upto;
+    }
+    __syncthreads();
+    return Reached{s.found[0], s.found[1]};
   }
-  __syncthreads();
-  return prefix;
 }
 
 __device__ void refuse(const SampleArgs& a, int64_t r) {
@@ -557,7 +539,7 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
   const bool few = s.n_list <= kList;
   const bool ordered = f.top_k || f.top_p < 1.f;
   uint64_t end = ~0ull - 1;                  // the last that stays; ~0 is no token
-  uint64_t mine, before, all, want = range.target, total;
+  uint64_t mine, before, want = range.target, total, all;
   if (ordered && s.n_list <= 64) {           // a wave puts them in order; none where min_p lets none of a bin stay
     if (tid == 0) s.found[3] = end;
     if (tid < 64 && s.n_list > 0) {
@@ -573,29 +555,16 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
     __syncthreads();
     end = s.found[3];
   } else if (ordered) {
-    // more than the list holds: the whole row, bit by bit
-    const auto sum_of = [&](const Source<T>& from) {
-      uint64_t sum = 0;
-      for (uint32_t i = tid; i < from.n; i += kSThreads) {
-        const uint64_t o = from[i];
-        if (o <= end && logit_of(o) >= f.low) sum += f.units(weight(f, logit_of(o)));
-      }
-      scan(sum, s, &all);
-      return all;
-    };
+    // the list, or the whole row where the list does not hold what there is
     const Source<T> from{few ? nullptr : f.at, few ? s.n_list : (uint32_t)a.vocab, s.list};
+    const float high = few ? fminf(range.from, (float)f.most) : (float)f.most, low = few ? range.to : f.low;
+    const uint64_t base = (uint64_t)~key_of(high) << 20, last = ((uint64_t)~key_of(low) << 20 | 0xFFFFFu) - base;
     if (f.top_k) {
-      const uint64_t target = few ? range.target : (uint64_t)f.top_k;
-      uint64_t there = 0;
-      if (few) {
-        all = from.n;
-      } else {
-        for (uint32_t i = tid; i < from.n; i += kSThreads) there += from[i] != ~0ull;
-        scan(there, s, &all);
-      }
-      if (all >= target) end = descend(from, f, false, target, end, s);
+      const Reached r = reach(from, f, base, last, false, f.top_p < 1.f, few ? range.target : (uint64_t)f.top_k, end, s);
+      end = r.order;
+      want = part_of(f, r.sum);
     }
-    if (f.top_p < 1.f) end = descend(from, f, true, f.top_k || !few ? part_of(f, sum_of(from)) : want, end, s);
+    if (f.top_p < 1.f) end = reach(from, f, base, last, true, true, f.top_k || few ? want : 0ull, end, s).order;
     if (few) {
       for (uint32_t i = tid; i < s.n_list; i += kSThreads) {
         const uint64_t o = s.list[i];
