@@ -286,15 +286,17 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
         }
         z = wave_sum(z);
         score_most = 1.f / z;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) c[i] *= score_most;
       }
+      const float by = a.sigmoid ? 1.f : score_most;
       __builtin_amdgcn_sched_barrier(0);
       if (a.bias) {
         Row<float, kN> bias;
         bias.load(a.bias, n_experts, 0u, lane);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) c[i] += bias[i];
+        for (int i = 0; i < kN; ++i) c[i] = fused(c[i], by, bias[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) c[i] *= by;
       }
       if (masked) {
 #pragma unroll
@@ -316,6 +318,11 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       for (int i = 0; i < kN; ++i) c[i] = x[i];
     }
     bad = bad || (z != z && most > -INFINITY);
+    if (bad || padding) {
+      if (lane < a.k) a.ids[t * a.k + lane] = -1, a.gates[t * a.k + lane] = 0.f;
+      if (!padding && lane == 0 && a.error) atomicAdd(a.error, 1u);
+      continue;
+    }
     __builtin_amdgcn_sched_barrier(0);
     // what two scores may be off together: exponentials of numbers rounded to 32 bits, sums of up to 64 + 6 additions
     const float off = a.sigmoid ? 0x1p-19f : 0x1p-17f * score_most;
@@ -330,7 +337,7 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       const int lanes = lanes_of(a.n_groups);
       bool near;
       stay = best_groups(a, group_value<float>(a, lanes, [&](int e) { return s.choice[e]; }), lanes, 2.f * off, &near);
-      if (near && !bad && !padding) stay = groups_exactly<T>(a, row, most);
+      if (near) stay = groups_exactly<T>(a, row, most);
     }
     if constexpr (kGroups) {
       if (!a.bias) {                         // the order is the logits': read again, rather than kept
@@ -384,7 +391,7 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       near = __any(lane < a.k && (uint32_t)lane + 1 < held && !(v - w > off + 0x1p-22f * fmaxf(fabsf(v), fabsf(w))));
     }
     __builtin_amdgcn_wave_barrier();
-    if ((n > 64 || near) && !bad && !padding) {
+    if (n > 64 || near) {
       if (n > 64) {
         id = choose_exactly<T>(a, row, most);
       } else {
@@ -402,8 +409,6 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       }
       if (id >= 0) l = logit_at<T>(row, id);
     }
-    if (bad || padding) id = -1;
-    if (bad && !padding && lane == 0 && a.error) atomicAdd(a.error, 1u);
     // gates of the chosen, in 64 bits but for the sum over all experts
     double g = id < 0 ? 0. : score_of(a, l, most, a.renorm ? 1. : (double)z);
     if (a.renorm) {
