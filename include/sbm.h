@@ -547,23 +547,30 @@ int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks
  * A block with a NaN or an infinity has scale NaN (byte 255) and zero codes.  The
  * mean of squares is summed in 64 bits; 16-bit results are computed in 32 bits, 8-bit
  * ones in 64.
- *   x:        fp16 (bf16 with SBM_F_IN_BF16, fp32 with SBM_F_IN_F32): row i at
- *             x + i * x_stride elements
- *   gates:    device fp32 [n_tokens x k], or NULL with k = 1: a gate of one
- *   residual: fp16 (bf16 / fp32 with SBM_F_RESIDUAL_F32), or NULL: zeros
- *   weight:   [dim] fp16 (bf16), or NULL: ones
- *   residual_out: of residual's type, may be residual itself (with its stride), or
- *             NULL: not written
- *   out:      fp16 (bf16), or bytes with SBM_F_OUT_FP8; with k = repeat = 1 it may be
- *             x itself (same type and stride)
- *   scales:   [n_tokens * repeat x ceil(dim / scale_block)] fp32 (scale_block 0: one a row) or
- *             bytes (32); NULL without SBM_F_OUT_FP8
- * Otherwise no output overlaps an input or another output.  dim 1..32768, any
- * alignment of rows that their elements have, k and repeat 1..64. */
-int sbm_add_rms_norm(const void* x, int64_t x_stride, const float* gates, int32_t k, const void* residual,
-                     int64_t residual_stride, const uint16_t* weight, double eps, int32_t n_tokens, int32_t dim,
-                     void* residual_out, int64_t residual_out_stride, void* out, int64_t out_stride, int32_t repeat,
-                     void* scales, int32_t scale_block, uint32_t flags, void* stream);
+ * No output overlaps an input or another output, but for residual_out = residual (with its stride)
+ * and, with k = repeat = 1, out = x (of the same type and stride). */
+typedef struct {
+  const void* x;            /* fp16 (bf16 with SBM_F_IN_BF16, fp32 with SBM_F_IN_F32): row i at x + i * x_stride elements */
+  int64_t x_stride;
+  const float* gates;       /* device fp32 [n_tokens x k], or NULL with k = 1: a gate of one */
+  const void* residual;     /* fp16 (bf16; fp32 with SBM_F_RESIDUAL_F32), or NULL: zeros */
+  int64_t residual_stride;
+  const uint16_t* weight;   /* [dim] fp16 (bf16), or NULL: ones */
+  void* residual_out;       /* of residual's type, or NULL: not written */
+  int64_t residual_out_stride;
+  void* out;                /* fp16 (bf16), bytes with SBM_F_OUT_FP8 */
+  int64_t out_stride;
+  void* scales;             /* [n_tokens * repeat x ceil(dim / scale_block)] fp32 (scale_block 0: one a row) or bytes (32); NULL
+                               without SBM_F_OUT_FP8 */
+  double eps;               /* not negative */
+  int32_t n_tokens;
+  int32_t dim;              /* 1..32768; rows have any alignment that their elements have */
+  int32_t k, repeat;        /* 1..64 */
+  int32_t scale_block;      /* 0, 32 or 128; 0 without SBM_F_OUT_FP8 */
+  uint32_t flags;
+} sbm_norm_args;
+
+int sbm_add_rms_norm(const sbm_norm_args* args, void* stream);
 
 /* Routing: each token's k experts and their gates, from the router's logits l.
  *   s = softmax(l), or 1 / (1 + e^-l) with SBM_F_SIGMOID
@@ -580,16 +587,26 @@ int sbm_add_rms_norm(const void* x, int64_t x_stride, const float* gates, int32_
  * is counted in `error` (device uint32 that the caller zeroes, may be NULL).  The
  * expert calls leave the rows of id -1 out, and sbm_add_rms_norm leaves them out of
  * the sum.
- *   logits: fp16 (bf16 with SBM_F_IN_BF16, fp32 with SBM_F_IN_F32), token t at logits +
- *           t * row_stride elements;  bias: device fp32 [n_experts] or NULL
- *   requests: device int32 [n_tokens] (a step plan's) or NULL
- *   ids:    device int32 [n_tokens x k];  gates: device fp32 [n_tokens x k]
- * n_experts 1..4096, k 1..32 and at most the experts of top_groups groups, n_groups
- * a divisor of n_experts up to 64.  No output overlaps an input or another output. */
-int sbm_moe_route(const void* logits, int64_t row_stride, const float* bias, const int32_t* requests,
-                  int32_t n_tokens, int32_t n_experts, int32_t k, int32_t n_groups, int32_t top_groups,
-                  int32_t group_best, float scale, int32_t* ids, float* gates, uint32_t flags, uint32_t* error,
-                  void* stream);
+ * No output overlaps an input or another output. */
+typedef struct {
+  const void* logits;       /* fp16 (bf16 with SBM_F_IN_BF16, fp32 with SBM_F_IN_F32): token t at logits + t * row_stride elements */
+  int64_t row_stride;
+  const float* bias;        /* device fp32 [n_experts] or NULL */
+  const int32_t* requests;  /* device int32 [n_tokens] (a step plan's) or NULL */
+  int32_t* ids;             /* device int32 [n_tokens x k] */
+  float* gates;             /* device fp32 [n_tokens x k] */
+  uint32_t* error;
+  float scale;              /* finite */
+  int32_t n_tokens;
+  int32_t n_experts;        /* 1..4096 */
+  int32_t k;                /* 1..32, at most the experts of top_groups groups */
+  int32_t n_groups;         /* a divisor of n_experts up to 64 */
+  int32_t top_groups;
+  int32_t group_best;       /* 1 or 2 */
+  uint32_t flags;
+} sbm_route_args;
+
+int sbm_moe_route(const sbm_route_args* args, void* stream);
 
 /* Workspace bytes of sbm_sample, enough for fewer rows and a shorter vocabulary
  * too; 0 for sizes that it does not take. */
@@ -610,17 +627,27 @@ size_t sbm_sample_workspace_bytes(int32_t n_rows, int32_t vocab);
  * nothing above -inf, with a negative or NaN temperature or a NaN among its numbers
  * gets token -1, logprob NaN, and is counted in `error` (device uint32 that the caller
  * zeroes, may be NULL).
- *   logits:  fp16 (bf16 with SBM_F_IN_BF16, fp32 with SBM_F_IN_F32), row r at logits +
- *            r * row_stride elements;  vocab 1..2^20
- *   uniforms: device fp32 [n_rows];  temperature, top_p, min_p: device fp32 [n_rows], top_k:
- *            device int32 [n_rows]; each of the four may be NULL (1, not applied)
- *   tokens:  device int32 [n_rows];  logprobs: device fp32 [n_rows] or NULL
- *   workspace: device, 16-byte aligned, sbm_sample_workspace_bytes(n_rows, vocab) bytes or
- *            more, with anything in it (calls that share one must not overlap)
  * No output overlaps an input or another output. */
-int sbm_sample(const void* logits, int64_t row_stride, int32_t n_rows, int32_t vocab, const float* uniforms,
-               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
-               float* logprobs, uint32_t flags, void* workspace, size_t workspace_bytes, uint32_t* error, void* stream);
+typedef struct {
+  const void* logits;       /* fp16 (bf16 with SBM_F_IN_BF16, fp32 with SBM_F_IN_F32): row r at logits + r * row_stride elements */
+  int64_t row_stride;
+  const float* uniforms;    /* device fp32 [n_rows] */
+  const float* temperature; /* device fp32 [n_rows], or NULL: 1 */
+  const int32_t* top_k;     /* device int32 [n_rows], or NULL: not applied */
+  const float* top_p;       /* device fp32 [n_rows], or NULL: not applied */
+  const float* min_p;       /* the same */
+  int32_t* tokens;          /* device int32 [n_rows] */
+  float* logprobs;          /* device fp32 [n_rows] or NULL */
+  void* workspace;          /* device, 16-byte aligned, with anything in it (calls that share one must not overlap) */
+  size_t workspace_bytes;   /* sbm_sample_workspace_bytes(n_rows, vocab) or more */
+  uint32_t* error;
+  int32_t n_rows;
+  int32_t vocab;            /* 1..2^20 */
+  uint32_t flags;
+  uint32_t reserved;
+} sbm_sample_args;
+
+int sbm_sample(const sbm_sample_args* args, void* stream);
 
 /* ------------------------------------------- synthetic stack generation */
 /* The QMoE page's c2048 stack (1.6T parameters, under 160 GB at ~0.8 bit per

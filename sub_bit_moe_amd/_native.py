@@ -59,6 +59,26 @@ class Heads(C.Structure):
 
 P = C.c_void_p
 I = C.c_int32
+
+
+class NormArgs(C.Structure):
+    _fields_ = [("x", P), ("x_stride", C.c_int64), ("gates", P), ("residual", P), ("residual_stride", C.c_int64), ("weight", P),
+                ("residual_out", P), ("residual_out_stride", C.c_int64), ("out", P), ("out_stride", C.c_int64), ("scales", P),
+                ("eps", C.c_double), ("n_tokens", I), ("dim", I), ("k", I), ("repeat", I), ("scale_block", I), ("flags", C.c_uint32)]
+
+
+class RouteArgs(C.Structure):
+    _fields_ = [("logits", P), ("row_stride", C.c_int64), ("bias", P), ("requests", P), ("ids", P), ("gates", P), ("error", P),
+                ("scale", C.c_float), ("n_tokens", I), ("n_experts", I), ("k", I), ("n_groups", I), ("top_groups", I),
+                ("group_best", I), ("flags", C.c_uint32)]
+
+
+class SampleArgs(C.Structure):
+    _fields_ = [("logits", P), ("row_stride", C.c_int64), ("uniforms", P), ("temperature", P), ("top_k", P), ("top_p", P), ("min_p", P),
+                ("tokens", P), ("logprobs", P), ("workspace", P), ("workspace_bytes", C.c_size_t), ("error", P), ("n_rows", I),
+                ("vocab", I), ("flags", C.c_uint32), ("reserved", C.c_uint32)]
+
+
 _SIGS = {
     "sbm_last_error": (C.c_char_p, []),
     "sbm_version": (C.c_char_p, []),
@@ -96,11 +116,10 @@ _SIGS = {
     "sbm_attention_kv4_workspace_bytes": (C.c_size_t, [I, I, I, I, I]),
     "sbm_attention_kv4": (C.c_int, [P, P, I, I, P, I, P, P, I, I, I, I, I, C.c_float, P, P, C.c_uint32, P, C.c_size_t,
                                     P, P]),
-    "sbm_add_rms_norm": (C.c_int, [P, C.c_int64, P, I, P, C.c_int64, P, C.c_double, I, I, P, C.c_int64, P, C.c_int64, I, P, I,
-                                   C.c_uint32, P]),
-    "sbm_moe_route": (C.c_int, [P, C.c_int64, P, P, I, I, I, I, I, I, C.c_float, P, P, C.c_uint32, P, P]),
+    "sbm_add_rms_norm": (C.c_int, [P, P]),
+    "sbm_moe_route": (C.c_int, [P, P]),
     "sbm_sample_workspace_bytes": (C.c_size_t, [I, I]),
-    "sbm_sample": (C.c_int, [P, C.c_int64, I, I, P, P, P, P, P, P, P, C.c_uint32, P, C.c_size_t, P, P]),
+    "sbm_sample": (C.c_int, [P, P]),
     "sbm_trie_words": (C.c_size_t, []),
     "sbm_build_trie": (C.c_int, [P, P]),
     "sbm_gen_count": (C.c_int, [C.c_uint64, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,

@@ -340,10 +340,10 @@ void launch_norm(const NormArgs& a, int32_t n_tokens, uint32_t flags, hipStream_
 
 using namespace sbm;
 
-extern "C" int sbm_add_rms_norm(const void* x, int64_t x_stride, const float* gates, int32_t k, const void* residual,
-                                int64_t residual_stride, const uint16_t* weight, double eps, int32_t n_tokens, int32_t dim,
-                                void* residual_out, int64_t residual_out_stride, void* out, int64_t out_stride,
-                                int32_t repeat, void* scales, int32_t scale_block, uint32_t flags, void* stream) {
+extern "C" int sbm_add_rms_norm(const sbm_norm_args* args, void* stream) {
+  if (!args) return fail(SBM_EINVAL, "null pointer");
+  const auto [x, x_stride, gates, residual, residual_stride, weight, residual_out, residual_out_stride, out, out_stride, scales, eps,
+              n_tokens, dim, k, repeat, scale_block, flags] = *args;
   if (flags & ~(SBM_F_IN_BF16 | SBM_F_IN_F32 | SBM_F_RESIDUAL_F32 | SBM_F_OUT_FP8))
     return fail(SBM_EINVAL, "unknown flags 0x%x", flags);
   if (n_tokens < 0 || dim < 1 || dim > kMostDim)

@@ -453,10 +453,10 @@ bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
 
 using namespace sbm;
 
-extern "C" int sbm_moe_route(const void* logits, int64_t row_stride, const float* bias, const int32_t* requests,
-                             int32_t n_tokens, int32_t n_experts, int32_t k, int32_t n_groups, int32_t top_groups,
-                             int32_t group_best, float scale, int32_t* ids, float* gates, uint32_t flags, uint32_t* error,
-                             void* stream) {
+extern "C" int sbm_moe_route(const sbm_route_args* args, void* stream) {
+  if (!args) return fail(SBM_EINVAL, "null pointer");
+  const auto [logits, row_stride, bias, requests, ids, gates, error, scale, n_tokens, n_experts, k, n_groups, top_groups, group_best,
+              flags] = *args;
   if (flags & ~(SBM_F_IN_BF16 | SBM_F_IN_F32 | SBM_F_SIGMOID | SBM_F_RENORM)) return fail(SBM_EINVAL, "unknown flags 0x%x", flags);
   if ((flags & SBM_F_IN_BF16) && (flags & SBM_F_IN_F32)) return fail(SBM_EINVAL, "logits of two types");
   if (n_tokens < 0 || n_experts < 1 || n_experts > kMostExperts)

@@ -753,9 +753,11 @@ size_t sbm_sample_workspace_bytes(int32_t n_rows, int32_t vocab) {
   return parts_of(1, vocab) > 1 ? std::max<size_t>((size_t)std::min(n_rows, kFull / 2) * (size_t)row_space(vocab), 256) : 256;
 }
 
-int sbm_sample(const void* logits, int64_t row_stride, int32_t n_rows, int32_t vocab, const float* uniforms,
-               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
-               float* logprobs, uint32_t flags, void* workspace, size_t workspace_bytes, uint32_t* error, void* stream) {
+int sbm_sample(const sbm_sample_args* args, void* stream) {
+  if (!args) return fail(SBM_EINVAL, "null pointer");
+  const auto [logits, row_stride, uniforms, temperature, top_k, top_p, min_p, tokens, logprobs, workspace, workspace_bytes, error, n_rows,
+              vocab, flags, reserved] = *args;
+  if (reserved) return fail(SBM_EINVAL, "reserved must be 0");
   if (flags & ~(SBM_F_IN_BF16 | SBM_F_IN_F32)) return fail(SBM_EINVAL, "unknown flags 0x%x", flags);
   if ((flags & SBM_F_IN_BF16) && (flags & SBM_F_IN_F32)) return fail(SBM_EINVAL, "logits of two types");
   if (n_rows < 0 || vocab < 1 || vocab > kMostVocab)
