@@ -16,10 +16,10 @@ __device__ __forceinline__ float to_f32(uint16_t u) {
 // 64 bits to 32 with what those cannot hold gathered in their lowest bit (round to odd): a further rounding to fewer
 // bits then sees on which side of a border the value was.
 __device__ __forceinline__ float to_odd(double y) {
-  uint64_t b = __builtin_bit_cast(uint64_t, y);
-  const uint32_t low = (uint32_t)b & 0x1FFFFFFFu;
-  b = (b & ~0x1FFFFFFFull) | (low ? 0x20000000u : 0u);
-  return (float)__builtin_bit_cast(double, b);
+  constexpr uint32_t kBelow = 0x1FFFFFFFu;
+  const uint64_t b = __builtin_bit_cast(uint64_t, y);
+  const uint32_t low = (uint32_t)b, carry = (low & kBelow) + kBelow;       // into the lowest bit that stays, if any below it is set
+  return (float)__builtin_bit_cast(double, b >> 32 << 32 | ((low | carry) & ~kBelow));
 }
 
 // One rounding to T.
