@@ -826,6 +826,8 @@ def _norm(x, weight, residual, gates, eps, repeat, out, residual_out, dtype, str
                 po, so = pr, sr
         if po == 0:
             po, so = _rows(residual_out, "residual_out", of, at, held)
+    if repeat < 1:
+        raise ValueError(f"repeat must be 1 or more, not {repeat}")
     rows = T * repeat
     if block is None:
         kind = dtype

@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kMostDim = 32768;
 constexpr int kMostThreads = 1024;
+constexpr int kMostGrid = 1 << 21;                // a launch has fewer than 2^32 threads
 constexpr int kFewThreads = 256;               // of a workgroup that has several rows
 
 struct NormArgs {
@@ -23,6 +24,7 @@ struct NormArgs {
   void* out;
   void* scales;
   int64_t x_stride, r_stride, ro_stride, o_stride;      // elements
+  int64_t first;                                        // the launch's first row
   double eps;
   int32_t dim, k, repeat, block;                        // block: elements that share a scale, the row's if `whole`
   int32_t n_tokens, lanes;                              // lanes: threads of a row
@@ -141,9 +143,9 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
   __shared__ double s_sum[kMostThreads / 64];
   // a workgroup has one row, or (kFew) several of fewer threads than a wave each
   const int G = kFew ? a.lanes : (int)blockDim.x, tid = kFew ? (int)threadIdx.x & (G - 1) : (int)threadIdx.x;
-  int64_t t = blockIdx.x;
+  int64_t t = a.first + blockIdx.x;
   if constexpr (kFew) {
-    t = t * (kFewThreads / G) + threadIdx.x / (uint32_t)G;
+    t = a.first + (int64_t)blockIdx.x * (kFewThreads / G) + threadIdx.x / (uint32_t)G;
     if (t >= a.n_tokens) return;
   }
   C h[kN][8];
@@ -310,12 +312,15 @@ void launch_norm(NormArgs a, int32_t n_tokens, hipStream_t s) {
   if (chunks <= 32)
     for (a.lanes = k8 ? 16 : 8; a.lanes < chunks;) a.lanes *= 2;
   const int rows = a.lanes < 64 ? kFewThreads / a.lanes : 1;
-  const dim3 grid((unsigned)(((int64_t)n_tokens + rows - 1) / rows)), block((unsigned)(a.lanes * rows));
+  const dim3 block((unsigned)(a.lanes * rows));
+  for (; a.first < n_tokens; a.first += (int64_t)kMostGrid * rows) {
+    const dim3 grid((unsigned)std::min<int64_t>((n_tokens - a.first + rows - 1) / rows, kMostGrid));
 #define SBM_NORM(N, FEW) hipLaunchKernelGGL((norm_kernel<T, kXF, kRF, k8, N, FEW>), grid, block, 0, s, a)
-  if (rows > 1) SBM_NORM(1, true);
-  else if (n == 1) SBM_NORM(1, false);
-  else if (n == 2) SBM_NORM(2, false);
-  else SBM_NORM(4, false);
+    if (rows > 1) SBM_NORM(1, true);
+    else if (n == 1) SBM_NORM(1, false);
+    else if (n == 2) SBM_NORM(2, false);
+    else SBM_NORM(4, false);
+  }
 #undef SBM_NORM
 }
 
@@ -383,7 +388,7 @@ extern "C" int sbm_add_rms_norm(const sbm_norm_args* args, void* stream) {
       if (&other < &o && overlap(o, other)) return fail(SBM_EINVAL, "outputs overlap");
   }
   const NormArgs a{x, residual, residual_out, weight, gates, out, scales, x_stride, residual_stride, residual_out_stride,
-                   out_stride, eps, dim, k, repeat, block, n_tokens, 0, scale_block == 0, scale_block == 32};
+                   out_stride, 0, eps, dim, k, repeat, block, n_tokens, 0, scale_block == 0, scale_block == 32};
   if (flags & SBM_F_IN_BF16) launch_norm<__bf16>(a, n_tokens, flags, (hipStream_t)stream);
   else launch_norm<_Float16>(a, n_tokens, flags, (hipStream_t)stream);
   const hipError_t e = hipGetLastError();

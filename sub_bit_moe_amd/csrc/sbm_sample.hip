@@ -35,6 +35,7 @@ struct SampleArgs {
   uint32_t* error;
   uint8_t* workspace;
   int64_t ws_row;                            // workspace bytes of a row
+  int64_t first;                             // the first row of a launch of sample_row_kernel
   int32_t vocab, parts;
 };
 
@@ -459,13 +460,14 @@ struct Reached {
 
 // Where `target` tokens, or units of weight (by_weight; 0: top_p of all of it), are reached among those of orders base .. base + last
 // up to `end`; all of them where they are fewer.  The stretch is cut into 1024 equal parts, each with its tokens and (sums) their
-// weight, and the part in which the end is into 1024 again, until a wave can put a part's tokens in order.
+// weight, and the part in which the end is into 1024 again, until a wave can put a part's tokens in order: after six times at most,
+// since an order has 52 bits.
 template <typename T>
 __device__ Reached reach(const Source<T>& from, const Row& f, uint64_t base, uint64_t last, bool by_weight, bool sums, uint64_t target,
                          uint64_t end, Shared& s) {
   const uint32_t tid = threadIdx.x;
   uint64_t sum_before = 0;
-  for (bool first = true;; first = false) {
+  for (int level = 0; level < 6; ++level) {
     const int shift = max(54 - __builtin_clzll(last | 1), 0);
     __syncthreads();
     s.sums[tid] = 0;
@@ -486,7 +488,7 @@ __device__ Reached reach(const Source<T>& from, const Row& f, uint64_t base, uin
     uint64_t total = 0, before = 0;
     if (!by_weight) place = scan(count, s, &all);
     if (sums) before = scan(sum, s, &total);
-    if (first) {
+    if (level == 0) {
       if (by_weight && target == 0) target = part_of(f, total);
       if (!by_weight && all < target) return Reached{end, total};
     }
@@ -506,7 +508,9 @@ __device__ Reached reach(const Source<T>& from, const Row& f, uint64_t base, uin
     if (there > 64) continue;
     for (uint32_t i = tid; i < from.n; i += kSThreads) {
       const uint64_t o = from[i];
-      if (o <= end && o - base <= last) s.few[atomicAdd(&s.n_few, 1u)] = o;
+      if (o > end || o - base > last) continue;
+      const uint32_t at = atomicAdd(&s.n_few, 1u);
+      if (at < 64) s.few[at] = o;
     }
     __syncthreads();
     if (tid < 64) {
@@ -517,6 +521,7 @@ __device__ Reached reach(const Source<T>& from, const Row& f, uint64_t base, uin
     __syncthreads();
     return Reached{s.found[0], s.found[1]};
   }
+  return Reached{base, sum_before};
 }
 
 __device__ void refuse(const SampleArgs& a, int64_t r) {
@@ -612,7 +617,7 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
 template <typename T, int kHold>
 __global__ __launch_bounds__(kSThreads) void sample_row_kernel(SampleArgs a) {
   __shared__ Shared s;
-  const int64_t r = blockIdx.x;
+  const int64_t r = a.first + blockIdx.x;
   Row f = row_of(a, r, __is_same(T, float) ? 4 : 2);
   const Tiles<T, kHold> tiles(f, a, 0);
   const float most = largest(tiles, s);
@@ -721,14 +726,20 @@ int parts_of(int32_t n_rows, int32_t vocab) {
   return std::max(1, std::min({(int)kMostParts, kFull / std::max(n_rows, 1), tiles / kSWaves}));
 }
 
+// A launch has fewer than 2^32 threads.
+constexpr int kMostRows = 1 << 21;
+
 template <typename T>
-void launch_sample(const SampleArgs& a, int32_t n_rows, hipStream_t s) {
-  const dim3 grid((unsigned)(n_rows * a.parts)), block(kSThreads);
-  if (a.vocab <= kHeld * kSWaves * kTile) {
-    hipLaunchKernelGGL((sample_row_kernel<T, kHeld>), grid, block, 0, s, a);
-  } else if (a.parts == 1) {
-    hipLaunchKernelGGL((sample_row_kernel<T, 0>), grid, block, 0, s, a);
+void launch_sample(SampleArgs a, int32_t n_rows, hipStream_t s) {
+  const dim3 block(kSThreads);
+  if (a.parts == 1) {
+    for (; a.first < n_rows; a.first += kMostRows) {
+      const dim3 grid((unsigned)std::min<int64_t>(n_rows - a.first, kMostRows));
+      if (a.vocab <= kHeld * kSWaves * kTile) hipLaunchKernelGGL((sample_row_kernel<T, kHeld>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((sample_row_kernel<T, 0>), grid, block, 0, s, a);
+    }
   } else {
+    const dim3 grid((unsigned)(n_rows * a.parts));
     hipLaunchKernelGGL((sample_max_kernel<T>), grid, block, 0, s, a);
     hipLaunchKernelGGL((sample_bins_kernel<T>), grid, block, 0, s, a);
     hipLaunchKernelGGL((sample_draw_kernel<T>), grid, block, 0, s, a);
@@ -784,7 +795,7 @@ int sbm_sample(const sbm_sample_args* args, void* stream) {
       if (&other < &o && overlap(o.p, o.bytes, other.p, other.bytes)) return fail(SBM_EINVAL, "outputs overlap");
   }
   const SampleArgs a{logits, row_stride, uniforms, temperature, top_p, min_p, top_k, tokens, logprobs, error, (uint8_t*)workspace,
-                     row_space(vocab), vocab, parts_of(n_rows, vocab)};
+                     row_space(vocab), 0, vocab, parts_of(n_rows, vocab)};
   if (flags & SBM_F_IN_F32) launch_sample<float>(a, n_rows, (hipStream_t)stream);
   else if (flags & SBM_F_IN_BF16) launch_sample<__bf16>(a, n_rows, (hipStream_t)stream);
   else launch_sample<_Float16>(a, n_rows, (hipStream_t)stream);

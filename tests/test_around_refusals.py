@@ -105,6 +105,7 @@ def test_front_end():
             (lambda: api.add_rms_norm(f), ValueError, "dtype must be given"),
             (lambda: api.add_rms_norm(x.double()), TypeError, "float16 or bfloat16"),
             (lambda: api.add_rms_norm(x, gates=torch.zeros(3, 2)), ValueError, "gates"),
+            (lambda: api.add_rms_norm(x, repeat=0), ValueError, "on the GPU|repeat"),
             (lambda: api.moe_route(f[0], 1), ValueError, "logits"),
             (lambda: api.moe_route(f.double(), 1), TypeError, "float32"),
             (lambda: api.moe_route(f, 1), ValueError, "on the GPU"),

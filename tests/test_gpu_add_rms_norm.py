@@ -184,6 +184,15 @@ def test_no_rows_and_many_rows(dev):
     _check(dev, *R.norm_case(rng, 70001, 16, dtype="fp16", gates=False), dtype="fp16")
 
 
+def test_more_rows_than_a_launch_has(dev):
+    from sub_bit_moe_amd import api
+    for n, D in (((1 << 21) + 3, 512), ((1 << 26) + 37, 8)):            # a row to a workgroup; 32 to one
+        x = torch.ones(n, D, dtype=torch.float16, device=dev)
+        x[n // 2:] = -2.0
+        out, _ = api.add_rms_norm(x, eps=0.0)
+        assert (out[:n // 2] == 1).all() and (out[n // 2:] == -1).all()
+
+
 def test_offsets_past_32_bits(dev):
     from sub_bit_moe_amd import api
     x = torch.zeros(140000, 16400, dtype=torch.bfloat16, device=dev)          # 4.6 GB

@@ -194,6 +194,18 @@ def test_offsets_past_32_bits(dev):
     assert torch.equal(got[-1:], api.sample(l[-1:].clone(), u[-1:])) and (got[:-1] == 125000).all()
 
 
+def test_more_rows_than_a_launch_has(dev):
+    from sub_bit_moe_amd import api
+    n = (1 << 22) + 5
+    l = torch.zeros(n, 2, device=dev)
+    l[::3, 1] = 50.0
+    got = api.sample(l, torch.full((n,), 0.5, device=dev))              # a tie's second half; the likely one
+    assert (got == 1).all()
+    l[::3, 0] = 100.0
+    got = api.sample(l, torch.full((n,), 0.5, device=dev))
+    assert (got[::3] == 0).all() and (got[1::3] == 1).all() and (got[2::3] == 1).all()
+
+
 def test_captured_on_a_stream_of_its_own_and_replayed(dev):
     from sub_bit_moe_amd import api
     for rows, vocab in ((3, 70000), (40, 3000)):
