@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kMostDim = 32768;
 constexpr int kMostThreads = 1024;
-constexpr int kMostGrid = 1 << 21;                // a launch has fewer than 2^32 threads
+constexpr int kMostGrid = 1 << 21;             // a launch has fewer than 2^32 threads
 constexpr int kFewThreads = 256;               // of a workgroup that has several rows
 
 struct NormArgs {
@@ -76,7 +76,6 @@ __device__ __forceinline__ void store_raw(void* p, const void* x, int n) {
   }
 }
 
-
 struct Sum {
   __device__ double operator()(double a, double b) const { return a + b; }
 };
@@ -133,10 +132,15 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int64_t t, int d0
   }
 }
 
+//   h = residual + sum over e of gate_e x_e,  residual_out = h rounded,  out = h (mean(h^2) + eps)^-1/2 weight
+// The norm takes h as it was before its rounding.  8-bit results: out / scale to e4m3, the scale from a block's largest magnitude.
 // A workgroup holds a row in its registers, kN times eight elements a thread: everything is read once and written once.  The
 // mean of squares is summed in 64 bits (f64 runs at the rate of unpacked f32 here), so that no row of finite numbers
 // overflows it; what becomes 8 bits is computed in 64 bits throughout (C), so that a code beside the border of two does not
 // depend on the order of a sum.
+// What bounds it: memory for prompts (8191 x 4096 with residual in and out, 268 MB: 50.5 us, 5.3 TB/s; vector units busy for 68 %);
+// for 8 bits with bytes of scales the 64-bit arithmetic, near to memory (4096 x 8192, 236 MB: 58 us, 4.1 TB/s, vector units busy for
+// 82 %); for few tokens one row's latency (3.6 us a token alone, 5.1 us 64 tokens of two experts; 9 us with the host's call).
 template <typename T, bool kXF, bool kRF, bool k8, int kN, bool kFew>
 __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
   using C = std::conditional_t<k8, double, float>;
@@ -307,7 +311,7 @@ void launch_norm(NormArgs a, int32_t n_tokens, hipStream_t s) {
   // sixteen from 256 threads on, so that more rows are in one CU (8192 rows of 4096: 55 instead of 61 us, 2080: 38 and 39); 16-bit
   // ones do not (4096: 54 instead of 50).
   const int chunks = (a.dim + 7) / 8, n = chunks > 2048 ? 4 : chunks > (k8 ? 256 : 1024) ? 2 : 1;
-  // rows of up to 256 elements share a wave; 16 lanes at least have a block of 128
+  // rows of up to 256 elements share a wave (65536 rows of 64: 10 instead of 34 us); 16 lanes at least have a block of 128
   a.lanes = ((chunks + n - 1) / n + 63) / 64 * 64;
   if (chunks <= 32)
     for (a.lanes = k8 ? 16 : 8; a.lanes < chunks;) a.lanes *= 2;
@@ -370,7 +374,7 @@ extern "C" int sbm_add_rms_norm(const sbm_norm_args* args, void* stream) {
   const int32_t block = scale_block ? scale_block : dim;
   const int64_t xb = xf ? 4 : 2, rb = rf ? 4 : 2, ob = f8 ? 1 : 2, sb = scale_block == 32 ? 1 : 4;
   const int64_t n_blocks = (dim + block - 1) / block, T = n_tokens;
-  if (((uintptr_t)x | (uintptr_t)0) % xb || (uintptr_t)residual % rb || (uintptr_t)residual_out % rb ||
+  if ((uintptr_t)x % xb || (uintptr_t)residual % rb || (uintptr_t)residual_out % rb ||
       (uintptr_t)weight % 2 || (uintptr_t)out % ob || (f8 && (uintptr_t)scales % sb) || (uintptr_t)gates % 4)
     return fail(SBM_EINVAL, "misaligned array");
   const Rows ins[] = {{x, T * k, dim * xb, x_stride * xb}, {residual, T, dim * rb, residual_stride * rb},

@@ -47,12 +47,15 @@ __device__ __forceinline__ float inverse_root(float x) {
 __device__ __forceinline__ float fused(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
 __device__ __forceinline__ double fused(double a, double b, double c) { return __builtin_fma(a, b, c); }
 
-// 2^x, to 4e-14 of itself: x's whole part goes to the exponent, 2^f for the rest, |f| <= 1/2, is a polynomial of degree 9 that
-// interpolates it at Chebyshev's points (3.7e-14 off at most) and is 1 at 0.  x below 1000; below -1000 it stays 2^-1000, for -inf
-// and NaN too.  f64 runs at the rate of unpacked f32 here.
-__device__ __forceinline__ double exp2_f64(double x) {
-  x = fmax(x, -1000.);
-  const double n = x + 0x1.8p52, y = x - (n - 0x1.8p52);             // n's low bits are x's nearest whole number
+// The 32-bit parts of 64.
+using Halves = uint32_t __attribute__((ext_vector_type(2)));
+
+// 2^(x by), to 4e-14 of itself, for x by within -1000 .. 1000: its whole part goes to the exponent, 2^f for the rest, |f| <= 1/2, is
+// a polynomial of degree 9 that interpolates it at Chebyshev's points (3.7e-14 off at most) and is 1 at 0.  f64 runs at the rate of
+// unpacked f32 here.
+__device__ __forceinline__ double exp2_f64(double x, double by) {
+  // n's low bits are the nearest whole number
+  const double n = __builtin_fma(x, by, 0x1.8p52), y = __builtin_fma(x, by, -(n - 0x1.8p52));
   // as one block, since the compiler would copy each coefficient into the register of the sum, an instruction more
   double p;
   asm("v_fma_f64 %0, %2, %1, %3\n\tv_fma_f64 %0, %0, %1, %4\n\tv_fma_f64 %0, %0, %1, %5\n\tv_fma_f64 %0, %0, %1, %6\n\t"
@@ -62,9 +65,12 @@ __device__ __forceinline__ double exp2_f64(double x) {
       : "v"(y), "v"(0x1.b63880a30e9ffp-24), "s"(0x1.63d136366db24p-20), "s"(0x1.ffcb9515a8016p-17), "s"(0x1.4308ac85aa947p-13),
         "s"(0x1.5d87fe86fe88ep-10), "s"(0x1.3b2ab7181b755p-7), "s"(0x1.c6b08d7047e52p-5), "s"(0x1.ebfbdff823cedp-3),
         "s"(0x1.62e42fefa39efp-1));
-  const uint64_t u = __builtin_bit_cast(uint64_t, p);
-  return __builtin_bit_cast(double, (uint64_t)((uint32_t)(u >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, n) << 20)) << 32 | (uint32_t)u);
+  Halves u = __builtin_bit_cast(Halves, p);
+  u[1] += __builtin_bit_cast(Halves, n)[0] << 20;
+  return __builtin_bit_cast(double, u);
 }
+// 2^x; below -1000 it stays 2^-1000, for -inf and NaN too.
+__device__ __forceinline__ double exp2_f64(double x) { return exp2_f64(fmax(x, -1000.), 1.); }
 
 // 1 / x of normal numbers: the hardware's estimate and two of Newton's steps.
 __device__ __forceinline__ double inverse(double x) {

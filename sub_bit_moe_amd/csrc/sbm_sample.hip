@@ -18,8 +18,8 @@ constexpr int kMostTiles = kMostVocab / kTile;
 constexpr int kBins = 4096;                  // of the distance below the largest logit: 128 to a doubling, from 2^-12 on
 constexpr int kDigits = 1024;                // ten bits of an order at a time
 constexpr int kList = 6144;                  // tokens of a row that are put in order in LDS
-constexpr int kHeld = 2;                     // tiles of a wave that stay in its registers
-constexpr int kBeside = 4;                   // logits of a lane whose weights are computed beside one another
+constexpr int kHeld = 2;                     // tiles of a wave that stay in its registers: a workgroup's 32768 tokens
+constexpr int kBeside = 4;                   // logits of a lane that are passed over together (2 and 8 take the same time)
 constexpr int kGroup = kPer;                 // neighbours of which one counts for a top_k
 constexpr int kMostGroups = 2048;
 constexpr int kMostParts = 64;               // workgroups of a row
@@ -61,8 +61,13 @@ constexpr int64_t row_space(int vocab) { return ((int64_t)sizeof(RowSpace) + 8 *
 // not below the vocabulary (or 2048), 2^-42 for the largest.
 struct Unit {
   double magic;                              // 2^52 units: the low bits of magic + w are w in units, rounded
+  // w in units above what none() is
+  __device__ __forceinline__ uint64_t above(double w) const { return __builtin_bit_cast(uint64_t, w + magic); }
+  __device__ __forceinline__ uint64_t none() const { return (uint64_t)__double2hiint(magic) << 32; }
   __device__ __forceinline__ uint64_t operator()(double w) const {
-    return __builtin_bit_cast(uint64_t, w + magic) - __builtin_bit_cast(uint64_t, magic);
+    Halves u = __builtin_bit_cast(Halves, w + magic);
+    u[1] -= (uint32_t)__double2hiint(magic);
+    return __builtin_bit_cast(uint64_t, u);
   }
 };
 
@@ -84,7 +89,7 @@ __device__ __forceinline__ float begin_of(uint32_t bin) {
 // A row's parameters.
 struct Row {
   const char* at;
-  double most, slope;                        // the largest logit; log2(e) / temperature
+  double most, slope, least;                 // the largest logit; log2(e) / temperature; -1000 / slope
   Unit units;
   float u, top_p, min_p, temperature;
   float low;                                 // the least logit that stays by min_p; above -inf
@@ -104,14 +109,15 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t r, int bytes)
   f.bad = f.u != f.u || !(f.temperature >= 0.f) || f.top_p != f.top_p || f.min_p != f.min_p;
   f.low = -3.402823466e38f;
   f.slope = f.temperature > 0.f ? fmax(1.4426950408889634 / (double)f.temperature, 1e-300) : 0.;      // not 0 * -inf
+  f.least = f.temperature > 0.f ? -1000. / f.slope : 0.;
   f.most = 0;
   const int bits = max(32 - __builtin_clz(max((unsigned)a.vocab, 2u) - 1u), 11);
   f.units.magic = __builtin_amdgcn_ldexp(1., bits - 10);
   return f;
 }
 
-// exp((l - most) / temperature), to 4e-14 of itself.
-__device__ __forceinline__ double weight(const Row& f, float l) { return exp2_f64(((double)l - f.most) * f.slope); }
+// exp((l - most) / temperature), to 4e-14 of itself; 2^-1000, which is no unit, for what is below that.
+__device__ __forceinline__ double weight(const Row& f, float l) { return exp2_f64(fmax((double)l - f.most, f.least), f.slope); }
 
 // The least key from lo to hi at which something holds that holds from there on, hi among it: 64 places at a time.
 template <typename F>
@@ -405,7 +411,8 @@ __device__ void sum_tiles(const X& tiles, const Row& f, const Range& r, uint64_t
     uint64_t sum = 0;
     if (r.from < -3e38f) {                   // all: -inf weighs nothing
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) sum += f.units(weight(f, x[i]));
+      for (int i = 0; i < kPer; ++i) sum += f.units.above(weight(f, x[i]));
+      sum -= kPer * f.units.none();
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; i += kBeside) {
@@ -416,9 +423,9 @@ __device__ void sum_tiles(const X& tiles, const Row& f, const Range& r, uint64_t
         if (__any(top >= r.from)) {
 #pragma unroll
           for (int j = 0; j < kBeside; ++j) {
-            const uint64_t u = f.units(weight(f, x[i + j]));
-            sum += x[i + j] >= r.from ? u : 0ull;
+            sum += f.units.above(weight(f, x[i + j] >= r.from ? x[i + j] : -INFINITY));
           }
+          sum -= kBeside * f.units.none();
         }
 #pragma unroll
         for (int j = 0; j < kBeside; ++j) {
@@ -612,6 +619,18 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
 }
 
 // ------------------------------------------------------------------ kernels
+//
+// A token stays if it is among the top_k, its weight w = exp((l - most) / temperature) is min_p at least, and the weights before it
+// in falling order are below top_p of those that stay so far; drawn is the first, by index, whose running sum of the weights that stay
+// passes u of their sum.  No row is sorted: the logits' distances from the largest, in bins of 1 / 128 of a doubling, say in which bin
+// the filter ends; the tokens above stay, those of the bin are put in order in LDS, and each tile's weights are summed on the way.  The
+// draw looks at the tiles' sums and then at one tile.  So a row is read three times: largest, bins, sums (once, as long as it stays in
+// registers).
+// What bounds it: 1 x 32000 in fp16 takes 11.5 us of one workgroup's steps after one another; 64 x 131072 in bf16 three launches of
+// 4.2, 15 and 22 us, of which the vector units are busy for 42, 47 and 34 % and the rest is the launches' ends and the last workgroup
+// of a row, which puts the list in order.  256 x 150001 in fp32 takes 110 us, the time of the row of which most stays: 22 for the
+// largest (memory, 7 TB/s), 34 for the bins, 20 to 45 for the sums (18 instructions of 64 bits a weight), 8 for the rest; 200 x 50021
+// without filters 20 us, a pass over memory and one of weights.
 
 // A workgroup has a row.
 template <typename T, int kHold>
@@ -718,7 +737,9 @@ __global__ __launch_bounds__(kSThreads) void sample_draw_kernel(SampleArgs a) {
   draw<T>(f, a, r, range, s);
 }
 
-// Workgroups of a row: one where its tiles stay in their registers, or where there are rows enough to fill the card.
+// Workgroups of a row: one where its tiles stay in their registers, or where there are rows enough to fill the card (1 x 131072: 25 us
+// by eight workgroups, 61 by one; 32 x 131072: 32 and 81; at 1 x 40000, just above what registers hold, 26 and 24).  One workgroup for
+// each of the card's 256 CUs: with up to 512 (200 x 50021) 36 us instead of 22, since three launches follow instead of one.
 constexpr int kFull = 256;
 int parts_of(int32_t n_rows, int32_t vocab) {
   const int tiles = (vocab + kTile - 1) / kTile;
