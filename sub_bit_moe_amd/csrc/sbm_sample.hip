@@ -739,7 +739,8 @@ __global__ __launch_bounds__(kSThreads) void sample_draw_kernel(SampleArgs a) {
 
 // Workgroups of a row: one where its tiles stay in their registers, or where there are rows enough to fill the card (1 x 131072: 25 us
 // by eight workgroups, 61 by one; 32 x 131072: 32 and 81; at 1 x 40000, just above what registers hold, 26 and 24).  One workgroup for
-// each of the card's 256 CUs: with up to 512 (200 x 50021) 36 us instead of 22, since three launches follow instead of one.
+// each of the card's 256 CUs (64 x 131072: 128 workgroups 54 us, 256 39, 512 42; 200 x 50021 with up to 512, which is two a row and three
+// launches instead of one, 36 and 22).
 constexpr int kFull = 256;
 int parts_of(int32_t n_rows, int32_t vocab) {
   const int tiles = (vocab + kTile - 1) / kTile;
