@@ -619,10 +619,10 @@ size_t sbm_sample_workspace_bytes(int32_t n_rows, int32_t vocab);
  *   reaches top_p times theirs stays;
  *   token = the first, in the order of indices, at which the running sum of the w that
  *   stayed passes u times their sum W;   logprob = ln(w_token / W).
- * Weights are computed in 64 bits and summed as whole multiples of 2^-42, so a
+ * Weights are computed in 64 bits and summed as whole multiples of 2^-42 or less, so a
  * token does not depend on the order of a sum.  temperature 0: the largest l (the
  * lowest index of equal ones), logprob 0.  top_k <= 0, top_p >= 1, min_p <= 0: not
- * applied; top_p <= 0 and min_p >= 1 leave the first, and those equal to it; u below 0
+ * applied; top_p <= 0 leaves the first, min_p >= 1 those equal to it too; u below 0
  * is 0, from 1 on the last token that stayed.  A row with a NaN or +inf logit, with
  * nothing above -inf, with a negative or NaN temperature or a NaN among its numbers
  * gets token -1, logprob NaN, and is counted in `error` (device uint32 that the caller
