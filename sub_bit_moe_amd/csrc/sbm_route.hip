@@ -229,10 +229,10 @@ struct WaveSpace {
 // are put in order.  Choices with a bias are compared in 32 bits, with what these may be off added to the candidates; where two
 // that follow each other are nearer than that (one token in some hundred to some thousand), the candidates' choices are computed
 // in 64, as the groups' values are where two at the border are.  With more than 64 candidates the whole token is.
-// What bounds it: 16384 x 2048 in fp32 (134 MB) takes 41 us on the card, 50 from call to call (26 us of memory at its copy's rate): a
-// token's choices fill the registers, so that four waves are in a SIMD and their vector units busy for 57 %; with room for five or six
-// the registers spill (82 and 98 us), and the next token's row read ahead takes the room of a wave (67 us).  8192 x 256 in groups:
-// 20 us, the chain of steps of one token (vector units 69 %).  64 x 2048: 5.3 us, one token's latency.
+// What bounds it: 16384 x 2048 in fp32 (134 MB) takes 39 us on the card, 48.5 from call to call (26 us of memory at its copy's rate): a
+// token's choices fill the registers, so that four waves are in a SIMD and their vector units busy for 52 %; with room for five or six
+// the registers spill (82 and 98 us), the next token's row read ahead takes the room of a wave (67 us), and by way of LDS it gains
+// 5 %.  8192 x 256 in groups: 20 us, the chain of steps of one token (vector units 69 %).  64 x 2048: 4.7 us, one token's latency.
 template <typename T, int kN, bool kGroups>
 __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(RouteArgs a) {
   __shared__ WaveSpace<kN, kGroups> s_space[kRWaves];
@@ -371,10 +371,11 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
     __builtin_amdgcn_sched_barrier(0);
     // candidates
     if (a.bias) border -= off + 0x1p-22f * fabsf(border);
+    border = fmaxf(border, -3.402823466e38f);          // never -inf
     uint32_t n = 0;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const bool is = c[i] >= border && c[i] > -INFINITY;
+      const bool is = c[i] >= border;
       const uint64_t m = __ballot(is);
       if (!m) continue;
       const uint32_t at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));

@@ -627,7 +627,7 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
 // draw looks at the tiles' sums and then at one tile.  So a row is read three times: largest, bins, sums (once, as long as it stays in
 // registers).
 // What bounds it: 1 x 32000 in fp16 takes 11.5 us of one workgroup's steps after one another; 64 x 131072 in bf16 three launches of
-// 4.2, 15 and 22 us, of which the vector units are busy for 42, 47 and 34 % and the rest is the launches' ends and the last workgroup
+// 4.2, 14.4 and 20.5 us, of which the vector units are busy for 44, 46 and 35 % and the rest is the launches' ends and the last workgroup
 // of a row, which puts the list in order.  256 x 150001 in fp32 takes 110 us, the time of the row of which most stays: 22 for the
 // largest (memory, 7 TB/s), 34 for the bins, 20 to 45 for the sums (18 instructions of 64 bits a weight), 8 for the rest; 200 x 50021
 // without filters 20 us, a pass over memory and one of weights.
