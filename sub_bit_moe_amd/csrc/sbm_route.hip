@@ -240,11 +240,19 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
   WaveSpace<kN, kGroups>& s = s_space[wave];
   constexpr uint32_t kNoneBits = __is_same(T, float) ? 0xFF800000u : __is_same(T, __bf16) ? 0xFF80u : 0xFC00u;
   constexpr int kSize = __is_same(T, float) ? 4 : 2;
-  // a bias that is no number or +inf refuses the tokens that it could be chosen for
+  // The bias goes to LDS once, where four workgroups of a CU have room for it (from memory for each token: 16384 x 2048 49 us).
+  // One that is no number or +inf refuses the tokens that it could be chosen for.
+  constexpr bool kHere = !kGroups || kN < 32;
+  __shared__ alignas(16) float s_bias[kHere ? kN * 64 : 1];
   bool odd = false;
-  if (a.bias)
-    for (int e = (int)threadIdx.x & 63; e < a.n_experts; e += 64) odd = odd || !(a.bias[e] < INFINITY);
-  odd = __any(odd);
+  if (a.bias) {
+    for (int e = (int)threadIdx.x; e < (kHere ? kN * 64 : a.n_experts); e += kRThreads) {
+      const float b = e < a.n_experts ? a.bias[e] : 0.f;
+      odd = odd || !(b < INFINITY);
+      if constexpr (kHere) s_bias[e] = b;
+    }
+    odd = __syncthreads_or(odd);
+  }
   const int64_t step = (int64_t)gridDim.x * kRWaves;
   for (int64_t t = (int64_t)blockIdx.x * kRWaves + wave; t < a.n_tokens; t += step) {
     const char* row = (const char*)a.logits + t * a.stride * kSize;
@@ -294,10 +302,15 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       const float by = a.sigmoid ? 1.f : score_most;
       __builtin_amdgcn_sched_barrier(0);
       if (a.bias) {
-        Row<float, kN> bias;
-        bias.load(a.bias, n_experts, 0u, lane);
+        if constexpr (kHere) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) c[i] = fused(c[i], by, bias[i]);
+          for (int i = 0; i < kN; ++i) c[i] = fused(c[i], by, s_bias[expert<kN>(i, lane)]);
+        } else {
+          Row<float, kN> bias;
+          bias.load(a.bias, n_experts, 0u, lane);
+#pragma unroll
+          for (int i = 0; i < kN; ++i) c[i] = fused(c[i], by, bias[i]);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < kN; ++i) c[i] *= by;
