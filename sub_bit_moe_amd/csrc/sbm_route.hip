@@ -440,13 +440,14 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
   }
 }
 
-// Workgroups that fill the chip: four waves of each SIMD, and each wave goes on to further tokens (16384 x 2048, by workgroups: 512
-// 64 us, 1024 51, 2048 56, 4096 64: each has to look at the bias first).
-constexpr int kRFull = 1024;
+// The most workgroups; each wave goes on to further tokens.  Above 1024 experts registers hold four waves of each SIMD, and more
+// workgroups only bring the bias to LDS more often (16384 x 2048, by workgroups: 1024 36.7 us, 2048 38.8, 4096 41.2); below more
+// waves fit, and tokens of different lengths even out (65536 x 256 in groups: 1024 124 us, 2048 109, 4096 100, 16384 102).
+constexpr int most_workgroups(int n) { return n > 16 ? 1024 : 4096; }
 
 template <typename T, int kN>
 void launch_route(const RouteArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)std::min<int64_t>(((int64_t)a.n_tokens + kRWaves - 1) / kRWaves, kRFull)), block(kRThreads);
+  const dim3 grid((unsigned)std::min<int64_t>(((int64_t)a.n_tokens + kRWaves - 1) / kRWaves, most_workgroups(kN))), block(kRThreads);
   if (a.n_groups > 1) hipLaunchKernelGGL((route_kernel<T, kN, true>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((route_kernel<T, kN, false>), grid, block, 0, s, a);
 }
