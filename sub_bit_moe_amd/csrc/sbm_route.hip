@@ -229,10 +229,11 @@ struct WaveSpace {
 // are put in order.  Choices with a bias are compared in 32 bits, with what these may be off added to the candidates; where two
 // that follow each other are nearer than that (one token in some hundred to some thousand), the candidates' choices are computed
 // in 64, as the groups' values are where two at the border are.  With more than 64 candidates the whole token is.
-// What bounds it: 16384 x 2048 in fp32 (134 MB) takes 39 us on the card, 48.5 from call to call (26 us of memory at its copy's rate): a
-// token's choices fill the registers, so that four waves are in a SIMD and their vector units busy for 52 %; with room for five or six
-// the registers spill (82 and 98 us), the next token's row read ahead takes the room of a wave (67 us), and by way of LDS it gains
-// 5 %.  8192 x 256 in groups: 20 us, the chain of steps of one token (vector units 69 %).  64 x 2048: 4.7 us, one token's latency.
+// What bounds it: 16384 x 2048 in fp32 (134 MB) takes 37.5 us on the card, 37 to 43 from call to call (26 us of memory at its copy's
+// rate): a token's choices fill the registers, so that four waves are in a SIMD, their vector units busy for 66 %, and all of them
+// wait for rows at about the same time; with room for five or six the registers spilled (82 and 98 us, when the bias came from
+// memory), the next token's row read ahead takes the room of a wave (67), and by way of LDS it is slower (40).  8192 x 256 in
+// groups: 18.5 us, vector units 82 %.  64 x 2048: 4.6 us, one token's latency.
 template <typename T, int kN, bool kGroups>
 __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(RouteArgs a) {
   __shared__ WaveSpace<kN, kGroups> s_space[kRWaves];
@@ -240,7 +241,8 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
   WaveSpace<kN, kGroups>& s = s_space[wave];
   constexpr uint32_t kNoneBits = __is_same(T, float) ? 0xFF800000u : __is_same(T, __bf16) ? 0xFF80u : 0xFC00u;
   constexpr int kSize = __is_same(T, float) ? 4 : 2;
-  // The bias goes to LDS once, where four workgroups of a CU have room for it (from memory for each token: 16384 x 2048 49 us).
+  // The bias goes to LDS once (16384 x 2048: 36.7 us, from memory for each token 49), unless groups' choices leave too little room
+  // there for four workgroups in a CU (16384 x 2048 in groups: 109 us, from memory 92).
   // One that is no number or +inf refuses the tokens that it could be chosen for.
   constexpr bool kHere = !kGroups || kN < 32;
   __shared__ alignas(16) float s_bias[kHere ? kN * 64 : 1];
