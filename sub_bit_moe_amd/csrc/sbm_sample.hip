@@ -39,6 +39,8 @@ struct SampleArgs {
   int32_t vocab, parts;
 };
 
+constexpr float kLowest = -3.402823466e38f;  // of the numbers; from there on is all but -inf
+
 // Where the last token that stays is: logits from `from` on stay, those below it from `to` on are put in order to see.
 struct Range {
   float from, to;
@@ -107,7 +109,7 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t r, int bytes)
   f.top_k = a.top_k ? a.top_k[r] : 0;
   if (f.top_k < 0 || f.top_k >= a.vocab) f.top_k = 0;
   f.bad = f.u != f.u || !(f.temperature >= 0.f) || f.top_p != f.top_p || f.min_p != f.min_p;
-  f.low = -3.402823466e38f;
+  f.low = kLowest;
   f.slope = f.temperature > 0.f ? fmax(1.4426950408889634 / (double)f.temperature, 1e-300) : 0.;      // not 0 * -inf
   f.least = f.temperature > 0.f ? -1000. / f.slope : 0.;
   f.most = 0;
@@ -379,7 +381,7 @@ __device__ Range find_bins(const V* bins, const Row& f, const SampleArgs& a, Sha
   // the bins' beginnings as logits, one by a wave each
   if (tid < 128) {
     const float most = (float)f.most, below = begin_of((uint32_t)s.found[tid >> 6]);
-    float l = below > 0.f ? -3.402823466e38f : INFINITY;
+    float l = below > 0.f ? kLowest : INFINITY;
     if (below > 0.f && below < INFINITY)
       l = of_key(first_key(key_of(l), key_of(most), [&](uint32_t k) { return most - of_key(k) < below; }));
     l = fmaxf(l, f.low);
@@ -409,7 +411,7 @@ __device__ void sum_tiles(const X& tiles, const Row& f, const Range& r, uint64_t
       return;
     }
     uint64_t sum = 0;
-    if (r.from < -3e38f) {                   // all: -inf weighs nothing
+    if (r.from == kLowest) {                 // all: -inf weighs nothing
 #pragma unroll
       for (int i = 0; i < kPer; ++i) sum += f.units.above(weight(f, x[i]));
       sum -= kPer * f.units.none();

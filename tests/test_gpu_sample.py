@@ -229,3 +229,21 @@ def test_captured_on_a_stream_of_its_own_and_replayed(dev):
             torch.cuda.synchronize()
             for a, b, c in zip(got, want, there):
                 assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("vocab", [3, 700, 5000, 40000, 100003])
+def test_filters_that_end_near_the_types_lowest(dev, vocab):
+    """Logits from -3.4e38 to -3.05e38 and temperatures at which their weights differ: a filter's end lies among them."""
+    rng = np.random.default_rng(vocab)
+    n = 12
+    l = np.float64(np.float32(-3.05e38 - 0.35e38 * rng.random((n, vocab))))
+    l[:, :3] = np.float64(np.float32([-3.05e38, -3.1e38, -3.3e38]))
+    l[3, 3:] = -np.inf
+    l[4, 1:] = np.float64(np.float32(-3.4028234e38))
+    u = rng.random(n)
+    u[0] = 0.9
+    for t in (1e38, 3e37, 3e36):
+        for how in (dict(), dict(min_p=0.9), dict(min_p=0.3), dict(top_p=0.4), dict(top_p=0.9), dict(top_p=0.9, min_p=0.8), dict(top_k=2),
+                    dict(top_k=max(vocab // 2, 1)), dict(top_k=max(vocab // 3, 1), top_p=0.7, min_p=0.75)):
+            _check(dev, l, u, temperature=t, **how)
+            _check(dev, R.held(l, "bf16"), u, "bf16", temperature=t, **how)

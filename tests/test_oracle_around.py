@@ -64,3 +64,10 @@ def test_kept_and_sample_by_hand():
     assert [A.sample(l, u)[0] for u in (0.0, 0.499, 0.51, 0.69, 0.71, 0.95, 1.0)] == [0, 0, 1, 1, 2, 3, 3]
     assert abs(A.sample(l, 0.6, top_k=2)[1] - np.log(0.5 / 0.7)) < 1e-12 or A.sample(l, 0.6, top_k=2)[0] == 0
     assert A.sample([-np.inf, -np.inf], 0.5)[0] == A.sample([0.0, np.nan], 0.5)[0] == A.sample([0.0, np.inf], 0.5)[0] == -1
+
+
+def test_choice_near_the_types_lowest():
+    l = [-3.05e38, -3.1e38, -3.3e38]
+    assert A.kept(l, temperature=1e38, min_p=0.9)[0].tolist() == [0, 1] and A.kept(l, temperature=1e38, top_p=0.5)[0].tolist() == [0, 1]
+    assert A.kept(l, temperature=1e38, top_p=0.3)[0].tolist() == [0] and A.kept(l, temperature=1e38)[0].tolist() == [0, 1, 2]
+    assert A.sample(l, 0.9, temperature=1e38, min_p=0.9)[0] == 1
