@@ -271,11 +271,12 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       most = fmaxf(most, x[i]);
       low = fminf(low, x[i]);
     }
-    if (a.sigmoid || (!a.bias && !kGroups && a.renorm)) {                  // else the softmax's sum tells
+    most = wave_max(most);
+    // else the softmax's sum tells, unless there is nothing but -inf beside
+    if (a.sigmoid || (!a.bias && !kGroups && a.renorm) || most == -INFINITY) {
 #pragma unroll
       for (int i = 1; i < kN; ++i) bad = bad || x[i] != x[i];
     }
-    most = wave_max(most);
     bad = __any(bad) || most == INFINITY;
     const bool masked = __any(low == -INFINITY);
     uint32_t hidden[(kN + 31) / 32] = {};    // a bit for each -inf, so that the logits need not be kept beside the choices

@@ -176,3 +176,28 @@ def test_captured_on_a_stream_of_its_own_and_replayed(dev):
         torch.cuda.synchronize()
         for a, b, c in zip(got, want, there):
             assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("E", [1, 40, 100, 128, 200, 256, 500, 1000, 2048, 4096])
+@pytest.mark.parametrize("others", ["finite", "masked", "some"])
+def test_no_number_at_any_place(dev, E, others):
+    """A NaN or +inf at each of the places that a lane has, beside finite logits, beside -inf alone, and beside both."""
+    rng = np.random.default_rng(E)
+    at = sorted({0, E - 1, *(p for p in range(0, E, 64)), *(int(p) for p in rng.integers(0, E, 12)),
+                 *(p + j for p in range(0, E, 256) for j in range(1, 4) if p + j < E)})
+    l = R.held(rng.standard_normal((2 * len(at) + 2, E)), "fp32")
+    if others == "masked":
+        l[:] = -np.inf
+    elif others == "some":
+        l[rng.random(l.shape) < 0.9] = -np.inf
+    for i, p in enumerate(at):
+        l[2 * i, p], l[2 * i + 1, p] = np.nan, np.inf
+    bias = R.held(0.1 * rng.standard_normal(E), "fp32")
+    groups = next(g for g in (4, 5, 3, 1) if E % g == 0)
+    k = min(3, E // groups)
+    for b in (None, bias):
+        for sigmoid in (False, True):
+            for renormalise in (False, True):
+                _check(dev, l, k, b, sigmoid=sigmoid, renormalise=renormalise)
+                _check(dev, l, k, b, sigmoid=sigmoid, renormalise=renormalise, n_groups=groups, top_groups=max(1, groups // 2))
+    _check(dev, l, k, requests=np.full(l.shape[0], -1))                # padding is not counted

@@ -71,3 +71,14 @@ def test_choice_near_the_types_lowest():
     assert A.kept(l, temperature=1e38, min_p=0.9)[0].tolist() == [0, 1] and A.kept(l, temperature=1e38, top_p=0.5)[0].tolist() == [0, 1]
     assert A.kept(l, temperature=1e38, top_p=0.3)[0].tolist() == [0] and A.kept(l, temperature=1e38)[0].tolist() == [0, 1, 2]
     assert A.sample(l, 0.9, temperature=1e38, min_p=0.9)[0] == 1
+
+
+def test_a_row_of_masks_with_no_number_is_refused():
+    for bad in (np.nan, np.inf):
+        for at in (0, 1, 100, 127):
+            l = np.full((1, 128), -np.inf)
+            l[0, at] = bad
+            for how in (dict(), dict(bias=np.zeros(128)), dict(n_groups=4), dict(sigmoid=True), dict(renormalise=True)):
+                ids, gates, refused = A.route(l, 2, **how)
+                assert refused == 1 and (ids == -1).all() and not gates.any()
+    assert A.route(np.full((1, 128), -np.inf), 2)[2] == 0
