@@ -97,12 +97,20 @@ struct Row {
 __device__ __forceinline__ float exp2_f32(float x) { return __builtin_amdgcn_exp2f(x); }
 constexpr float kLog2e = 1.44269504f;
 
-// A score of an expert's logit in 64 bits; most, sum: the softmax's.  Where e^-l passes 2^700 the sigmoid is 0.
+// 2^x as 64 bits hold it, below 2^-1000 as well, which exp2_f64 does not go: as a denormal, or 0 where there is none.
+__device__ __forceinline__ double exp2_any(double x) {
+  double y = exp2_f64(x);
+  if (__any(x < -1000.)) y = x < -1000. ? exp2_f64(x + 200.) * 0x1p-200 : y;
+  return y;
+}
+
+// A score of an expert's logit in 64 bits; most, sum: the softmax's.  Where e^-l is no number of 64 bits the sigmoid is 0.
 __device__ __forceinline__ double score_of(const RouteArgs& a, float l, float most, double sum) {
   constexpr double kLog2e64 = 1.4426950408889634;
-  if (!a.sigmoid) return exp2_f64(((double)l - (double)most) * kLog2e64) * inverse(sum);
+  if (!a.sigmoid) return exp2_any(((double)l - (double)most) * kLog2e64) * inverse(sum);
   const double x = -(double)l * kLog2e64;
-  return x > 700. ? 0. : inverse(1. + exp2_f64(x));
+  if (__any(x > 1000.)) return x >= 1024. ? 0. : x > 1000. ? exp2_any(-x) : inverse(1. + exp2_f64(x));
+  return inverse(1. + exp2_f64(x));
 }
 
 // The softmax's sum in 64 bits.
@@ -434,7 +442,8 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
     double g = id < 0 ? 0. : score_of(a, l, most, a.renorm ? 1. : (double)z);
     if (a.renorm) {
       const double total = wave_sum(g);
-      if (total > 0.) g *= 1. / total;
+      if (total > 0x1p-900) g *= inverse(total);
+      else if (total > 0.) g = g * 0x1p150 * inverse(total * 0x1p150);     // 1 / total may be no number of 64 bits
     }
     if (lane < a.k) {
       a.ids[t * a.k + lane] = id;

@@ -201,3 +201,36 @@ def test_no_number_at_any_place(dev, E, others):
                 _check(dev, l, k, b, sigmoid=sigmoid, renormalise=renormalise)
                 _check(dev, l, k, b, sigmoid=sigmoid, renormalise=renormalise, n_groups=groups, top_groups=max(1, groups // 2))
     _check(dev, l, k, requests=np.full(l.shape[0], -1))                # padding is not counted
+
+
+def test_scores_far_below_the_largest(dev):
+    """Softmax scores that 64 bits hold as denormals or not at all: the choice, the groups and the gates are those of 64 bits."""
+    l = np.zeros((1, 16))
+    l[0, 0], l[0, 3] = 1000.0, 100.0
+    bias = np.zeros(16)
+    bias[0] = -np.inf
+    for k in (1, 2, 5):
+        ids, gates = _check(dev, l, k, bias, renormalise=True)           # nothing is left of any score: gates stay 0
+        assert not gates.any()
+    l[0] = 0.0
+    l[0, [0, 3, 7, 9]] = 1000.0, 300.0, 270.0, 330.0
+    _check(dev, l, 4, bias, renormalise=True)
+    _check(dev, l, 4, bias)
+    l = np.float64([[0, -800, -720, -720, -700, -700], [0, -800, -700, -720, -720, -700], [-690, -690, -700, -680, 0, -1e5]])
+    for best in (1, 2):
+        ids, _ = _check(dev, l, 4, n_groups=3, top_groups=2, group_best=best)
+        _check(dev, l, 4, n_groups=3, top_groups=2, group_best=best, renormalise=True)
+        _check(dev, l, 4, np.float64([0, 0, 0, 0, 0, 0]), n_groups=3, top_groups=2, group_best=best, renormalise=True)
+    assert ids[0].tolist() == [0, 4, 5, 1]
+
+
+def test_sigmoid_scores_far_below_one(dev):
+    """As far down as 64 bits hold 1 / (1 + e^-l)."""
+    l = np.float64([[-500, -500, -501, -700, -5000, -5000], [-486, -485, -484, -490, -495, -600], [-708, -708.5, -709.5, -712, -745, -3e38],
+                    [-712, -720, -745, -800, -1e4, -3e38]])
+    l = np.float64(np.float32(l))
+    for b in (None, np.zeros(6)):
+        _check(dev, l, 2, b, sigmoid=True, renormalise=True)
+        _check(dev, l, 4, b, sigmoid=True, renormalise=True, scale=2.5)
+        _check(dev, l, 2, b, sigmoid=True, renormalise=True, n_groups=3, top_groups=1)
+        _check(dev, l, 2, b, sigmoid=True, renormalise=True, n_groups=2, top_groups=1)

@@ -82,3 +82,14 @@ def test_a_row_of_masks_with_no_number_is_refused():
                 ids, gates, refused = A.route(l, 2, **how)
                 assert refused == 1 and (ids == -1).all() and not gates.any()
     assert A.route(np.full((1, 128), -np.inf), 2)[2] == 0
+
+
+def test_scores_far_below_the_largest():
+    l, bias = np.zeros((1, 16)), np.zeros(16)
+    l[0, 0], l[0, 3], bias[0] = 1000.0, 100.0, -np.inf
+    ids, gates, _ = A.route(l, 2, bias, renormalise=True)
+    assert ids.tolist() == [[1, 2]] and gates.tolist() == [[0.0, 0.0]]
+    ids, _, _ = A.route([[0, -800, -720, -720, -700, -700]], 4, n_groups=3, top_groups=2)
+    assert ids.tolist() == [[0, 4, 5, 1]]
+    ids, gates, _ = A.route([[-500.0, -500.0, -700.0]], 2, sigmoid=True, renormalise=True)
+    assert ids.tolist() == [[0, 1]] and gates.tolist() == [[0.5, 0.5]]
