@@ -146,30 +146,40 @@ __device__ __forceinline__ int lanes_of(int n_groups) {
   return lanes;
 }
 
-// The groups that stay, as bits, from the values that groups' lanes have; `near`: whether two at the border are nearer than `off`.
+// A group's value, and how large the choices are that it is the sum of: what it may be off by goes by those, not by what is left
+// of them.
 template <typename C>
-__device__ __forceinline__ uint64_t best_groups(const RouteArgs& a, C value, int lanes, C off, bool* near) {
+struct Group {
+  C value, size;
+};
+
+// The groups that stay, as bits, from what the groups' lanes have; `near`: whether one that stays and one that does not are too near
+// to tell apart, where a value may be off by `off` and by roundings of what it is the sum of.
+template <typename C>
+__device__ __forceinline__ uint64_t best_groups(const RouteArgs& a, Group<C> v, int lanes, C off, bool* near) {
   const int lane = (int)threadIdx.x & 63, g = lane / lanes;
   int place = 0;
   for (int h = 0; h < a.n_groups; ++h) {
-    const C v = of_lane(value, h * lanes);
-    place += v > value || (v == value && h < g);
+    const C o = of_lane(v.value, h * lanes);
+    place += o > v.value || (o == v.value && h < g);
   }
-  const bool is = g < a.n_groups && lane % lanes == 0 && value > -(C)INFINITY;
+  const bool is = g < a.n_groups && lane % lanes == 0 && v.value > -(C)INFINITY;
   const uint64_t kept = __ballot(is && place < a.top_groups);
   if (near) {
-    const float least = -wave_max(is && place < a.top_groups ? -(float)value : -INFINITY);
-    const float next = wave_max(is && place >= a.top_groups ? (float)value : -INFINITY);
-    *near = next > -INFINITY && !(least - next > off + 0x1p-21f * fmaxf(fabsf(least), fabsf(next)));
+    // two choices and their sum, each rounded to 2^-24 of itself, and the additions here
+    const float by = (float)(off + (C)0x1p-22f * v.size);
+    const float least = -wave_max(is && place < a.top_groups ? by - (float)v.value : -INFINITY);
+    const float next = wave_max(is && place >= a.top_groups ? (float)v.value + by : -INFINITY);
+    *near = next > -INFINITY && !(least > next);
   }
   uint64_t stay = 0;
   for (uint64_t m = kept; m; m &= m - 1) stay |= 1ull << (__builtin_ctzll(m) / lanes);
   return stay;
 }
 
-// The value of a lane's group from its two largest choices.
+// What a lane's group is worth, from its two largest choices.
 template <typename C, typename F>
-__device__ __forceinline__ C group_value(const RouteArgs& a, int lanes, F choice) {
+__device__ __forceinline__ Group<C> group_value(const RouteArgs& a, int lanes, F choice) {
   const int lane = (int)threadIdx.x & 63, g = lane / lanes, per = a.n_experts / a.n_groups;
   C one = -(C)INFINITY, two = one;
   if (g < a.n_groups) {
@@ -185,14 +195,16 @@ __device__ __forceinline__ C group_value(const RouteArgs& a, int lanes, F choice
     two = two > less ? two : less;
     one = one > o1 ? one : o1;
   }
-  return a.group_best == 2 && two > -(C)INFINITY ? one + two : one;
+  const C first = one < 0 ? -one : one;
+  if (a.group_best == 2 && two > -(C)INFINITY) return Group<C>{one + two, first + (two < 0 ? -two : two)};
+  return Group<C>{one, first};
 }
 
 template <typename T>
 __device__ uint64_t groups_exactly(const RouteArgs& a, const void* row, float most) {
   const double sum = a.sigmoid ? 1. : sum_of<T>(a, row, most);
   const int lanes = lanes_of(a.n_groups);
-  const double value = group_value<double>(a, lanes, [&](int e) {
+  const Group<double> value = group_value<double>(a, lanes, [&](int e) {
     const float l = logit_at<T>(row, e);
     return l == -INFINITY ? -(double)INFINITY : score_of(a, l, most, sum) + (a.bias ? (double)a.bias[e] : 0.);
   });
@@ -364,7 +376,7 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
       const int lanes = lanes_of(a.n_groups);
       bool near;
-      stay = best_groups(a, group_value<float>(a, lanes, [&](int e) { return s.choice[e]; }), lanes, 2.f * off, &near);
+      stay = best_groups(a, group_value<float>(a, lanes, [&](int e) { return s.choice[e]; }), lanes, off, &near);
       if (near) stay = groups_exactly<T>(a, row, most);
     }
     if constexpr (kGroups) {

@@ -234,3 +234,17 @@ def test_sigmoid_scores_far_below_one(dev):
         _check(dev, l, 4, b, sigmoid=True, renormalise=True, scale=2.5)
         _check(dev, l, 2, b, sigmoid=True, renormalise=True, n_groups=3, top_groups=1)
         _check(dev, l, 2, b, sigmoid=True, renormalise=True, n_groups=2, top_groups=1)
+
+
+@pytest.mark.parametrize("E,groups", [(128, 64), (256, 32), (2048, 64), (60, 20)])
+@pytest.mark.parametrize("size", [20.0, 1e3, 1e6])
+def test_groups_whose_largest_cancel(dev, E, groups, size):
+    """Biases of both signs, far larger than the scores: a group's value is what their sum leaves of them."""
+    rng = np.random.default_rng(E + int(size))
+    T, per = 400, E // groups
+    l = R.held(rng.standard_normal((T, E)), "fp32")
+    bias = np.full((groups, per), -2 * size)
+    bias[:, 0], bias[:, 1] = size, -size
+    bias = np.float64(np.float32(bias.reshape(-1)))
+    for sigmoid in (False, True):
+        _check(dev, l, 5, bias, sigmoid=sigmoid, n_groups=groups, top_groups=5, renormalise=True)

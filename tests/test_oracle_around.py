@@ -93,3 +93,11 @@ def test_scores_far_below_the_largest():
     assert ids.tolist() == [[0, 4, 5, 1]]
     ids, gates, _ = A.route([[-500.0, -500.0, -700.0]], 2, sigmoid=True, renormalise=True)
     assert ids.tolist() == [[0, 1]] and gates.tolist() == [[0.5, 0.5]]
+
+
+def test_groups_by_what_cancels_and_by_the_types_lowest():
+    # scores 1/4 each: values 0.5, 0.5 + 0.125 and the lowest
+    ids, _, _ = A.route([[0.0] * 4], 1, [1e6, -1e6, 1e6, -1e6 + 0.125], n_groups=2)
+    assert ids.tolist() == [[2]]
+    ids, _, _ = A.route([[0.0] * 4], 3, [0.0, 0.0, -3.4028234663852886e38, -3.4028234663852886e38], n_groups=2, top_groups=2)
+    assert ids.tolist() == [[0, 1, 2]]
