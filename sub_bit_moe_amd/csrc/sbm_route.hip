@@ -196,7 +196,11 @@ __device__ __forceinline__ Group<C> group_value(const RouteArgs& a, int lanes, F
     one = one > o1 ? one : o1;
   }
   const C first = one < 0 ? -one : one;
-  if (a.group_best == 2 && two > -(C)INFINITY) return Group<C>{one + two, first + (two < 0 ? -two : two)};
+  if (a.group_best == 2 && two > -(C)INFINITY) {
+    // a sum past the type's lowest is a group still; its size says that it cannot be told from others
+    const C sum = one + two;
+    return Group<C>{sum > -(C)INFINITY ? sum : -(C)3.402823466e38f, first + (two < 0 ? -two : two)};
+  }
   return Group<C>{one, first};
 }
 

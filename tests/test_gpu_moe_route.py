@@ -248,3 +248,22 @@ def test_groups_whose_largest_cancel(dev, E, groups, size):
     bias = np.float64(np.float32(bias.reshape(-1)))
     for sigmoid in (False, True):
         _check(dev, l, 5, bias, sigmoid=sigmoid, n_groups=groups, top_groups=5, renormalise=True)
+
+
+@pytest.mark.parametrize("lowest", [-3.4028234663852886e38, -3e38, -1.8e38, 1.8e38, 3.4028234663852886e38])
+def test_groups_of_the_types_lowest_and_largest_biases(dev, lowest):
+    """Experts kept back by the type's lowest value are experts still: their groups are chosen where there are no others."""
+    rng = np.random.default_rng(6)
+    for E, groups in ((12, 3), (256, 8), (2048, 16)):
+        l = R.held(rng.standard_normal((9, E)), "fp32")
+        per = E // groups
+        bias = np.zeros((groups, per))
+        bias[1:] = lowest
+        bias[-1, 0] = 0.25
+        bias = np.float64(np.float32(bias.reshape(-1)))
+        for sigmoid in (False, True):
+            for best in (1, 2):
+                for top in (1, 2, groups):
+                    k = min(per * top, 32)
+                    ids, _ = _check(dev, l, k, bias, sigmoid=sigmoid, n_groups=groups, top_groups=top, group_best=best)
+                    assert (ids >= 0).all()
