@@ -267,3 +267,32 @@ def test_groups_of_the_types_lowest_and_largest_biases(dev, lowest):
                     k = min(per * top, 32)
                     ids, _ = _check(dev, l, k, bias, sigmoid=sigmoid, n_groups=groups, top_groups=top, group_best=best)
                     assert (ids >= 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("E", [1, 8, 60, 64, 128, 200, 256, 512, 1000, 1024, 2048, 4096])
+def test_gates_to_what_is_claimed(dev, E, dtype):
+    """Gates are of 64 bits (weights to 4e-14) and rounded to fp32: half a step, 2^-24.  A softmax that is not renormalised divides by a
+    sum of fp32 exponentials, which adds, in units of 2^-24: 4 for an exponential, 2 for the additions of fours in 32 bits (the rest are in
+    64), and for the exponent -t, whose difference and product are rounded once each to 2^-24 of t, 2 ln 2 times t: on the sum's
+    average."""
+    rng = np.random.default_rng(E + 1)
+    l = 2 * rng.standard_normal((24, E))
+    l[0] *= 20
+    l = R.held(l, dtype)
+    l[1:5][rng.random((4, E)) < 0.5] = -np.inf
+    l[5] = 0.75
+    t = np.where(l > -np.inf, (l.max(1, keepdims=True).clip(-1e30) - l) / np.log(2), 0.0)
+    p = np.where(l > -np.inf, np.exp2(-t), 0.0)
+    sums = 6 + 2 * np.log(2) * (p * t).sum(1, keepdims=True) / p.sum(1, keepdims=True).clip(1)
+    bias = R.held(0.1 * rng.standard_normal(E), "fp32")
+    groups = 4 if E % 4 == 0 else 1
+    for k in {1, min(E // groups, 6)}:
+        for b in (None, bias):
+            for sigmoid in (False, True):
+                for how in (dict(), dict(renormalise=True, scale=2.5), dict(n_groups=groups, top_groups=max(1, groups // 2)), dict(scale=0.1)):
+                    how = {**how, "scale": float(np.float32(how.get("scale", 1.0)))}
+                    _, gates = _check(dev, l, k, b, dtype=dtype, sigmoid=sigmoid, **how)
+                    want = A.route(l, k, b, sigmoid=sigmoid, **how)[1]
+                    units = 1 + (0 if sigmoid or how.get("renormalise") else sums)
+                    assert (np.abs(V.array(gates) - want) <= (2.0 ** -24 * units + 1e-12) * want + 2.0 ** -149).all()
