@@ -306,11 +306,11 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
   const int64_t step = (int64_t)gridDim.x * kRWaves;
   for (int64_t t = (int64_t)blockIdx.x * kRWaves + wave; t < a.n_tokens; t += step) {
     const char* row = (const char*)a.logits + t * a.stride * kSize;
-    // what depends on these is made anew for each token: kept, it would fill the registers
-    int lane = (int)threadIdx.x & 63, n_experts = a.n_experts;
-    asm("" : "+v"(lane), "+s"(n_experts));
+    // what depends on it is made anew for each token: kept, it would fill the registers
+    int lane = (int)threadIdx.x & 63;
+    asm("" : "+v"(lane));
     Row<T, kN> x;
-    x.load(row, n_experts, kNoneBits, lane);
+    x.load(row, a.n_experts, kNoneBits, lane);
     const bool padding = a.requests && a.requests[t] < 0;
     float most = x[0], low = x[0];
     bool bad = !(x[0] < INFINITY);
@@ -353,7 +353,7 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
           for (int i = 0; i < kN; ++i) c[i] = fused(c[i], by, s_bias[expert<kN>(i, lane)]);
         } else {
           Row<float, kN> bias;
-          bias.load(a.bias, n_experts, 0u, lane);
+          bias.load(a.bias, a.n_experts, 0u, lane);
 #pragma unroll
           for (int i = 0; i < kN; ++i) c[i] = fused(c[i], by, bias[i]);
         }
@@ -399,7 +399,7 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
     }
     if constexpr (kGroups) {
       if (!a.bias) {                         // the order is the logits': read again, rather than kept
-        x.load(row, n_experts, kNoneBits, lane);
+        x.load(row, a.n_experts, kNoneBits, lane);
 #pragma unroll
         for (int i = 0; i < kN; ++i) c[i] = x[i];
       }
