@@ -543,7 +543,7 @@ int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks
  * halves to even, at most 448 in magnitude.  The elements of a block share a scale:
  *   scale_block 0 (the row) or 128: fp32, max|y| / 448 rounded to fp32, at least 2^-126
  *   scale_block 32: a byte s for 2^(s - 127), the smallest s from 1 to 254 at which
- *     no |y| passes 448 * 2^(s - 127) (254 where one does at any; codes are then 448)
+ *     no |y| passes 448 * 2^(s - 127) (at 254 none can: |y| <= sqrt(dim) |weight|)
  * A block with a NaN or an infinity has scale NaN (byte 255) and zero codes.  The
  * mean of squares is summed in 64 bits; 16-bit results are computed in 32 bits, 8-bit
  * ones in 64.

@@ -247,10 +247,22 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
         top = Most()(top, (uint32_t)__shfl_xor((int)top, 1, 64));          // four neighbouring lanes hold a block
         top = Most()(top, (uint32_t)__shfl_xor((int)top, 2, 64));
         // the least power of two at which nothing passes 448 = 1.75 * 2^8
-        const int e = min(max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u), -126), 127);
-        const bool bad = top >= 0x7F800000u;
-        const float by = __builtin_amdgcn_ldexpf(1.f, -e);
-        store_codes(a, t, d0, n_blocks, q, by, bad, (uint8_t)(bad ? 255 : e + 127));
+        int e = max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u), -126);
+        float by = __builtin_amdgcn_ldexpf(1.f, -e);
+        bool bad = false;
+        if (top >= 0x7F800000u) {                       // past the numbers of 32 bits (four lanes together): the same in 64
+          uint64_t all = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) all = Most()(all, magnitude(h[i][j]));
+          all = Most()(all, (uint64_t)__shfl_xor(all, 1, 64));
+          all = Most()(all, (uint64_t)__shfl_xor(all, 2, 64));
+          bad = all >= 0x7FF0000000000000ull;
+          e = bad ? 128 : (int)(all >> 52) - 1023 - 8 + ((all & 0xFFFFFFFFFFFFFull) > 0xC000000000000ull);
+          by = 1.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) q[j] = to_odd(__builtin_amdgcn_ldexp(h[i][j], -e));
+        }
+        store_codes(a, t, d0, n_blocks, q, by, bad, (uint8_t)(e + 127));
       }
     } else {
       uint64_t top[kN];

@@ -228,3 +228,32 @@ def test_captured_on_a_stream_of_its_own_and_replayed(dev):
         torch.cuda.synchronize()
         for a, b in zip(there, want):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("block", [0, 32, 128])
+@pytest.mark.parametrize("dtype,r_type", [("bf16", "bf16"), ("bf16", "fp32")])
+@pytest.mark.parametrize("D", [32, 100, 256, 2080, 8200, 32768])
+def test_eight_bits_of_results_past_32_bits(dev, D, block, dtype, r_type):
+    """bf16 weights up to the type's largest: finite results from 2^128 on have scales and codes as the smaller ones do."""
+    rng = np.random.default_rng(D + block)
+    x, g, r, w = R.norm_case(rng, 6, D, dtype=dtype, x_type="fp32", r_type=r_type, gates=False)
+    w = R.held(np.where(rng.random(D) < 0.5, 3.3e38, 1e38) * rng.uniform(0.5, 1.0, D), "bf16")
+    x[0] = r[0] = x[4] = r[4] = 0.0
+    x[0, D // 2], x[4, 0] = 7.0, -1e-3                        # alone in their rows: sqrt(D) times their weights
+    x[1] *= 1e-3
+    x = R.held(x, "fp32")
+    w[0], w[D // 2] = R.held([3.3e38, 3.3895e38], "bf16")
+    _check(dev, x, None, r, w, dtype=dtype, x_type="fp32", r_type=r_type, block=block)
+    w[:] = R.held([3.3895e38], "bf16")
+    _check(dev, x, None, r, w, dtype=dtype, x_type="fp32", r_type=r_type, block=block)
+    x[2, D - 1], x[3, 1] = np.nan, np.inf                      # which are still no numbers
+    _check_bad(dev, x, w, block)
+
+
+def _check_bad(dev, x, w, block):
+    from sub_bit_moe_amd import api
+    codes, scales, _ = api.add_rms_norm_fp8(R.tensor(x, "fp32", dev), R.tensor(w, "bf16", dev), scale_block=block)
+    want, unit, powers = A.fp8(A.rms_norm(x, w), block)
+    assert np.array_equal(scales.cpu().numpy(), unit if powers is None else powers, equal_nan=True)
+    got = codes.double().cpu().numpy() * np.repeat(unit, block or x.shape[1], 1)[:, :x.shape[1]]
+    assert np.array_equal(got, want, equal_nan=True)

@@ -101,3 +101,11 @@ def test_groups_by_what_cancels_and_by_the_types_lowest():
     assert ids.tolist() == [[2]]
     ids, _, _ = A.route([[0.0] * 4], 3, [0.0, 0.0, -3.4028234663852886e38, -3.4028234663852886e38], n_groups=2, top_groups=2)
     assert ids.tolist() == [[0, 1, 2]]
+
+
+def test_scales_of_results_past_32_bits():
+    y = np.zeros((3, 32))
+    y[0, 0], y[1, 3], y[2, 5] = 1e39, 2.0 ** 128, 6.1e40
+    v, scales, powers = A.fp8(y, 32)
+    assert powers[:, 0].tolist() == [248, 247, 254]
+    assert v[1, 3] == 2.0 ** 128 and abs(v[0, 0] / 1e39 - 1) < 2.0 ** -4 and np.isfinite(v).all()
