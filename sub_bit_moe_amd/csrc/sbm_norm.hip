@@ -250,14 +250,17 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
         int e = max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u), -126);
         float by = __builtin_amdgcn_ldexpf(1.f, -e);
         bool bad = false;
-        if (top >= 0x7F800000u) {                       // past the numbers of 32 bits (four lanes together): the same in 64
+        // From 64 bits where 32 do not hold the block, or where codes could come from numbers below their least normal one, 2^-126, which
+        // have fewer bits (with a scale of 2^-115 or more those are below half the least code).  Four lanes are here together.
+        constexpr uint32_t kLeast = (uint32_t)(127 - 115 + 8) << 23;
+        if (top && top - kLeast >= 0x7F800000u - kLeast) {
           uint64_t all = 0;
 #pragma unroll
           for (int j = 0; j < 8; ++j) all = Most()(all, magnitude(h[i][j]));
           all = Most()(all, (uint64_t)__shfl_xor(all, 1, 64));
           all = Most()(all, (uint64_t)__shfl_xor(all, 2, 64));
           bad = all >= 0x7FF0000000000000ull;
-          e = bad ? 128 : (int)(all >> 52) - 1023 - 8 + ((all & 0xFFFFFFFFFFFFFull) > 0xC000000000000ull);
+          e = bad ? 128 : max((int)(all >> 52) - 1023 - 8 + ((all & 0xFFFFFFFFFFFFFull) > 0xC000000000000ull), -126);
           by = 1.f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) q[j] = to_odd(__builtin_amdgcn_ldexp(h[i][j], -e));

@@ -257,3 +257,22 @@ def _check_bad(dev, x, w, block):
     assert np.array_equal(scales.cpu().numpy(), unit if powers is None else powers, equal_nan=True)
     got = codes.double().cpu().numpy() * np.repeat(unit, block or x.shape[1], 1)[:, :x.shape[1]]
     assert np.array_equal(got, want, equal_nan=True)
+
+
+def test_every_code_and_border_of_the_smallest_scale(dev):
+    """Results below the least normal number of 32 bits: e4m3 numbers, borders between two, and what is beside those."""
+    from sub_bit_moe_amd import api
+    D = 32
+    borders = np.concatenate([A.E4M3, (A.E4M3[1:] + A.E4M3[:-1]) / 2])
+    a = np.concatenate([borders * s for s in (1, 1 + 2.0 ** -22, 1 - 2.0 ** -22)])
+    a = np.concatenate([a, -a, np.zeros(-2 * a.size % D)])
+    a = a[np.argsort(np.abs(a), kind="stable")].reshape(-1, D)             # rows of like sizes
+    for power in (-126, -127, -130):
+        x = np.float64(np.float32(a * 2.0 ** (power + 60)))
+        # an eps beside which the mean is nothing: the norm divides by 2^60
+        y = A.rms_norm(x, None, 2.0 ** 120)
+        for block in (32, 0, 128):
+            want, unit, powers = A.fp8(y, block)
+            codes, scales, _ = api.add_rms_norm_fp8(R.tensor(x, "fp32", dev), eps=2.0 ** 120, scale_block=block, dtype=torch.bfloat16)
+            assert np.array_equal(scales.cpu().numpy(), unit if powers is None else powers)
+            assert np.array_equal(codes.double().cpu().numpy() * unit, want)
