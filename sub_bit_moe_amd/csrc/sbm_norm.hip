@@ -293,10 +293,14 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
         const double most = __builtin_bit_cast(double, top[i]);
         const bool bad = !(most < (double)INFINITY);
         const float scale = fmaxf((float)(most / 448.), 0x1p-126f);
-        const double by = 1. / (double)scale;
+        const double unit = (double)scale, by = 1. / unit;
         float q[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = to_odd(h[i][j] * by);
+        for (int j = 0; j < 8; ++j) {
+          // a quotient that 64 bits hold, the middle between two codes among them, comes out as itself
+          const double about = h[i][j] * by;
+          q[j] = to_odd(fused(fused(-about, unit, h[i][j]), by, about));
+        }
         store_codes(a, t, (tid + i * G) * 8, n_blocks, q, 1.f, bad, bad ? __builtin_nanf("") : scale);
       }
     }

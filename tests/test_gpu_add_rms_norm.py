@@ -276,3 +276,18 @@ def test_every_code_and_border_of_the_smallest_scale(dev):
             codes, scales, _ = api.add_rms_norm_fp8(R.tensor(x, "fp32", dev), eps=2.0 ** 120, scale_block=block, dtype=torch.bfloat16)
             assert np.array_equal(scales.cpu().numpy(), unit if powers is None else powers)
             assert np.array_equal(codes.double().cpu().numpy() * unit, want)
+
+
+@pytest.mark.parametrize("block", [0, 128])
+def test_borders_with_scales_that_are_no_powers_of_two(dev, block):
+    """Results that are a scale times a border between two codes go to the even one, whatever the scale's reciprocal rounds to."""
+    from sub_bit_moe_amd import api
+    rng = np.random.default_rng(12)
+    borders = (A.E4M3[1:] + A.E4M3[:-1]) / 2
+    unit = 1 + rng.integers(0, 1 << 18, 400) / 2.0 ** 18                   # 448 and borders times these are fp32 numbers
+    x = np.concatenate([448 * unit[:, None], unit[:, None] * borders[None]], 1)[:, :127]
+    assert np.array_equal(x, np.float64(np.float32(x)))
+    want, scale, _ = A.fp8(A.rms_norm(x, None, 2.0 ** 120), block)         # the norm divides by 2^60
+    codes, scales, _ = api.add_rms_norm_fp8(R.tensor(x, "fp32", dev), eps=2.0 ** 120, scale_block=block, dtype=torch.bfloat16)
+    assert np.array_equal(scales.cpu().numpy(), scale)
+    assert np.array_equal(codes.double().cpu().numpy() * scale, want)
