@@ -192,8 +192,12 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
         store_raw<4>(row + (int64_t)d0 * 4, y, a.dim - d0);
       } else {
         uint16_t y[8];
+        if constexpr (k8) {
+          round_once8<T>(h[i], y);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = round_once<T>(h[i][j]);
+          for (int j = 0; j < 8; ++j) y[j] = round_once<T>(h[i][j]);
+        }
         store_raw<2>(row + (int64_t)d0 * 2, y, a.dim - d0);
       }
     }

@@ -14,7 +14,7 @@ __device__ __forceinline__ float to_f32(uint16_t u) {
 }
 
 // 64 bits to 32 with what those cannot hold gathered in their lowest bit (round to odd): a further rounding to fewer
-// bits then sees on which side of a border the value was.
+// bits then sees on which side of a border the value was.  Of numbers from 2^-126 on; those below are rounded to the nearest.
 __device__ __forceinline__ float to_odd(double y) {
   constexpr uint32_t kBelow = 0x1FFFFFFFu;
   const uint64_t b = __builtin_bit_cast(uint64_t, y);
@@ -30,6 +30,28 @@ __device__ __forceinline__ uint16_t round_once(float y) {
 template <typename T>
 __device__ __forceinline__ uint16_t round_once(double y) {
   return round_once<T>(to_odd(y));
+}
+
+// Eight numbers, also those of bf16 below 2^-126.
+template <typename T>
+__device__ __forceinline__ void round_once8(const double* x, uint16_t* y) {
+  float odd[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) odd[j] = to_odd(x[j]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = round_once<T>(odd[j]);
+  if constexpr (__is_same(T, __bf16)) {
+    bool small = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) small = small || __builtin_isfpclass(odd[j], 0x0090);        // subnormal
+    if (small) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double steps = __builtin_rint(__builtin_fabs(x[j]) * 0x1p133);
+        if (__builtin_fabs(x[j]) < 0x1p-126) y[j] = (uint16_t)((uint32_t)steps | (__float_as_uint(odd[j]) >> 31) << 15);
+      }
+    }
+  }
 }
 
 // 1 / sqrt(x): the hardware's estimate and one step of third order (2^-23 to below 2^-60).

@@ -291,3 +291,19 @@ def test_borders_with_scales_that_are_no_powers_of_two(dev, block):
     codes, scales, _ = api.add_rms_norm_fp8(R.tensor(x, "fp32", dev), eps=2.0 ** 120, scale_block=block, dtype=torch.bfloat16)
     assert np.array_equal(scales.cpu().numpy(), scale)
     assert np.array_equal(codes.double().cpu().numpy() * scale, want)
+
+
+@pytest.mark.parametrize("block", [0, 32])
+def test_the_sum_beside_8_bit_results_is_rounded_once(dev, block):
+    """bf16 residuals below the least normal number: between two, with something beside the middle."""
+    m = np.arange(1, 128)
+    D = m.size
+    x = np.stack([(2 * m + 1) * 2.0 ** -133, np.full(D, 2.0 ** -126), (2 * m + 1) * 2.0 ** -133, np.full(D, -2.0 ** -126),
+                  (2 * m + 1) * 2.0 ** -133, np.zeros(D)])
+    x = R.held(x, "fp32")
+    g = np.float64([[0.5, 2.0 ** -30], [-0.5, 2.0 ** -30], [0.5, 1.0]])
+    from sub_bit_moe_amd import api
+    r = np.zeros((3, D))
+    _, _, res = api.add_rms_norm_fp8(R.tensor(x, "fp32", dev), None, R.tensor(r, "bf16", dev), gates=R.tensor(g, "fp32", dev), scale_block=block)
+    want = np.stack([m + 1, -(m + 1), np.where(m % 2, m + 1, m)]) * 2.0 ** -133
+    assert np.array_equal(V.array(res), want)
