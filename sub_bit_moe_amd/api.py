@@ -766,6 +766,8 @@ def _rows(t, what: str, dtype, at: int, shape):
 
 def _norm(x, weight, residual, gates, eps, repeat, out, residual_out, dtype, stream, block, scales):
     import torch
+    if repeat < 1:
+        raise ValueError(f"repeat must be 1 or more, not {repeat}")
     f32, at, shape, kind, flags = torch.float32, x.get_device(), x.shape, x.dtype, 0
     if len(shape) != 2:
         raise ValueError("x must be [tokens, dim], or [tokens * k, dim] with gates")
@@ -826,8 +828,6 @@ def _norm(x, weight, residual, gates, eps, repeat, out, residual_out, dtype, str
                 po, so = pr, sr
         if po == 0:
             po, so = _rows(residual_out, "residual_out", of, at, held)
-    if repeat < 1:
-        raise ValueError(f"repeat must be 1 or more, not {repeat}")
     rows = T * repeat
     if block is None:
         kind = dtype
