@@ -766,6 +766,8 @@ def _rows(t, what: str, dtype, at: int, shape):
 
 def _norm(x, weight, residual, gates, eps, repeat, out, residual_out, dtype, stream, block, scales):
     import torch
+    if x is None:
+        raise ValueError("x must be given")
     if repeat < 1:
         raise ValueError(f"repeat must be 1 or more, not {repeat}")
     f32, at, shape, kind, flags = torch.float32, x.get_device(), x.shape, x.dtype, 0
@@ -899,6 +901,10 @@ def moe_route(logits, k: int, bias=None, sigmoid: bool = False, n_groups: int = 
     bias [E] for the choice, out of the top_groups best of n_groups groups.
     requests (a plan's, int32 [T]): negative ones get id -1, gate 0."""
     import torch
+    if logits is None:
+        raise ValueError("logits must be given")
+    if k < 1:
+        raise ValueError(f"k must be 1 or more, not {k}")
     i32, f32, at = torch.int32, torch.float32, logits.get_device()
     p, stride, flags = _logits(logits, at)
     T, E = logits.shape
@@ -952,6 +958,8 @@ def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=Non
     applied.  Returns tokens int32 [R], or (tokens, logprobs fp32 [R]) with
     return_logprobs or a logprobs buffer; -1 for a row that has no distribution."""
     import torch
+    if logits is None:
+        raise ValueError("logits must be given")
     i32, f32, at = torch.int32, torch.float32, logits.get_device()
     p, stride, flags = _logits(logits, at)
     R, V = logits.shape
