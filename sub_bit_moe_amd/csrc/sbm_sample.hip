@@ -739,14 +739,19 @@ __global__ __launch_bounds__(kSThreads) void sample_draw_kernel(SampleArgs a) {
   draw<T>(f, a, r, range, s);
 }
 
-// Workgroups of a row: one where its tiles stay in their registers, or where there are rows enough to fill the card (1 x 131072: 25 us
-// by eight workgroups, 61 by one; 32 x 131072: 32 and 81; at 1 x 40000, just above what registers hold, 26 and 24).  One workgroup for
-// each of the card's 256 CUs (64 x 131072: 128 workgroups 54 us, 256 39, 512 42; 200 x 50021 with up to 512, which is two a row and three
-// launches instead of one, 36 and 22).
+// Workgroups of a row: one below 48 tiles or where there are rows enough to fill the card, else one for each 16 tiles, as far as the card's
+// 256 CUs go.  Us by the rule's several workgroups and by one (bf16; no filter; a top_p; users' different wishes):
+//    1 x 40000    15 and 12, 23 and 19, 23 and 18        64 x 40000    16 and 13, 33 and 30, 34 and 31
+//    1 x 49152    13 and 14, 22 and 22, 21 and 21        64 x 49152    14 and 14, 32 and 36, 31 and 36
+//    1 x 131072   13 and 29, 22 and 45, 22 and 42        64 x 131072   18 and 30, 41 and 75, 39 and 73
+// A small top_k in every row leaves little to share: up to 98304 tokens one is faster (65536: 16 instead of 21), which the host does not
+// see.  64 x 131072 with 128 workgroups in all takes 54 us, with 256 39, with 512 42; 200 x 50021 with up to 512, which is two a row and
+// three launches instead of one, 36 instead of 22.
 constexpr int kFull = 256;
+constexpr int kLeastShared = 3 * kSWaves;
 int parts_of(int32_t n_rows, int32_t vocab) {
   const int tiles = (vocab + kTile - 1) / kTile;
-  if (tiles <= kHeld * kSWaves) return 1;
+  if (tiles < kLeastShared) return 1;
   return std::max(1, std::min({(int)kMostParts, kFull / std::max(n_rows, 1), tiles / kSWaves}));
 }
 

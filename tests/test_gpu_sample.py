@@ -247,3 +247,12 @@ def test_filters_that_end_near_the_types_lowest(dev, vocab):
                     dict(top_k=max(vocab // 2, 1)), dict(top_k=max(vocab // 3, 1), top_p=0.7, min_p=0.75)):
             _check(dev, l, u, temperature=t, **how)
             _check(dev, R.held(l, "bf16"), u, "bf16", temperature=t, **how)
+
+
+@pytest.mark.parametrize("vocab", [32768, 32769, 47104, 48128, 48129, 49151, 49152, 49153, 65536])
+def test_rows_of_one_and_of_several_workgroups(dev, vocab):
+    """Around the lengths from which a row no longer stays in registers, and from which workgroups share it."""
+    rng = np.random.default_rng(vocab)
+    for rows in (1, 5, 130):
+        l = R.logits_case(rng, rows, vocab, "bf16")
+        _check(dev, l, rng.random(rows), "bf16", **_mixed(rng, rows))
