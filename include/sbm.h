@@ -546,7 +546,8 @@ int sbm_attention_kv4(const sbm_heads* q, const uint8_t* cache, int32_t n_blocks
  *     no |y| passes 448 * 2^(s - 127) (at 254 none can: |y| <= sqrt(dim) |weight|)
  * A block with a NaN or an infinity has scale NaN (byte 255) and zero codes.  The
  * mean of squares is summed in 64 bits; 16-bit results are computed in 32 bits, 8-bit
- * ones in 64.
+ * ones in 64 (a y that is the middle between two codes but for some 2^-51 of it may go
+ * to either).
  * No output overlaps an input or another output, but for residual_out = residual (with its stride)
  * and, with k = repeat = 1, out = x (of the same type and stride). */
 typedef struct {
@@ -573,14 +574,16 @@ typedef struct {
 int sbm_add_rms_norm(const sbm_norm_args* args, void* stream);
 
 /* Routing: each token's k experts and their gates, from the router's logits l.
- *   s = softmax(l), or 1 / (1 + e^-l) with SBM_F_SIGMOID
+ *   s = softmax(l), or 1 / (1 + e^-l) with SBM_F_SIGMOID, as 64 bits hold them (0 below)
  *   c = s + bias in 64 bits (the order of l itself where bias is NULL)
  * With n_groups > 1 the experts are that many runs of n_experts / n_groups; a
  * group's value is the sum of its group_best (1 or 2) largest c (of s without a
  * bias), and only experts of the top_groups groups of largest value are chosen
  * from.  ids get the k of largest c, falling; of equal values the lower expert or
  * group comes first.  gates get scale * s of those, divided by the sum of the
- * token's k scores first with SBM_F_RENORM (unless that is 0).
+ * token's k scores first with SBM_F_RENORM (unless that is 0).  Gates are those of 64
+ * bits rounded to fp32, but that a softmax's sum is of fp32 exponentials where it
+ * divides them itself (off by less than 2^-19 of it, mostly by less than 2^-24).
  * An expert with l = -inf (or bias -inf) is never chosen; where fewer than k are
  * left the rest are id -1, gate 0.  A token with requests[t] < 0 gets only
  * those; so does one with a NaN or +inf among its logits (or biased scores), which

@@ -138,9 +138,10 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int64_t t, int d0
 // mean of squares is summed in 64 bits (f64 runs at the rate of unpacked f32 here), so that no row of finite numbers
 // overflows it; what becomes 8 bits is computed in 64 bits throughout (C), so that a code beside the border of two does not
 // depend on the order of a sum.
-// What bounds it: memory for prompts (8191 x 4096 with residual in and out, 268 MB: 50.5 us, 5.3 TB/s; vector units busy for 67 %);
-// for 8 bits with bytes of scales the 64-bit arithmetic, near to memory (4096 x 8192, 236 MB: 58 us, 4.1 TB/s, vector units busy for
-// 81 %); for few tokens one row's latency (3.6 us a token alone, 5.0 us 64 tokens of two experts; 9 us with the host's call).
+// What bounds it: memory for prompts (8191 x 4096 with residual in and out, 268 MB: 50.7 us, 5.3 TB/s; vector units busy for 68 %;
+// 8192 x 4096 of eight fp32 rows each, 1.41 GB: 272 us, 5.2 TB/s); for 8 bits the 64-bit arithmetic, near to memory (4096 x 8192, 236 MB,
+// bytes of scales: 58 us, 4.1 TB/s, vector units busy for 85 %; fp32 scales of 128 elements 58, of a row 60); for few tokens one row's
+// latency (3.5 us a token alone, 5.0 us 64 tokens of two experts; 9 us with the host's call).
 template <typename T, bool kXF, bool kRF, bool k8, int kN, bool kFew>
 __global__ __launch_bounds__(kMostThreads) void norm_kernel(NormArgs a) {
   using C = std::conditional_t<k8, double, float>;

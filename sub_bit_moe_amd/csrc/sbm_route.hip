@@ -113,9 +113,9 @@ __device__ __forceinline__ double score_of(const RouteArgs& a, float l, float mo
   return inverse(1. + exp2_f64(x));
 }
 
-// e^(l - most) in 32 bits, and the sum over a wave's experts: fours in 32 bits, those in 64.  On average an exponent's roundings
-// come to 2^-23 of it, the rest to 6 of 2^-24: 2^-22 to 2^-20 of the sum, mostly far less.  (The exponentials in 64 bits took 40 instead
-// of 26 us for 16384 x 2048, and 71 instead of 34 with a bias.)
+// e^(l - most) in 32 bits, and the sum over a wave's experts: fours in 32 bits, those in 64.  An exponent's roundings come
+// to 2^-23 of it, the rest to 6 of 2^-24: less than 2^-19 of the sum (the weights' average exponent is 8 at most), mostly less than 2^-24.
+// (The exponentials in 64 bits took 40 instead of 26 us for 16384 x 2048, and 71 instead of 34 with a bias.)
 __device__ __forceinline__ float weight_f32(float l, float most) {
   const float d = l - most;
   return exp2_f32(fused(d, kLog2e, d * kLog2eLow));
@@ -277,11 +277,13 @@ struct WaveSpace {
 // are put in order.  Choices with a bias are compared in 32 bits, with what these may be off added to the candidates; where two
 // that follow each other are nearer than that (one token in some hundred to some thousand), the candidates' choices are computed
 // in 64, as the groups' values are where two at the border are.  With more than 64 candidates the whole token is.
-// What bounds it: 16384 x 2048 in fp32 (134 MB) takes 37.5 us on the card, 37 to 43 from call to call (26 us of memory at its copy's
-// rate): a token's choices fill the registers, so that four waves are in a SIMD, their vector units busy for 66 %, and all of them
-// wait for rows at about the same time; with room for five or six the registers spilled (82 and 98 us, when the bias came from
-// memory), the next token's row read ahead takes the room of a wave (67), and by way of LDS it is slower (40).  8192 x 256 in
-// groups: 18.5 us, vector units 82 %.  64 x 2048: 4.6 us, one token's latency.
+// What bounds it: 16384 x 2048 in fp32 (134 MB) takes 33 to 40 us from one allocation to another (26 us of memory at its copy's rate,
+// which it reaches without a bias): a token's choices fill the registers, so that four waves are in a SIMD, their vector units busy for
+// 72 %, and all of them wait for rows at about the same time; with room for five or six the registers spill (39.6 and 57.8 us beside
+// 35.3), the next token's row read ahead takes the room of a wave (67 us, when this took 50), and by way of LDS it was slower (40
+// beside 37).  8192 x 256 in groups: 18.3 us, vector units 83 %.  64 x 2048: 4.9 us, one token's latency.  Where more than 64 choices are
+// the same within what 32 bits tell apart, choose_exactly looks k times at the row: 16384 x 2048 of equal logits 212 us, with a bias
+// 289, in groups 542; 64 x 2048 36, 50 and 80.
 template <typename T, int kN, bool kGroups>
 __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(RouteArgs a) {
   __shared__ WaveSpace<kN, kGroups> s_space[kRWaves];
@@ -290,7 +292,7 @@ __global__ __launch_bounds__(kRThreads, kN > 32 ? 2 : 4) void route_kernel(Route
   constexpr uint32_t kNoneBits = __is_same(T, float) ? 0xFF800000u : __is_same(T, __bf16) ? 0xFF80u : 0xFC00u;
   constexpr int kSize = __is_same(T, float) ? 4 : 2;
   // The bias goes to LDS once (16384 x 2048: 36.7 us, from memory for each token 49), unless groups' choices leave too little room
-  // there for four workgroups in a CU (16384 x 2048 in groups: 109 us, from memory 92).
+  // there for four workgroups in a CU (16384 x 2048 in groups: 109 us and from memory 92, now 85).
   // One that is no number or +inf refuses the tokens that it could be chosen for.
   constexpr bool kHere = !kGroups || kN < 32;
   __shared__ alignas(16) float s_bias[kHere ? kN * 64 : 1];

@@ -539,7 +539,10 @@ __device__ void refuse(const SampleArgs& a, int64_t r) {
   if (a.error) atomicAdd(a.error, 1u);
 }
 
-// The token of a row from its tiles' sums (s.tiles) and the tokens to be ordered (s.list, s.n_list of them).
+// The token of a row from its tiles' sums (s.tiles) and the tokens to be ordered (s.list, s.n_list of them).  Where the list does not
+// hold those (a top_k from some thousand on beside a top_p; more than 6144 logits alike where a filter ends, such as masks of the type's
+// lowest number under a top_k above what is left) one workgroup orders them from the row itself: 64 x 131072 in 0.44 to 0.58 ms, 1.05
+// where all are alike and a top_p ends among them; with -inf for the masks it is 0.023.
 template <typename T>
 __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& range, Shared& s) {
   const int tid = (int)threadIdx.x, wave = tid >> 6, tiles = (a.vocab + kTile - 1) / kTile;
@@ -628,11 +631,12 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
 // the filter ends; the tokens above stay, those of the bin are put in order in LDS, and each tile's weights are summed on the way.  The
 // draw looks at the tiles' sums and then at one tile.  So a row is read three times: largest, bins, sums (once, as long as it stays in
 // registers).
-// What bounds it: 1 x 32000 in fp16 takes 11.5 us of one workgroup's steps after one another; 64 x 131072 in bf16 three launches of
-// 4.2, 14.4 and 20.5 us, of which the vector units are busy for 44, 46 and 35 % and the rest is the launches' ends and the last workgroup
-// of a row, which puts the list in order.  256 x 150001 in fp32 takes 110 us, the time of the row of which most stays: 22 for the
-// largest (memory, 7 TB/s), 34 for the bins, 20 to 45 for the sums (18 instructions of 64 bits a weight), 8 for the rest; 200 x 50021
-// without filters 20 us, a pass over memory and one of weights.
+// What bounds it: 1 x 32000 in fp16 takes 11.3 us of one workgroup's steps after one another; 64 x 131072 in bf16 three launches of
+// 4.1, 14.2 and 21 us, of which the vector units are busy for 44, 47 and 36 % and the rest is the launches' ends and the last workgroup
+// of a row, which puts the list in order.  256 x 150001 in fp32 takes 105 us, the time of the row of which most stays: 22 for the
+// largest (memory, 7 TB/s), 34 for the bins, 41 for the sums (18 instructions of 64 bits a weight; 12 where few stay), 7 for the rest;
+// 200 x 50021 without filters 20 us, 5 of a pass over memory and 10 of one of weights.  The largest alone (temperature 0): 1 x 32000 4.8 us, 64 x 131072 11.4,
+// 256 x 150001 43.
 
 // A workgroup has a row.
 template <typename T, int kHold>
