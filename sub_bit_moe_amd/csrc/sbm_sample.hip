@@ -635,8 +635,8 @@ __device__ void draw(const Row& f, const SampleArgs& a, int64_t r, const Range& 
 // 4.1, 14.2 and 21 us, of which the vector units are busy for 44, 47 and 36 % and the rest is the launches' ends and the last workgroup
 // of a row, which puts the list in order.  256 x 150001 in fp32 takes 105 us, the time of the row of which most stays: 22 for the
 // largest (memory, 7 TB/s), 34 for the bins, 41 for the sums (18 instructions of 64 bits a weight; 12 where few stay), 7 for the rest;
-// 200 x 50021 without filters 20 us, 5 of a pass over memory and 10 of one of weights.  The largest alone (temperature 0): 1 x 32000 4.8 us, 64 x 131072 11.4,
-// 256 x 150001 43.
+// 200 x 50021 without filters 20 us, 5 of a pass over memory and 10 of one of weights.  The largest alone (temperature 0): 1 x 32000
+// 4.8 us, 64 x 131072 11.4, 256 x 150001 43.
 
 // A workgroup has a row.
 template <typename T, int kHold>
